@@ -49,6 +49,7 @@ extern "C" {
 #define MAC_DEV_WAIT_TIMEOUT 0x4   /* a bounded wait on a copy gave up: item skipped */
 #define MAC_DEV_NONFINITE_Q 0x8    /* non-finite query: treated as a miss */
 #define MAC_DEV_BAD_COPY 0x10      /* a copy outside its tile was refused (internal check) */
+#define MAC_DEV_NO_ROOM 0x20       /* free pages or token rows ran out: request not admitted */
 
 /* ---- configuration ------------------------------------------------------ */
 enum { MAC_BF16 = 0, MAC_F32 = 1 };
@@ -93,6 +94,20 @@ typedef struct {
   int32_t max_pages; /* paged only */
   int32_t n_pages;   /* paged only: physical pages (bounds check) */
 } mac_kv;
+
+/* Where the requests' tokens live, for mac_build_tables.  Paged: the table
+ * and page count of the cache (as in mac_kv) and a stack of free page ids,
+ * entries [0, *n_free_in) of free_pages, the last one on top.  Contiguous:
+ * capacity only. */
+typedef struct {
+  int32_t *page_table;      /* paged: [B][max_pages], extended in place */
+  int32_t *free_pages;      /* paged: [n_pages] */
+  const int32_t *n_free_in; /* paged: one int32, entries of the stack before the call */
+  int32_t *n_free_out;      /* paged: one int32, entries after it (may be n_free_in) */
+  int64_t capacity;         /* contiguous only: tokens per (b, kv-head) block */
+  int32_t max_pages;        /* paged only */
+  int32_t n_pages;          /* paged only: physical pages */
+} mac_pages;
 
 /* Byte offsets of the parts of a ring workspace (for inspection/snapshots). */
 typedef struct {
@@ -204,6 +219,93 @@ int mac_full_attention(const mac_config *cfg, void *scratch_ws, const void *q_pr
  *     the next call and is not readable through mac_last_status. */
 int mac_full_attention_noalloc(const mac_config *cfg, const void *q_pre, const int32_t *seq_len,
                                const mac_kv *kv, float *out, float *lse, void *stream);
+
+/* ---- batches of new tokens ----------------------------------------------
+ * A step that brings new tokens into the cache (prompts, chunks of prompts,
+ * or one token per request ahead of a decode step) is three calls on one
+ * stream: mac_build_tables lays the tokens out, mac_write_kv rotates and
+ * stores them, mac_chunk_attention attends them.  ([MAC] "Production
+ * version" keeps prefill on the exact path and the cache in pages; the
+ * pages describe neither call, so the interfaces are this library's own.)
+ *
+ * The batch is n_tokens packed rows, in request order: request b's new
+ * tokens are rows q_start[b] .. q_start[b+1] - 1, and rows from q_start[B]
+ * on belong to nobody (a captured graph keeps n_tokens fixed while the
+ * device arrays change).  chunk_ws: a workspace of
+ * mac_chunk_workspace_size bytes, zero-filled before its first use, for one
+ * stream at a time (two graphs that may run at once need one each); its
+ * device status word is read by mac_last_status(cfg, chunk_ws, ..). */
+
+/* Bytes of chunk_ws for batches of up to n_tokens rows.  Does not depend on
+ * the context length. */
+int mac_chunk_workspace_size(const mac_config *cfg, int32_t n_tokens, size_t *chunk_bytes);
+
+/* Page tables, slots and positions of a batch, from its lengths alone, on
+ * the device.  Request b holds len_in[b] tokens and brings new_len[b] >= 0.
+ *   reset_flags (device int32 [B] or NULL): a request whose flag is set
+ *     first gives its ceil(len_in/16) pages back and starts at length 0: in
+ *     order of request and page they go on top of the stack.  The flags
+ *     are not cleared (mac_reset_requests on the same flags, after this
+ *     call, empties the request's rings and clears them).
+ *   Pages: the k-th new page, in order of request and page, is the stack's
+ *     k-th entry from the top.  Entries above the count stay as they are.
+ *   A request is admitted whole or not at all: while the pages and the rows
+ *     asked for by it and all requests before it fit (one that asks for no
+ *     page needs only the rows).  One that is not admitted keeps its length
+ *     and pages, gets no row, and sets MAC_DEV_NO_ROOM.  A negative length,
+ *     or one that would pass max_context, max_pages * 16 or capacity, is
+ *     not admitted and sets MAC_DEV_BAD_SEQ_LEN (with a reset flag and
+ *     len_in itself out of range, no page is given back and the length
+ *     stays).  A free or held page id outside [0, n_pages) sets
+ *     MAC_DEV_BAD_PAGE; its tokens get slot -1, a new table entry is -1.
+ * Outputs: len_out [B] (may be len_in); q_start int32 [B+1]; pos int32
+ * [n_tokens], 1-based; slot int64 [n_tokens]: page * 16 + row (paged) or
+ * b * capacity + pos - 1 (contiguous); rows that belong to nobody get pos 0
+ * and slot -1.  n_tokens >= 1.  One launch. */
+int mac_build_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pages,
+                     const int32_t *reset_flags, const int32_t *len_in, const int32_t *new_len,
+                     int32_t n_tokens, int32_t *len_out, int32_t *q_start, int32_t *pos,
+                     int64_t *slot, void *stream);
+
+/* Rotate and store the batch's rows: q_out[t] = R(pos[t]) q[t], and the K/V
+ * of slot[t] <- (R(pos[t]) k[t], v[t]), with cfg's rotation ([MAC] "Match
+ * (1)"; keys are kept rotated, [ACSP] "Why only K/V are cached"); angles
+ * are exact to fp32, one rounding to dtype.  q, k, v: dtype rows of Hq, Hkv
+ * and Hkv heads of d, row t at element t * {q,k,v}_stride (multiples of 16
+ * bytes; a fused projection's rows have stride (Hq + 2 Hkv) d).  q and
+ * q_out NULL: keys and values only (a decode step takes q unrotated).
+ * q_out: [n_tokens][Hq][d], may be q itself if q_stride is Hq * d.  The
+ * caches kv->k and kv->v are written (kv->page_table is not read).  A row
+ * with a negative slot is skipped, its q_out row left as it was; one with
+ * a slot outside the cache too, setting MAC_DEV_BAD_PAGE, and one with
+ * pos < 1, setting MAC_DEV_BAD_SEQ_LEN.  Of two rows with the same slot the
+ * cache gets an unspecified mixture: mac_build_tables makes none. */
+int mac_write_kv(const mac_config *cfg, void *chunk_ws, const void *q, int64_t q_stride,
+                 const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                 const int32_t *pos, const int64_t *slot, int32_t n_tokens, const mac_kv *kv,
+                 void *q_out, void *stream);
+
+/* Exact causal attention of the batch's rows over the cache: row t of
+ * request b, the i-th of its n = q_start[b+1] - q_start[b] new tokens, is
+ * position p = seq_len[b] - n + i (i from 1) and attends [1, p]
+ * ([ACSP] MHA with repeat_kv; the miss path of [MAC] for many queries).
+ * q: [n_tokens][Hq][d] of dtype, already rotated (mac_write_kv's q_out);
+ * seq_len[b] counts the new tokens, whose K/V are in the cache.  out:
+ * [n_tokens][Hq][d] of dtype; lse: f32 [n_tokens][Hq] natural-log softmax
+ * denominators, or NULL.  Requests with n = 0 are passed over; rows that
+ * belong to nobody keep what out and lse held.  Tokens on a page id outside
+ * [0, n_pages) are left out (MAC_DEV_BAD_PAGE); a row that so has nothing
+ * to attend gets out 0 and lse -inf, and so does every row of a request
+ * whose seq_len is below n or beyond the cache (MAC_DEV_BAD_SEQ_LEN);
+ * a request whose rows q_start puts outside [0, n_tokens] is passed over
+ * (MAC_DEV_BAD_SEQ_LEN).  Cache rows beyond seq_len may hold anything.  K
+ * and V of positions up to seq_len must be finite where a row of the same
+ * call does not attend them yet: they meet its zero weights.  dtype bf16:
+ * products of bf16, sums and statistics in fp32, the probabilities rounded
+ * to bf16 before they meet V. */
+int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
+                        const int32_t *q_start, const int32_t *seq_len, int32_t n_tokens,
+                        const mac_kv *kv, void *out, float *lse, void *stream);
 
 /* Make stream_main wait for the last append enqueued on ring_ws (no-op if
  * none is pending).  Needed before ending a stream capture that used a

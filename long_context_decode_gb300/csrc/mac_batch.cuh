@@ -1,0 +1,68 @@
+// mac_batch.cuh -- parameter blocks and launchers of the calls on a batch of
+// new tokens: page tables and slots, the cache writer, chunk attention.
+#pragma once
+
+#include "mac_common.cuh"
+
+namespace mac {
+
+constexpr int kPage = 16;         // tokens per page of a paged cache
+
+struct TablesParams {
+  int B, T;
+  int paged;
+  int64_t limit;                  // longest length a request may reach
+  int64_t capacity;               // contiguous: slots per request
+  int max_pages, n_pages;
+  int32_t *table, *free_pages;
+  const int32_t *n_free_in;
+  int32_t *n_free_out;
+  const int32_t *flags, *len_in, *new_len;
+  int32_t *len_out, *q_start, *pos;
+  int64_t *slot;
+  uint32_t *status;
+};
+
+struct WriteParams {
+  int T, Hq, Hkv, rope_mode, paged;
+  int64_t capacity;               // contiguous: slots per request
+  int64_t n_slots;                // slots of the whole cache
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // elements
+  const int32_t *pos;
+  const int64_t *slot;
+  void *cache_k, *cache_v, *q_out;
+  uint32_t *status;
+  unsigned long long rope_f[kHeadDim / 2];
+};
+
+// Chunk attention.  A unit is (request b, KV head g, tile i of the request's
+// new tokens): ROWS packed rows, token-major, the G heads of a token next to
+// one another, so that the group loads each K/V tile once.
+struct ChunkParams {
+  int B, Hq, Hkv, G, T;
+  float q_scale;                  // log2(e)/sqrt(d)
+  int64_t max_len;
+  KvView kv;
+  const void *q;
+  const int32_t *q_start, *seq_len;
+  void *out;
+  float *lse;                     // or null
+  uint32_t *status;
+  uint32_t *count;                // [kChunkGrid] finished pieces of the split unit that starts in a CTA
+  float *part;                    // [2 * grid][part_rows][kPartStride]
+  int part_rows;
+  long long wait_limit;
+};
+
+constexpr int kChunkGrid = 512;   // most CTAs of a launch
+constexpr int kChunkRowsBf16 = 256, kChunkRowsF32 = 64;  // rows per unit
+constexpr int kMaxTokens = 1 << 24;
+
+cudaError_t launch_chunk_f32(const ChunkParams &p, int sms, cudaStream_t s);
+cudaError_t launch_chunk_bf16(const ChunkParams &p, int sms, cudaStream_t s);
+
+cudaError_t launch_tables(const TablesParams &p, cudaStream_t s);
+cudaError_t launch_write(const WriteParams &p, int dtype, cudaStream_t s);
+
+}  // namespace mac

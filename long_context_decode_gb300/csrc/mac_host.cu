@@ -7,6 +7,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "mac_batch.cuh"
 #include "mac_common.cuh"
 
 using namespace mac;
@@ -165,6 +166,12 @@ int step_grid(const mac_config *c) {
 
 cudaError_t launch_step(StepParams p, const mac_config *c, cudaStream_t s);
 
+void rope_table(const mac_config *c, unsigned long long *f) {
+  for (int j = 0; j < kHeadDim / 2; ++j)
+    f[j] = (unsigned long long)ldexp(
+        pow(c->rope_base, -2.0 * (double)j / (double)c->head_dim) / 6.283185307179586, 64);
+}
+
 // Common part of every step launch: shapes, constants, K/V, scratch.
 StepParams step_params(const mac_config *c, const ScratchLayout &S, uint8_t *scratch,
                        const mac_kv *kv, int mode) {
@@ -185,9 +192,7 @@ StepParams step_params(const mac_config *c, const ScratchLayout &S, uint8_t *scr
   a.kv = kv_view(c, kv);
   a.max_len = max_len(c, a.kv);
   a.q_stride = c->head_dim;
-  for (int j = 0; j < kHeadDim / 2; ++j)
-    a.rope_f[j] = (unsigned long long)ldexp(
-        pow(c->rope_base, -2.0 * (double)j / (double)c->head_dim) / 6.283185307179586, 64);
+  rope_table(c, a.rope_f);
   a.ctl = (uint32_t *)(scratch + S.ctl);
   a.best = (unsigned long long *)(scratch + S.best);
   a.unit_done = (uint32_t *)(scratch + S.unit_done);
@@ -225,6 +230,35 @@ AppendParams append_params(const mac_config *c, const mac_ring_layout &R, uint8_
   q.ring_lse = (float *)(ring + R.lse);
   return q;
 }
+
+// Chunk workspace: the status word first (where mac_last_status reads a
+// scratch's), the counts of the split units' pieces, then the pieces.  The
+// counts start at zero and a clean launch leaves them so.
+struct ChunkLayout {
+  size_t ctl, count, part, total;
+  int part_rows;
+};
+
+ChunkLayout chunk_layout(const mac_config *c, int32_t n_tokens) {
+  const bool f32 = c->dtype == MAC_F32;
+  const int64_t rows = (int64_t)n_tokens * (c->n_q_heads / c->n_kv_heads);
+  const int unit = f32 ? kChunkRowsF32 : kChunkRowsBf16;
+  ChunkLayout L;
+  L.part_rows = (int)(rows < unit ? rows : unit);
+  size_t off = 0;
+  L.ctl = off;    off = align_up(off + 64 * 4, 256);
+  L.count = off;  off = align_up(off + (size_t)kChunkGrid * 4, 256);
+  L.part = off;   off = align_up(off + 2 * (size_t)kChunkGrid * L.part_rows * kPartStride * 4, 256);
+  L.total = off;
+  return L;
+}
+
+int check_tokens(int32_t n_tokens) {
+  if (n_tokens < 1) return MAC_ERR_INVALID_ARG;
+  return n_tokens > kMaxTokens ? MAC_ERR_UNSUPPORTED : MAC_OK;
+}
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // ---- per-ring events: the append of step n on stream_aux must finish before
 // step n+1 on the same ring reads or rewrites the rings ([MAC] K3 runs on an
@@ -547,6 +581,141 @@ int mac_full_attention_noalloc(const mac_config *cfg, const void *q_pre, const i
   if (cudaMemsetAsync(scratch, 0, scratch_layout(cfg).parts, (cudaStream_t)stream) != cudaSuccess)
     return MAC_ERR_CUDA;
   return mac_full_attention(cfg, scratch, q_pre, seq_len, kv, out, lse, stream);
+}
+
+int mac_chunk_workspace_size(const mac_config *cfg, int32_t n_tokens, size_t *chunk_bytes) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_tokens(n_tokens)) != MAC_OK) return v;
+  if (!chunk_bytes) return MAC_ERR_INVALID_ARG;
+  *chunk_bytes = chunk_layout(cfg, n_tokens).total;
+  return MAC_OK;
+}
+
+int mac_build_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pages,
+                     const int32_t *reset_flags, const int32_t *len_in, const int32_t *new_len,
+                     int32_t n_tokens, int32_t *len_out, int32_t *q_start, int32_t *pos,
+                     int64_t *slot, void *stream) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_tokens(n_tokens)) != MAC_OK) return v;
+  if (!chunk_ws || !pages || !len_in || !new_len || !len_out || !q_start || !pos || !slot || !aligned16(chunk_ws) ||
+      !aligned(reset_flags, 4) || !aligned(len_in, 4) || !aligned(new_len, 4) || !aligned(len_out, 4) ||
+      !aligned(q_start, 4) || !aligned(pos, 4) || !aligned(slot, 8))
+    return MAC_ERR_INVALID_ARG;
+  TablesParams p;
+  memset(&p, 0, sizeof p);
+  p.paged = cfg->page_size != 0;
+  if (p.paged) {
+    if (!pages->page_table || !pages->free_pages || !pages->n_free_in || !pages->n_free_out || pages->max_pages < 1 ||
+        pages->n_pages < 1 || !aligned(pages->page_table, 4) || !aligned(pages->free_pages, 4) ||
+        !aligned(pages->n_free_in, 4) || !aligned(pages->n_free_out, 4))
+      return MAC_ERR_INVALID_ARG;
+  } else if (pages->capacity < 1) {
+    return MAC_ERR_INVALID_ARG;
+  }
+  p.B = cfg->batch;
+  p.T = n_tokens;
+  p.capacity = p.paged ? (int64_t)pages->max_pages * cfg->page_size : pages->capacity;
+  p.limit = p.capacity < cfg->max_context ? p.capacity : cfg->max_context;
+  p.max_pages = pages->max_pages;
+  p.n_pages = pages->n_pages;
+  p.table = pages->page_table;
+  p.free_pages = pages->free_pages;
+  p.n_free_in = pages->n_free_in;
+  p.n_free_out = pages->n_free_out;
+  p.flags = reset_flags;
+  p.len_in = len_in;
+  p.new_len = new_len;
+  p.len_out = len_out;
+  p.q_start = q_start;
+  p.pos = pos;
+  p.slot = slot;
+  p.status = (uint32_t *)chunk_ws;
+  note_launch((cudaStream_t)stream, nullptr, nullptr);
+  return launch_tables(p, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+}
+
+int mac_write_kv(const mac_config *cfg, void *chunk_ws, const void *q, int64_t q_stride,
+                 const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                 const int32_t *pos, const int64_t *slot, int32_t n_tokens, const mac_kv *kv,
+                 void *q_out, void *stream) {
+  int rc = validate(cfg);
+  if (rc != MAC_OK) return rc;
+  if ((rc = check_tokens(n_tokens)) != MAC_OK) return rc;
+  if (!chunk_ws || !k || !v || !pos || !slot || !kv || !kv->k || !kv->v || (q == nullptr) != (q_out == nullptr) ||
+      !aligned16(chunk_ws) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      !aligned16(kv->k) || !aligned16(kv->v) || !aligned(pos, 4) || !aligned(slot, 8))
+    return MAC_ERR_INVALID_ARG;
+  const int64_t es = elem_size(cfg), dq = (int64_t)cfg->n_q_heads * cfg->head_dim, dk = (int64_t)cfg->n_kv_heads * cfg->head_dim;
+  if (k_stride < dk || v_stride < dk || k_stride * es % 16 || v_stride * es % 16 ||
+      (q && (q_stride < dq || q_stride * es % 16 || (q == q_out && q_stride != dq))))
+    return MAC_ERR_INVALID_ARG;
+  if (cfg->page_size ? kv->n_pages < 1 : kv->capacity < 1) return MAC_ERR_INVALID_ARG;
+  WriteParams p;
+  memset(&p, 0, sizeof p);
+  p.T = n_tokens;
+  p.Hq = cfg->n_q_heads;
+  p.Hkv = cfg->n_kv_heads;
+  p.rope_mode = cfg->rope_mode;
+  p.paged = cfg->page_size != 0;
+  p.capacity = kv->capacity;
+  p.n_slots = p.paged ? (int64_t)kv->n_pages * cfg->page_size : (int64_t)cfg->batch * kv->capacity;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.pos = pos;
+  p.slot = slot;
+  p.cache_k = const_cast<void *>(kv->k);
+  p.cache_v = const_cast<void *>(kv->v);
+  p.q_out = q_out;
+  p.status = (uint32_t *)chunk_ws;
+  rope_table(cfg, p.rope_f);
+  note_launch((cudaStream_t)stream, nullptr, nullptr);  // the next step reads this K/V: it waits
+  return launch_write(p, cfg->dtype, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+}
+
+int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
+                        const int32_t *q_start, const int32_t *seq_len, int32_t n_tokens,
+                        const mac_kv *kv, void *out, float *lse, void *stream) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_tokens(n_tokens)) != MAC_OK) return v;
+  if (!chunk_ws || !q || !q_start || !seq_len || !out || q == out || !aligned16(chunk_ws) || !aligned16(q) ||
+      !aligned16(out) || !aligned(q_start, 4) || !aligned(seq_len, 4) || !aligned(lse, 4))
+    return MAC_ERR_INVALID_ARG;
+  if ((v = check_kv(cfg, kv)) != MAC_OK) return v;
+  const ChunkLayout L = chunk_layout(cfg, n_tokens);
+  uint8_t *ws = (uint8_t *)chunk_ws;
+  ChunkParams p;
+  memset(&p, 0, sizeof p);
+  p.B = cfg->batch;
+  p.Hq = cfg->n_q_heads;
+  p.Hkv = cfg->n_kv_heads;
+  p.G = cfg->n_q_heads / cfg->n_kv_heads;
+  p.T = n_tokens;
+  p.q_scale = q_scale(cfg);
+  p.kv = kv_view(cfg, kv);
+  p.max_len = max_len(cfg, p.kv);
+  p.q = q;
+  p.q_start = q_start;
+  p.seq_len = seq_len;
+  p.out = out;
+  p.lse = lse;
+  p.status = (uint32_t *)(ws + L.ctl);
+  p.count = (uint32_t *)(ws + L.count);
+  p.part = (float *)(ws + L.part);
+  p.part_rows = L.part_rows;
+  p.wait_limit = kWaitLimit;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int sms = num_sms();
+  if (sms < 1) return MAC_ERR_CUDA;
+  note_launch(s, nullptr, nullptr);
+  const cudaError_t e = cfg->dtype == MAC_F32 ? launch_chunk_f32(p, sms, s) : launch_chunk_bf16(p, sms, s);
+  return e == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
 }
 
 int mac_join_aux(void *ring_ws, void *stream_main) {

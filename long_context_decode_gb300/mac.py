@@ -14,6 +14,7 @@ from . import build as _build
 
 MAC_OK, MAC_ERR_INVALID_ARG, MAC_ERR_UNSUPPORTED, MAC_ERR_CUDA = 0, -1, -2, -3
 MAC_DEV_BAD_SEQ_LEN, MAC_DEV_BAD_PAGE, MAC_DEV_WAIT_TIMEOUT, MAC_DEV_NONFINITE_Q, MAC_DEV_BAD_COPY = 1, 2, 4, 8, 16
+MAC_DEV_NO_ROOM = 32
 MAC_TRACE_POINTS = 32
 MAC_BF16, MAC_F32 = 0, 1
 MAC_THR_ONE_MINUS_TAU, MAC_THR_TAU = 0, 1
@@ -23,7 +24,8 @@ MAC_ROPE_HALF, MAC_ROPE_INTERLEAVED, MAC_ROPE_NONE = 0, 1, 2
 EXPORTS = ("mac_workspace_size", "mac_ring_layout_of", "mac_init_rings", "mac_decode_step",
            "mac_full_attention", "mac_full_attention_noalloc", "mac_join_aux", "mac_release_ring",
            "mac_last_status", "mac_set_phase_events", "mac_set_trace", "mac_status_string",
-           "mac_threshold_sq", "mac_reset_requests", "mac_test_wait_budget")
+           "mac_threshold_sq", "mac_reset_requests", "mac_test_wait_budget",
+           "mac_chunk_workspace_size", "mac_build_tables", "mac_write_kv", "mac_chunk_attention")
 MAC_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -42,6 +44,14 @@ class mac_kv(ctypes.Structure):
     _fields_ = [
         ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
         ("capacity", ctypes.c_int64), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+    ]
+
+
+class mac_pages(ctypes.Structure):
+    _fields_ = [
+        ("page_table", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("n_free_in", ctypes.c_void_p),
+        ("n_free_out", ctypes.c_void_p), ("capacity", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
     ]
 
 
@@ -85,6 +95,10 @@ def load() -> ctypes.CDLL:
     L.mac_set_trace.argtypes = [vp]
     L.mac_reset_requests.argtypes = [P(mac_config), vp, vp, vp]
     L.mac_test_wait_budget.argtypes = [i64, i32]
+    L.mac_chunk_workspace_size.argtypes = [P(mac_config), i32, P(ctypes.c_size_t)]
+    L.mac_build_tables.argtypes = [P(mac_config), vp, P(mac_pages), vp, vp, vp, i32, vp, vp, vp, vp, vp]
+    L.mac_write_kv.argtypes = [P(mac_config), vp, vp, i64, vp, i64, vp, i64, vp, vp, i32, P(mac_kv), vp, vp]
+    L.mac_chunk_attention.argtypes = [P(mac_config), vp, vp, vp, vp, i32, P(mac_kv), vp, vp, vp]
     L.mac_status_string.argtypes = [ctypes.c_int]
     L.mac_status_string.restype = ctypes.c_char_p
     L.mac_threshold_sq.argtypes = [P(mac_config)]
@@ -208,6 +222,51 @@ def mac_test_wait_budget(cycles: int, withhold_use: int = -1):
     _check(load().mac_test_wait_budget(int(cycles), int(withhold_use)), "mac_test_wait_budget")
 
 
+def mac_chunk_workspace_size(cfg: mac_config, n_tokens: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mac_chunk_workspace_size(ctypes.byref(cfg), int(n_tokens), ctypes.byref(n)),
+           "mac_chunk_workspace_size")
+    return n.value
+
+
+def mac_build_tables(cfg, chunk_ws, pages: mac_pages, reset_flags, len_in, new_len, n_tokens, len_out, q_start, pos,
+                     slot, stream=None):
+    """Pages, packed rows, positions and slots of a batch of new tokens,
+    from device lengths (see include/mac.h)."""
+    _check(load().mac_build_tables(ctypes.byref(cfg), _ptr(chunk_ws), ctypes.byref(pages) if pages is not None else None,
+                                   _ptr(reset_flags), _ptr(len_in), _ptr(new_len), int(n_tokens), _ptr(len_out),
+                                   _ptr(q_start), _ptr(pos), _ptr(slot), _stream(stream)), "mac_build_tables")
+
+
+def _row_stride(t, heads, head_dim) -> int:
+    """Elements between rows of [T, heads, d] whose rows are whole (a raw
+    pointer's rows lie end to end)."""
+    if t is None or isinstance(t, int):
+        return heads * head_dim
+    st = t.stride()
+    if st[1:] != (head_dim, 1) and not (t.shape[1] == 1 and st[2] == 1):
+        raise MacError("mac_write_kv: a row's heads must lie end to end")
+    return st[0]
+
+
+def mac_write_kv(cfg, chunk_ws, q, k, v, pos, slot, n_tokens, kv: mac_kv, q_out, stream=None):
+    """Rotate and store the rows of a batch.  q, k, v: [T, heads, d] tensors,
+    strided views of a fused projection included, or pointers to contiguous
+    rows; q and q_out None for keys and values only."""
+    d = cfg.head_dim
+    _check(load().mac_write_kv(ctypes.byref(cfg), _ptr(chunk_ws), _ptr(q), _row_stride(q, cfg.n_q_heads, d), _ptr(k),
+                               _row_stride(k, cfg.n_kv_heads, d), _ptr(v), _row_stride(v, cfg.n_kv_heads, d), _ptr(pos),
+                               _ptr(slot), int(n_tokens), ctypes.byref(kv) if kv is not None else None, _ptr(q_out),
+                               _stream(stream)), "mac_write_kv")
+
+
+def mac_chunk_attention(cfg, chunk_ws, q, q_start, seq_len, n_tokens, kv: mac_kv, out, lse=None, stream=None):
+    """Exact causal attention of a batch's rotated rows over the cache."""
+    _check(load().mac_chunk_attention(ctypes.byref(cfg), _ptr(chunk_ws), _ptr(q), _ptr(q_start), _ptr(seq_len),
+                                      int(n_tokens), ctypes.byref(kv) if kv is not None else None, _ptr(out), _ptr(lse),
+                                      _stream(stream)), "mac_chunk_attention")
+
+
 def mac_status_string(code: int) -> str:
     return load().mac_status_string(code).decode()
 
@@ -237,6 +296,21 @@ def kv_view(k, v, page_table=None, capacity=0, max_pages=0, n_pages=0) -> mac_kv
         max_pages = max_pages or page_table.shape[1]
         n_pages = n_pages or k.shape[0]
     return mac_kv(_ptr(k), _ptr(v), _ptr(page_table), int(capacity), int(max_pages), int(n_pages))
+
+
+def pages_view(page_table=None, free_pages=None, n_free_in=None, n_free_out=None, capacity=0, max_pages=0,
+               n_pages=0) -> mac_pages:
+    """Page pool descriptor from torch tensors: page table [B, max_pages], free
+    stack [n_pages] and its counts (n_free_out defaults to n_free_in), or
+    just the capacity of a contiguous cache."""
+    if page_table is not None:
+        max_pages = max_pages or page_table.shape[1]
+        n_pages = n_pages or free_pages.shape[0]
+        n_free_out = n_free_in if n_free_out is None else n_free_out
+    view = mac_pages(_ptr(page_table), _ptr(free_pages), _ptr(n_free_in), _ptr(n_free_out), int(capacity),
+                     int(max_pages), int(n_pages))
+    view.tensors = (page_table, free_pages, n_free_in, n_free_out)  # alive as long as the view
+    return view
 
 
 class MacLayer:
