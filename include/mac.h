@@ -326,10 +326,10 @@ int mac_join_aux(void *ring_ws, void *stream_main);
 int mac_reset_requests(const mac_config *cfg, void *ring_ws, int32_t *reset_flags, void *stream);
 
 /* Test hook for the bounded waits (no counterpart on the pages): the next
- * step kernel launched by the calling thread gives every wait (a stage's
+ * step or chunk-attention kernel launched by the calling thread gives every wait (a stage's
  * copy, a flag, the grid barrier, a piece count) `cycles` SM cycles instead
  * of about a second, and, if withhold_use >= 0, never issues the copy of
- * that stage use (per CTA in the span kernel, per warp in the ring kernel),
+ * that stage use (per CTA; per warp in the ring kernel),
  * so the wait for it runs out: the kernel sets MAC_DEV_WAIT_TIMEOUT, stops
  * its work, lets its other copies land and returns.  The launch's outputs
  * are then undefined; its scratch workspace must be cleared (or replaced)

@@ -52,7 +52,8 @@ struct ChunkParams {
   uint32_t *count;                // [kChunkGrid] finished pieces of the split unit that starts in a CTA
   float *part;                    // [2 * grid][part_rows][kPartStride]
   int part_rows;
-  long long wait_limit;
+  long long wait_limit;           // bf16 kernel: cycles a wait may take
+  int withhold;                   // run-out test only: the stage use (>= 0) whose copy is never issued
 };
 
 constexpr int kChunkGrid = 512;   // most CTAs of a launch

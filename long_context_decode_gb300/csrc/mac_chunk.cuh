@@ -23,7 +23,8 @@ __device__ __forceinline__ long long ceil_sum(long long n, int s) {
 }
 
 struct ChunkUnit {
-  int b, g;
+  int b, g, i;         // request, KV head, row tile of the request's new tokens
+  int a, n, row0;      // the request's tokens before the new ones, new tokens, first row
   int tok0, n_tok;     // first row (token) of the unit in the batch, tokens in it
   int pos0;            // tokens attended by its first token (its 1-based position)
   int tiles;           // key tiles its last token attends
@@ -127,8 +128,8 @@ struct ChunkPlan {
       if (prefix[mid] <= x) lo = mid; else hi = mid;
     }
     const int tt = ROWS / p.G;
-    int a, n, row0;
-    request(p, lo, &a, &n, &row0);
+    request(p, lo, &u.a, &u.n, &u.row0);
+    const int a = u.a, n = u.n;
     const long long per = cost(a, n, tt);
     const long long off = x - prefix[lo];
     u.b = lo;
@@ -139,17 +140,37 @@ struct ChunkPlan {
       const int mid = (i0 + i1) >> 1;
       if (tiles_before(a, tt, mid) + (long long)mid * COST0 <= rem) i0 = mid; else i1 = mid;
     }
-    set(u, p, a, n, row0, i0);
+    set(u, p, i0);
     u.at = prefix[lo] + u.g * per + tiles_before(a, tt, i0) + (long long)i0 * COST0 + COST0;
     return u;
   }
 
-  __device__ static void set(ChunkUnit &u, const ChunkParams &p, int a, int n, int row0, int i) {
+  // The unit after u (there is one).
+  __device__ static void advance(ChunkUnit &u, const ChunkParams &p) {
     const int tt = ROWS / p.G;
-    u.tok0 = row0 + i * tt;
-    u.n_tok = min(tt, n - i * tt);
-    u.pos0 = a + i * tt + 1;
-    u.tiles = (int)(((long long)a + i * tt + u.n_tok + KT - 1) / KT);
+    const long long at = u.at + u.tiles + COST0;
+    int i = u.i + 1;
+    if (i * tt >= u.n) {
+      i = 0;
+      if (++u.g == p.Hkv) {
+        u.g = 0;
+        do {
+          ++u.b;
+          request(p, u.b, &u.a, &u.n, &u.row0);
+        } while (u.n == 0);
+      }
+    }
+    set(u, p, i);
+    u.at = at;
+  }
+
+  __device__ static void set(ChunkUnit &u, const ChunkParams &p, int i) {
+    const int tt = ROWS / p.G;
+    u.i = i;
+    u.tok0 = u.row0 + i * tt;
+    u.n_tok = min(tt, u.n - i * tt);
+    u.pos0 = u.a + i * tt + 1;
+    u.tiles = (int)(((long long)u.a + i * tt + u.n_tok + KT - 1) / KT);
   }
 };
 

@@ -1,0 +1,749 @@
+// mac_chunk_bf16.cu -- chunk attention in bf16 on the tensor cores.
+//
+// For a row with rotated query q at position p, over key tiles of 128:
+//   S = Q K^T (fp32);  x_j = S_j log2(e)/sqrt(d), j <= p;
+//   P_j = 2^(x_j - m) with m a running reference of the row's maximum;
+//   l = sum P_j (fp32);  O = sum P_j V_j (P rounded to bf16, sums in fp32);
+//   out = O / l;  lse = m ln 2 + ln l.
+// The reference m moves only when the maximum has grown by more than 8 in
+// base 2 (P stays below 2^8, and bf16 keeps the same relative precision
+// there), so O is rarely rescaled; any m gives the same quotient.
+//
+// One CTA per SM, twelve warps:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1 (a thread owns a row);
+//   warp 8          copies Q, K and V by TMA into swizzled shared memory;
+//   warp 9          issues the products: S into TMEM from shared memory, and
+//                   O += P V with P read back from TMEM;
+//   warp 10         clears V rows past the end of the sequence.
+// A unit has up to 256 packed rows (token-major, the G heads of a token
+// together), two row tiles of 128.  With 128 rows or fewer both softmax
+// groups work on the same rows and take the key tiles in turn.  While one
+// group works on its scores the tensor cores work for the other.
+//
+// TMEM (512 columns): S0, S1, O0, O1, 128 columns each; P overwrites S.
+#include <cuda.h>
+#include <math.h>
+
+#include "mac_chunk.cuh"
+
+namespace mac {
+namespace {
+
+constexpr int kTile = 128;                    // rows of a row tile, keys of a key tile
+constexpr int kCost0 = 2, kMinShare = 4;
+constexpr int kThr = 384;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;  // registers per thread once the roles have split
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThr * 168, "the split comes out of the launch's registers");
+constexpr int kNSt = 5;                       // stages of the K/V ring
+constexpr int kTileBytes = kTile * kHeadDim * 2;
+constexpr float kLazy = 8.f;                  // growth of the maximum (base 2) that moves the reference
+using Plan = ChunkPlan<kChunkRowsBf16, kTile, kCost0>;
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+struct Control {
+  unsigned long long full[kNSt], empty[kNSt];
+  unsigned long long q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, fixed, drain;
+  uint32_t tmem;
+  int abort, last;
+  long long share, total;
+  float2 ml[2][kTile];                        // states of the two groups that share rows
+};
+constexpr int kSmemBytes = (kNSt + 2) * kTileBytes + (int)sizeof(Control);
+static_assert(kSmemBytes <= (int)kMaxSmem, "shared memory of a CTA");
+static_assert(sizeof(Plan) <= kNSt * kTileBytes, "the plan is made where the stages go");
+
+// ---- tcgen05 ---------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// D[128 x 128] (+)= A B, 16 deep; bf16 inputs, fp32 sums.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)add)
+      : "memory");
+}
+
+// Instruction descriptor: fp32 sums (bit 4), bf16 A and B (bits 7, 10), B
+// along N where asked (bit 16), N/8 from bit 17, M/16 from bit 24.
+__host__ __device__ constexpr uint32_t idesc(bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+}
+
+// Shared memory descriptor, 128-byte swizzle: address / 16, leading and
+// stride byte offsets / 16, version 1 (bit 46), swizzle mode 2 (bit 61).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+
+__device__ __forceinline__ void tc_ld32(float *r, uint32_t addr) {
+  uint32_t *u = reinterpret_cast<uint32_t *>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]),
+      "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
+      "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
+      "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::"r"(u[0]),
+      "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- TMA -------------------------------------------------------------------
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// ---- packed fp32 -----------------------------------------------------------
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// ---- the pieces of a CTA, as every role walks them ---------------------------
+struct Piece {
+  ChunkUnit u;
+  int t0, t1;       // its key tiles
+  int pair;         // both groups on row tile 0, key tiles in turn
+  int end[2];       // normal: key tiles of each row tile end here (after t0, or none)
+  int c0, c1;       // CTAs that hold the unit's pieces
+  __device__ int n() const { return t1 - t0; }
+  // key tiles of group w
+  __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : max(0, end[w] - t0); }
+};
+
+struct Walk {
+  long long x, end, share;
+  ChunkUnit u;
+  bool first;
+  // Next piece with a tile; false when the CTA's work is done.
+  __device__ bool next(const ChunkParams &p, Piece &q) {
+    while (x < end) {
+      if (!first) Plan::advance(u, p);
+      first = false;
+      const long long u_end = u.at + u.tiles;
+      q.t0 = (int)max(0LL, x - u.at);
+      q.t1 = (int)min((long long)u.tiles, end - u.at);
+      x = u_end;
+      if (q.t0 >= q.t1) continue;
+      q.u = u;
+      q.pair = u.n_tok * p.G <= kTile;
+      const int tok = kTile / p.G;  // tokens of row tile 0
+      q.end[0] = min(q.t1, (u.pos0 + tok - 1 + kTile - 1) / kTile);
+      q.end[1] = q.t1;
+      q.c0 = (int)(u.at / share);
+      q.c1 = (int)((u_end - 1) / share);
+      return true;
+    }
+    return false;
+  }
+};
+
+// Ring position of the i-th key (value) tile of a piece of n tiles, in the
+// order in which they are copied and used: K0 K1 V0 K2 V1 .. V(n-1).
+__device__ __forceinline__ int k_use(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_use(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
+
+// Waits that every role makes.  After one has run out (or another role's
+// has: ct->abort) all return false at once; the roles then walk through
+// their loops without touching anything, so that their barriers still meet.
+struct Waiter {
+  Control *ct;
+  uint32_t *status;
+  long long limit;
+  bool dead;
+  __device__ bool operator()(unsigned long long *bar, uint32_t parity) {
+    if (dead) return false;
+    if (!mbar_wait_bounded(smem_addr(bar), parity, (volatile int *)&ct->abort, limit)) {
+      dead = true;
+      *(volatile int *)&ct->abort = 1;
+      set_status(status, MAC_DEV_WAIT_TIMEOUT);
+      return false;
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ bool bad_page(const ChunkParams &p, int id) {
+  return id < 0 || id >= p.kv.n_pages;
+}
+
+// ---- copies (warp 8) ---------------------------------------------------------
+template <bool PAGED>
+__device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stages, uint32_t qbuf, Control *ct, Walk walk) {
+  const int lane = threadIdx.x & 31;
+  Waiter wait{ct, p.status, p.wait_limit, false};
+  int use = 0;       // stage uses so far
+  uint32_t nq = 0;   // Q tiles so far
+  Piece q = {};
+  auto tile = [&](const CUtensorMap *m, int t) {
+    const int st = use % kNSt, round = use / kNSt;
+    const bool ok = wait(&ct->empty[st], (round + 1) & 1);  // the first round finds the stages free
+    const uint32_t bar = smem_addr(&ct->full[st]), dst = stages + st * kTileBytes;
+    if (__all_sync(0xffffffffu, ok)) {
+      if (PAGED) {
+        int id = p.kv.n_pages;  // out of range: the copy fills with zeros
+        const int pg = t * (kTile / kPage) + lane;
+        if (lane < kTile / kPage && (int64_t)pg * kPage < q.u.pos0 + q.u.n_tok - 1) {
+          id = p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + pg];
+          if (bad_page(p, id)) id = p.kv.n_pages;
+        }
+        if (lane == 0) mbar_expect_tx(bar, kTileBytes);
+        __syncwarp();
+        if (lane < kTile / kPage && use != p.withhold) {
+          tma_4d(dst + lane * 2048, m, 0, 0, q.u.g, id, bar);
+          tma_4d(dst + kTileBytes / 2 + lane * 2048, m, 64, 0, q.u.g, id, bar);
+        }
+      } else if (lane == 0) {
+        mbar_expect_tx(bar, kTileBytes);
+        if (use != p.withhold) {
+          tma_3d(dst, m, 0, t * kTile, q.u.b * p.Hkv + q.u.g, bar);
+          tma_3d(dst + kTileBytes / 2, m, 64, t * kTile, q.u.b * p.Hkv + q.u.g, bar);
+        }
+      }
+      ++use;
+    }
+    __syncwarp();
+  };
+  while (walk.next(p, q)) {
+    const int n = q.n();
+    tile(&maps.k, q.t0);
+    {
+      const bool ok = wait(&ct->q_empty, (nq + 1) & 1);
+      if (ok && lane == 0) {
+        const uint32_t bar = smem_addr(&ct->q_full);
+        mbar_expect_tx(bar, (q.pair ? 1 : 2) * kTileBytes);
+        for (int w = 0; w < (q.pair ? 1 : 2); ++w)
+          for (int h = 0; h < 2; ++h)
+            tma_3d(qbuf + w * kTileBytes + h * (kTileBytes / 2), &maps.q, 64 * h, q.u.g * p.G, q.u.tok0 + w * (kTile / p.G), bar);
+      }
+      if (ok) ++nq;
+      __syncwarp();
+    }
+    if (n > 1) tile(&maps.k, q.t0 + 1);
+    for (int i = 0; i < n; ++i) {
+      tile(&maps.v, q.t0 + i);
+      if (i + 2 < n) tile(&maps.k, q.t0 + i + 2);
+    }
+  }
+  // After a wait ran out, copies may still be in flight: let them land
+  // before the CTA gives its shared memory up.
+  if (*(volatile int *)&ct->abort) {
+    const int dummy = 0;
+    for (int u = use > kNSt ? use - kNSt : 0; u < use; ++u)
+      mbar_wait_bounded(smem_addr(&ct->full[u % kNSt]), (u / kNSt) & 1, (volatile int *)&dummy, p.wait_limit);
+    if (nq) mbar_wait_bounded(smem_addr(&ct->q_full), (nq - 1) & 1, (volatile int *)&dummy, p.wait_limit);
+  }
+}
+
+// ---- products (warp 9, one thread) ---------------------------------------------
+__device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, Control *ct, Walk walk, uint32_t tmem) {
+  Waiter wait{ct, p.status, p.wait_limit, false};
+  int base = 0;
+  uint32_t nq = 0, np[2] = {0, 0}, nfix = 0;
+  Piece q = {};
+  auto stage = [&](int use) { return stages + (use % kNSt) * kTileBytes; };
+  auto loaded = [&](int use) { return wait(&ct->full[use % kNSt], (use / kNSt) & 1); };
+  auto release = [&](int use) {
+    if (!wait.dead) tc_commit(smem_addr(&ct->empty[use % kNSt]));
+  };
+  auto scores = [&](int w, uint32_t k) {  // S_w = Q K^T, then tell group w
+    if (wait.dead) return;
+    const uint32_t qa = qbuf + (q.pair ? 0 : w) * kTileBytes;
+#pragma unroll
+    for (int s = 0; s < kHeadDim / 16; ++s) {
+      const uint32_t off = (s >> 2) * (kTileBytes / 2) + (s & 3) * 32;
+      tc_mma_ss(tmem + w * kTile, smem_desc(qa + off, 16, 1024), smem_desc(k + off, 16, 1024), idesc(false), s > 0);
+    }
+    tc_commit(smem_addr(&ct->s_full[w]));
+  };
+  auto values = [&](int w, uint32_t v, bool add) {  // O_w (+)= P_w V
+    if (wait.dead) return;
+#pragma unroll
+    for (int s = 0; s < kTile / 16; ++s)
+      tc_mma_ts(tmem + 2 * kTile + w * kTile, tmem + w * kTile + s * 8, smem_desc(v + s * 2048, kTileBytes / 2, 1024), idesc(true),
+                add || s > 0);
+  };
+  auto weights = [&](int w) {  // P_w is there (and O_w rescaled)
+    if (wait(&ct->p_full[w], np[w] & 1)) ++np[w];
+    tc_fence_after();
+  };
+  while (walk.next(p, q)) {
+    const int n = q.n();
+    // V rows past the end of the sequence are cleared by warp 10
+    const bool fix = q.t1 == q.u.tiles && q.t1 * kTile > q.u.a + q.u.n;
+    if (wait(&ct->q_full, nq & 1)) ++nq;
+    auto values_ready = [&](int i) {
+      loaded(base + v_use(i, n));
+      if (fix && i == n - 1) {
+        if (!wait.dead) mbar_arrive(smem_addr(&ct->tail));  // it has landed
+        if (wait(&ct->fixed, nfix & 1)) ++nfix;
+      }
+      tc_fence_after();
+    };
+    if (q.pair) {
+      for (int i = 0; i < 2 && i < n; ++i) {
+        const int use = base + k_use(i);
+        loaded(use);
+        scores(i, stage(use));
+        release(use);
+      }
+      if (n <= 2 && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
+      for (int i = 0; i < n; ++i) {
+        const int w = i & 1, use = base + v_use(i, n);
+        values_ready(i);
+        weights(w);
+        values(w, stage(use), i >= 2);
+        release(use);
+        if (i + 2 < n) {
+          const int ku = base + k_use(i + 2);
+          loaded(ku);
+          scores(w, stage(ku));
+          release(ku);
+          if (i + 3 == n && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
+        } else if (!wait.dead) {
+          tc_commit(smem_addr(&ct->o_full[w]));
+        }
+      }
+    } else {
+      loaded(base);
+      for (int w = 0; w < 2; ++w)
+        if (q.t0 < q.end[w]) scores(w, stage(base));
+      release(base);
+      if (n == 1 && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
+      for (int i = 0; i < n; ++i) {
+        const int vu = base + v_use(i, n), ku = base + k_use(i + 1);
+        const bool more = i + 1 < n;
+        if (more) loaded(ku);
+        values_ready(i);
+        for (int w = 0; w < 2; ++w) {
+          if (q.t0 + i >= q.end[w]) continue;
+          weights(w);
+          values(w, stage(vu), i > 0);
+          if (q.t0 + i + 1 < q.end[w]) scores(w, stage(ku));
+          else if (!wait.dead) tc_commit(smem_addr(&ct->o_full[w]));
+        }
+        release(vu);
+        if (more) release(ku);
+        if (i + 2 == n && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
+      }
+    }
+    base += 2 * n;
+  }
+  // every product has ended before the CTA gives its memory up
+  const int dummy = 0;
+  tc_commit(smem_addr(&ct->drain));
+  if (!mbar_wait_bounded(smem_addr(&ct->drain), 0, (volatile int *)&dummy, p.wait_limit)) {
+    *(volatile int *)&ct->abort = 1;
+    set_status(p.status, MAC_DEV_WAIT_TIMEOUT);
+  }
+}
+
+// ---- V rows past the end (warp 10) ----------------------------------------------
+// Zero weights meet whatever the cache holds there: it may be anything, so
+// the rows are cleared in shared memory before the product reads them.
+__device__ void fix_role(const ChunkParams &p, uint8_t *stages, Control *ct, Walk walk) {
+  const int lane = threadIdx.x & 31;
+  Waiter wait{ct, p.status, p.wait_limit, false};
+  int base = 0;
+  uint32_t nt = 0;
+  Piece q = {};
+  while (walk.next(p, q)) {
+    const int n = q.n(), m = q.u.a + q.u.n;
+    if (q.t1 == q.u.tiles && q.t1 * kTile > m) {
+      const int use = base + v_use(n - 1, n);
+      if (wait(&ct->tail, nt & 1)) {
+        ++nt;
+        uint8_t *v = stages + (use % kNSt) * kTileBytes;
+        const int r0 = max(0, m - (q.t1 - 1) * kTile);
+        for (int i = r0 * 8 + lane; i < kTile * 8; i += 32) {
+          *reinterpret_cast<uint4 *>(v + i * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(v + kTileBytes / 2 + i * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ct->fixed));
+      }
+      __syncwarp();
+    }
+    base += 2 * n;
+  }
+}
+
+// ---- softmax, output (warps 0-7) --------------------------------------------------
+template <bool PAGED>
+__device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t tmem) {
+  const int tid = threadIdx.x, w = tid >> 7, r = tid & 127, lane = tid & 31;
+  const uint32_t lanes = (uint32_t)((tid >> 5) & 3) << 21;  // this warp's 32 TMEM lanes
+  const uint32_t s_at = tmem + w * kTile + lanes;
+  Waiter wait{ct, p.status, p.wait_limit, false};
+  const float scale = p.q_scale, lazy = kLazy / scale;
+  const float2 scale2 = make_float2(scale, scale);
+  uint32_t ns = 0, no[2] = {0, 0};
+  uint32_t status = 0;
+  Piece q = {};
+  while (walk.next(p, q)) {
+    const int tok = ((q.pair ? 0 : w * kTile) + r) / p.G;   // token of this row
+    const int lim = q.u.pos0 + tok;                         // it attends keys [0, lim)
+    const int mine = q.count(w), step = q.pair ? 2 : 1, first = q.t0 + (q.pair ? w : 0);
+    const int n_keys = q.u.pos0 + q.u.n_tok - 1;
+    float m = -INFINITY;
+    float2 l2 = make_float2(0.f, 0.f);
+    for (int i = 0; i < mine; ++i) {
+      const int key0 = (first + i * step) * kTile;
+      uint32_t gone = 0;  // pages of the tile that do not exist
+      if (PAGED) {
+        bool bad = false;
+        const int pg = key0 / kPage + lane;
+        if (lane < kTile / kPage && pg * kPage < n_keys)
+          bad = bad_page(p, p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + pg]);
+        gone = __ballot_sync(0xffffffffu, bad);
+      }
+      const bool live = __all_sync(0xffffffffu, wait(&ct->s_full[w], ns & 1));
+      if (!live) continue;
+      ++ns;
+      tc_fence_after();
+      float s[kTile];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
+      tc_wait_ld();
+      if (key0 + kTile > q.u.pos0) {  // some row of the unit does not attend the whole tile
+        const int left = lim - key0;
+#pragma unroll
+        for (int c = 0; c < kTile; ++c) s[c] = c < left ? s[c] : -INFINITY;
+      }
+      if (PAGED && gone) {
+        status |= MAC_DEV_BAD_PAGE;
+#pragma unroll
+        for (int c = 0; c < kTile; ++c) s[c] = (gone >> (c / kPage)) & 1 ? -INFINITY : s[c];
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kTile; c += 4)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[c + j]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (__any_sync(0xffffffffu, top > m + lazy)) {
+        const float mn = fmaxf(m, top), ms = mn == -INFINITY ? 0.f : mn;
+        const float corr = ex2((m - ms) * scale);
+        m = mn;
+        l2.x *= corr;
+        l2.y *= corr;
+        if (i > 0) {  // the last product into O_w has ended: S_w was issued after it
+          const uint32_t o_at = tmem + 2 * kTile + w * kTile + lanes;
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 32) {
+            float o[32];
+            tc_ld32(o, o_at + c);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= corr;
+            tc_st32(o_at + c, reinterpret_cast<uint32_t *>(o));
+          }
+        }
+      }
+      const float ms = m == -INFINITY ? 0.f : m;
+      const float2 neg = make_float2(-ms * scale, -ms * scale);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float2 x = fma2(make_float2(s[c + 2 * j], s[c + 2 * j + 1]), scale2, neg);
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+          acc[j & 1] = add2(acc[j & 1], x);
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x.y), "f"(x.x));
+        }
+        tc_st16(s_at + c / 2, pk);
+      }
+      l2 = add2(l2, add2(acc[0], acc[1]));
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ct->p_full[w]));
+    }
+    // ---- the piece's rows
+    float l = l2.x + l2.y;
+    const int n_rows = q.u.n_tok * p.G;
+    bool live = true;
+    for (int x = 0; x < 2; ++x)
+      if (q.count(x) > 0) {  // group 0's products end before group 1's
+        if (q.pair || x == w) live &= wait(&ct->o_full[x], no[x] & 1);
+        ++no[x];
+      }
+    float f[2] = {1.f, 1.f};  // factors of O_w and (pair) of the other group's
+    if (q.pair) {
+      ct->ml[w][r] = make_float2(m, l);
+      named_sync(2, 256);
+      const float2 other = ct->ml[w ^ 1][r];
+      const float mn = fmaxf(m, other.x), ms = mn == -INFINITY ? 0.f : mn;
+      f[0] = ex2((m - ms) * scale);
+      f[1] = ex2((other.x - ms) * scale);
+      l = w == 0 ? fmaf(f[0], l, f[1] * other.y) : fmaf(f[1], other.y, f[0] * l);
+      m = mn;
+    }
+    live = __all_sync(0xffffffffu, live) && !wait.dead;
+    tc_fence_after();
+    const int row = (q.pair ? 0 : w * kTile) + r;
+    const bool whole = q.c0 == q.c1, keep = live && row < n_rows;
+    const int c = blockIdx.x;
+    float *part = p.part + ((int64_t)(2 * c + (c == q.c0 ? 1 : 0)) * p.part_rows + row) * kPartStride;
+    const int64_t out_row = (int64_t)(q.u.tok0 + row / p.G) * p.Hq + q.u.g * p.G + row % p.G;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    // a pair's groups take half of the columns each
+#pragma unroll 1
+    for (int cc = q.pair ? w * 64 : 0; cc < (q.pair ? w * 64 + 64 : kHeadDim); cc += 32) {
+      float o[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = 0.f;
+      if (live) {
+        if (mine > 0) {
+          tc_ld32(o, tmem + 2 * kTile + w * kTile + lanes + cc);
+          tc_wait_ld();
+        }
+        if (q.pair) {
+          float o2[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o2[j] = 0.f;
+          if (q.count(w ^ 1) > 0) {
+            tc_ld32(o2, tmem + 2 * kTile + (w ^ 1) * kTile + lanes + cc);
+            tc_wait_ld();
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = w == 0 ? fmaf(f[0], o[j], f[1] * o2[j]) : fmaf(f[1], o2[j], f[0] * o[j]);
+        }
+      }
+      if (!keep) continue;
+      if (whole) {
+        uint16_t *dst = (uint16_t *)p.out + out_row * kHeadDim + cc;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          uint4 v;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o[j + 1] * inv), "f"(o[j] * inv));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o[j + 3] * inv), "f"(o[j + 2] * inv));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.z) : "f"(o[j + 5] * inv), "f"(o[j + 4] * inv));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.w) : "f"(o[j + 7] * inv), "f"(o[j + 6] * inv));
+          *reinterpret_cast<uint4 *>(dst + j) = v;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) store_out(part + cc + j, make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]));
+      }
+    }
+    if (keep && !(q.pair && w == 1)) {
+      if (!whole) *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(m * scale, l);  // base 2, as the merge takes it
+      else if (p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : m * scale * kLn2 + logf(l);
+    }
+    if (q.pair || !whole) {
+      tc_fence_before();
+      named_sync(2, 256);  // O has been read by both groups, the partial is complete
+    }
+    if (whole) continue;
+    if (tid == 0) {
+      ct->last = 0;
+      if (!*(volatile int *)&ct->abort) {
+        const uint32_t n = q.c1 - q.c0 + 1;
+        ct->last = add_acq_rel(p.count + q.c0, 1) == n - 1;
+        if (ct->last) p.count[q.c0] = 0;  // for the next launch
+      }
+    }
+    named_sync(2, 256);
+    const int last = ct->last;
+    named_sync(2, 256);  // read before the next piece writes it
+    if (last) chunk_merge<uint16_t>(p, q.u, q.c0, q.c1, n_rows, tid, 256);
+  }
+  if (status) set_status(p.status, status);
+}
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  uint8_t *qbuf = smem + kNSt * kTileBytes;
+  Control *ct = reinterpret_cast<Control *>(qbuf + 2 * kTileBytes);
+  if (smem_addr(smem) & 1023) {  // the swizzled tiles need it; dynamic shared memory starts there
+    if (threadIdx.x == 0) set_status(p.status, MAC_DEV_BAD_COPY);
+    return;
+  }
+  // this CTA's part of the work, the plan made where the stages go
+  Walk walk;
+  {
+    Plan &plan = *reinterpret_cast<Plan *>(smem);
+    plan.build(p, kMinShare);
+    if (plan.any_bad) chunk_bad_requests<uint16_t, Plan>(p);
+    walk.share = plan.share;
+    walk.x = blockIdx.x * plan.share;
+    walk.end = min(plan.prefix[p.B], walk.x + plan.share);
+    walk.first = true;
+    if (walk.x < walk.end) walk.u = plan.find(p, walk.x);
+  }
+  if (walk.x >= walk.end) return;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNSt; ++i) {
+      mbar_init(smem_addr(&ct->full[i]), 1);
+      mbar_init(smem_addr(&ct->empty[i]), 1);
+    }
+    mbar_init(smem_addr(&ct->q_full), 1);
+    mbar_init(smem_addr(&ct->q_empty), 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_addr(&ct->s_full[w]), 1);
+      mbar_init(smem_addr(&ct->p_full[w]), 4);
+      mbar_init(smem_addr(&ct->o_full[w]), 1);
+    }
+    mbar_init(smem_addr(&ct->tail), 1);
+    mbar_init(smem_addr(&ct->fixed), 1);
+    mbar_init(smem_addr(&ct->drain), 1);
+    ct->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ct->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_proxy_async();  // the plan was in the stages' memory
+  tc_fence_before();
+  block_sync();
+  tc_fence_after();
+  const uint32_t tmem = ct->tmem;
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax_role<PAGED>(p, ct, walk, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8) load_role<PAGED>(p, maps, smem_addr(smem), smem_addr(qbuf), ct, walk);
+    else if (warp == 9) {
+      if ((threadIdx.x & 31) == 0) mma_role(p, smem_addr(smem), smem_addr(qbuf), ct, walk, tmem);
+      __syncwarp();
+    } else if (warp == 10) fix_role(p, smem, ct, walk);
+  }
+  tc_fence_before();
+  block_sync();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ---- host ---------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeFn)f;
+  }();
+  return fn;
+}
+
+// Tensor map of bf16 elements, boxes 64 elements (128 bytes, swizzled) wide.
+bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+  const cuuint32_t unit[4] = {1, 1, 1, 1};
+  EncodeFn fn = encode_fn();
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool PAGED>
+cudaError_t launch(const ChunkParams &p, const Maps &maps, int grid, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, chunk_kernel<PAGED>)) != cudaSuccess) return e;
+  if (fa.numRegs * kThr < 256 * kRegsSoftmax + 128 * kRegsOther) return cudaErrorInvalidValue;  // the split would wait forever
+  chunk_kernel<PAGED><<<grid, kThr, kSmemBytes, s>>>(p, maps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_bf16(const ChunkParams &p, int sms, cudaStream_t s) {
+  Maps maps;
+  const cuuint64_t row = kHeadDim * 2;
+  const cuuint32_t G = p.G;
+  {
+    const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.T}, strides[2] = {row, row * p.Hq};
+    const cuuint32_t box[3] = {64, G, kTile / G};
+    if (!encode(&maps.q, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  for (int i = 0; i < 2; ++i) {
+    CUtensorMap *m = i ? &maps.v : &maps.k;
+    const void *base = i ? p.kv.v : p.kv.k;
+    if (p.kv.paged) {
+      const cuuint64_t dims[4] = {kHeadDim, kPage, (cuuint64_t)p.Hkv, (cuuint64_t)p.kv.n_pages};
+      const cuuint64_t strides[3] = {row, row * kPage, row * kPage * p.Hkv};
+      const cuuint32_t box[4] = {64, kPage, 1, 1};
+      if (!encode(m, base, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    } else {
+      const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)p.kv.capacity, (cuuint64_t)p.B * p.Hkv};
+      const cuuint64_t strides[2] = {row, row * p.kv.capacity};
+      const cuuint32_t box[3] = {64, kTile, 1};
+      if (!encode(m, base, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+  }
+  const int grid = sms < kChunkGrid ? sms : kChunkGrid;
+  return p.kv.paged ? launch<true>(p, maps, grid, s) : launch<false>(p, maps, grid, s);
+}
+
+}  // namespace mac

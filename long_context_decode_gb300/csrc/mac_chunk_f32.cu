@@ -243,12 +243,4 @@ cudaError_t launch_chunk_f32(const ChunkParams &p, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_chunk_bf16(const ChunkParams &p, int sms, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<uint16_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
-  if (e != cudaSuccess) return e;
-  const int grid = 2 * sms < kChunkGrid ? 2 * sms : kChunkGrid;
-  chunk_kernel<uint16_t><<<grid, kThr, sizeof(Shared), s>>>(p);
-  return cudaGetLastError();
-}
-
 }  // namespace mac

@@ -700,6 +700,7 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
   p.q_scale = q_scale(cfg);
   p.kv = kv_view(cfg, kv);
   p.max_len = max_len(cfg, p.kv);
+  if (p.max_len > 0x7ffffe00) p.max_len = 0x7ffffe00;  // key numbers, rounded up to a tile, in 32 bits
   p.q = q;
   p.q_start = q_start;
   p.seq_len = seq_len;
@@ -709,7 +710,10 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
   p.count = (uint32_t *)(ws + L.count);
   p.part = (float *)(ws + L.part);
   p.part_rows = L.part_rows;
-  p.wait_limit = kWaitLimit;
+  p.wait_limit = t_wait_limit > 0 ? t_wait_limit : kWaitLimit;
+  p.withhold = t_withhold;
+  t_wait_limit = 0;
+  t_withhold = -1;
   cudaStream_t s = (cudaStream_t)stream;
   const int sms = num_sms();
   if (sms < 1) return MAC_ERR_CUDA;
