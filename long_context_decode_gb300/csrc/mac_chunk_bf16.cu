@@ -11,7 +11,7 @@
 //
 // One CTA per SM, twelve warps:
 //   warps 0-3, 4-7  softmax of row tile 0 and 1 (a thread owns a row);
-//   warp 8          copies Q, K and V by TMA into swizzled shared memory;
+//   warps 8, 11     copy Q and K, and V, by TMA into swizzled shared memory;
 //   warp 9          issues the products: S into TMEM from shared memory, and
 //                   O += P V with P read back from TMEM;
 //   warp 10         clears V rows past the end of the sequence.
@@ -34,7 +34,7 @@ constexpr int kCost0 = 2, kMinShare = 4;
 constexpr int kThr = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;  // registers per thread once the roles have split
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThr * 168, "the split comes out of the launch's registers");
-constexpr int kNSt = 5;                       // stages of the K/V ring
+constexpr int kStK = 2, kStV = 3, kNSt = kStK + kStV;  // stages of the K ring and of the V ring
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr float kLazy = 8.f;                  // growth of the maximum (base 2) that moves the reference
 using Plan = ChunkPlan<kChunkRowsBf16, kTile, kCost0>;
@@ -59,21 +59,67 @@ static_assert(sizeof(Plan) <= kNSt * kTileBytes, "the plan is made where the sta
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One arrival on `bar` once the products issued so far have ended.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// D[128 x 128] (+)= A B, 16 deep; bf16 inputs, fp32 sums.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+
+// Shared memory descriptor, 128-byte swizzle: address / 16 and leading byte
+// offset / 16 (bit 16) in the low word; in the high one, stride byte offset
+// / 16 (groups of eight rows are 1024 bytes apart), version 1 (bit 46) and
+// swizzle mode 2 (bit 61).  A tile is two halves of 64 columns, 128-byte rows: Q and K
+// step 16 columns along a row (32 bytes); V, whose columns are the
+// product's N, steps 16 rows (2048 bytes), its halves a leading offset apart.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
+
+// The products of a tile, D[128 x 128] (+)= A B in eight steps of depth 16;
+// bf16 inputs, fp32 sums.  a, b: low words of shared memory descriptors (a of
+// tc_values: TMEM).  The whole warp runs them and one lane issues: with its
+// control flow uniform the operands stay in uniform registers, where the
+// instruction takes them from.  tc_scores ends with one arrival on `bar`
+// once all products issued so far have ended.
+__device__ __forceinline__ void tc_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)add)
+      "{\n\t.reg .pred q, t, e;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 q, %4, %4;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 1024;\n\tadd.u32 y, %2, 1024;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 1026;\n\tadd.u32 y, %2, 1026;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 1028;\n\tadd.u32 y, %2, 1028;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u32 x, %1, 1030;\n\tadd.u32 y, %2, 1030;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_values(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred q, t, e;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+      "add.u32 x, %1, 32;\n\tadd.u32 y, %2, 512;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+      "add.u32 x, %1, 40;\n\tadd.u32 y, %2, 640;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+      "add.u32 x, %1, 48;\n\tadd.u32 y, %2, 768;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+      "add.u32 x, %1, 56;\n\tadd.u32 y, %2, 896;\n\tmov.b64 b, {y, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n\t"
+      "}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(add)
+      : "memory");
+}
+// Two arrivals at once (the stages of a key and a value tile).
+__device__ __forceinline__ void tc_commit2(uint32_t bar0, uint32_t bar1) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(bar0), "r"(bar1)
       : "memory");
 }
 
@@ -81,13 +127,6 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 // along N where asked (bit 16), N/8 from bit 17, M/16 from bit 24.
 __host__ __device__ constexpr uint32_t idesc(bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
-}
-
-// Shared memory descriptor, 128-byte swizzle: address / 16, leading and
-// stride byte offsets / 16, version 1 (bit 46), swizzle mode 2 (bit 61).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46) |
-         (2ull << 61);
 }
 
 __device__ __forceinline__ void tc_ld32(float *r, uint32_t addr) {
@@ -118,6 +157,13 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *u) {
       "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
       "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
       : "memory");
+}
+// Registers that a load has filled are used after the wait only.
+__device__ __forceinline__ void tc_loaded32(float *r) {
+  asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+               "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]));
+  asm volatile("" : "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+               "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -161,11 +207,12 @@ struct Piece {
   ChunkUnit u;
   int t0, t1;       // its key tiles
   int pair;         // both groups on row tile 0, key tiles in turn
-  int end[2];       // normal: key tiles of each row tile end here (after t0, or none)
+  int end0;         // normal: key tiles of row tile 0 end here (those of row tile 1 at t1)
   int c0, c1;       // CTAs that hold the unit's pieces
   __device__ int n() const { return t1 - t0; }
   // key tiles of group w
-  __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : max(0, end[w] - t0); }
+  __device__ int end(int w) const { return w ? t1 : end0; }
+  __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : max(0, end(w) - t0); }
 };
 
 struct Walk {
@@ -185,8 +232,7 @@ struct Walk {
       q.u = u;
       q.pair = u.n_tok * p.G <= kTile;
       const int tok = kTile / p.G;  // tokens of row tile 0
-      q.end[0] = min(q.t1, (u.pos0 + tok - 1 + kTile - 1) / kTile);
-      q.end[1] = q.t1;
+      q.end0 = min(q.t1, (u.pos0 + tok - 1 + kTile - 1) / kTile);
       q.c0 = (int)(u.at / share);
       q.c1 = (int)((u_end - 1) / share);
       return true;
@@ -195,12 +241,7 @@ struct Walk {
   }
 };
 
-// Ring position of the i-th key (value) tile of a piece of n tiles, in the
-// order in which they are copied and used: K0 K1 V0 K2 V1 .. V(n-1).
-__device__ __forceinline__ int k_use(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int v_use(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
-
-// Waits that every role makes.  After one has run out (or another role's
+// Waits that every role makes, a whole warp at a time.  After one has run out (or another role's
 // has: ct->abort) all return false at once; the roles then walk through
 // their loops without touching anything, so that their barriers still meet.
 struct Waiter {
@@ -208,9 +249,13 @@ struct Waiter {
   uint32_t *status;
   long long limit;
   bool dead;
-  __device__ bool operator()(unsigned long long *bar, uint32_t parity) {
+  __device__ __forceinline__ bool operator()(unsigned long long *bar, uint32_t parity) {
+    if (!__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity)) || dead) return slow(smem_addr(bar), parity);
+    return true;
+  }
+  __device__ __forceinline__ bool slow(uint32_t bar, uint32_t parity) {
     if (dead) return false;
-    if (!mbar_wait_bounded(smem_addr(bar), parity, (volatile int *)&ct->abort, limit)) {
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, (volatile int *)&ct->abort, limit))) {
       dead = true;
       *(volatile int *)&ct->abort = 1;
       set_status(status, MAC_DEV_WAIT_TIMEOUT);
@@ -224,167 +269,179 @@ __device__ __forceinline__ bool bad_page(const ChunkParams &p, int id) {
   return id < 0 || id >= p.kv.n_pages;
 }
 
-// ---- copies (warp 8) ---------------------------------------------------------
-template <bool PAGED>
+// ---- copies (warps 8 and 11) ---------------------------------------------------
+// One ring's copies: key or value tiles into stages st0 .. st0 + NST - 1, and
+// (K) the Q tiles.  A paged tile is 8 pages of two 64-column halves, one copy each.
+template <bool PAGED, bool IS_K>
 __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stages, uint32_t qbuf, Control *ct, Walk walk) {
-  const int lane = threadIdx.x & 31;
+  constexpr int NST = IS_K ? kStK : kStV, ST0 = IS_K ? 0 : kStK;
+  const CUtensorMap *map = IS_K ? &maps.k : &maps.v;
+  const int lane = threadIdx.x & 31, half = lane >> 3 & 1, pg = lane & 7;
   Waiter wait{ct, p.status, p.wait_limit, false};
   int use = 0;       // stage uses so far
   uint32_t nq = 0;   // Q tiles so far
   Piece q = {};
-  auto tile = [&](const CUtensorMap *m, int t) {
-    const int st = use % kNSt, round = use / kNSt;
-    const bool ok = wait(&ct->empty[st], (round + 1) & 1);  // the first round finds the stages free
-    const uint32_t bar = smem_addr(&ct->full[st]), dst = stages + st * kTileBytes;
-    if (__all_sync(0xffffffffu, ok)) {
-      if (PAGED) {
-        int id = p.kv.n_pages;  // out of range: the copy fills with zeros
-        const int pg = t * (kTile / kPage) + lane;
-        if (lane < kTile / kPage && (int64_t)pg * kPage < q.u.pos0 + q.u.n_tok - 1) {
-          id = p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + pg];
-          if (bad_page(p, id)) id = p.kv.n_pages;
-        }
+  while (walk.next(p, q)) {
+    const int n_pages = (q.u.pos0 + q.u.n_tok - 1 + kPage - 1) / kPage;  // of the unit's keys
+    auto page = [&](int t) {  // page of this lane's copy; out of range where there is none: the copy fills with zeros
+      const int k = t * (kTile / kPage) + pg;
+      int id = k < n_pages ? p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + k] : -1;
+      return bad_page(p, id) ? p.kv.n_pages : id;
+    };
+    int id = PAGED ? page(q.t0) : 0;
+    for (int t = q.t0; t < q.t1; ++t) {
+      const int next = PAGED && t + 1 < q.t1 ? page(t + 1) : 0;  // ahead of its use
+      const int st = ST0 + use % NST;
+      if (wait(&ct->empty[st], (use / NST + 1) & 1)) {  // the first round finds the stages free
+        const uint32_t bar = smem_addr(&ct->full[st]), dst = stages + st * kTileBytes;
         if (lane == 0) mbar_expect_tx(bar, kTileBytes);
         __syncwarp();
-        if (lane < kTile / kPage && use != p.withhold) {
-          tma_4d(dst + lane * 2048, m, 0, 0, q.u.g, id, bar);
-          tma_4d(dst + kTileBytes / 2 + lane * 2048, m, 64, 0, q.u.g, id, bar);
+        if (!IS_K || use != p.withhold) {
+          if (PAGED) {
+            if (lane < 16) tma_4d(dst + half * (kTileBytes / 2) + pg * (kPage * 128), map, 64 * half, 0, q.u.g, id, bar);
+          } else if (lane < 2) {
+            tma_3d(dst + lane * (kTileBytes / 2), map, 64 * lane, t * kTile, q.u.b * p.Hkv + q.u.g, bar);
+          }
         }
-      } else if (lane == 0) {
-        mbar_expect_tx(bar, kTileBytes);
-        if (use != p.withhold) {
-          tma_3d(dst, m, 0, t * kTile, q.u.b * p.Hkv + q.u.g, bar);
-          tma_3d(dst + kTileBytes / 2, m, 64, t * kTile, q.u.b * p.Hkv + q.u.g, bar);
-        }
+        ++use;
       }
-      ++use;
-    }
-    __syncwarp();
-  };
-  while (walk.next(p, q)) {
-    const int n = q.n();
-    tile(&maps.k, q.t0);
-    {
-      const bool ok = wait(&ct->q_empty, (nq + 1) & 1);
-      if (ok && lane == 0) {
-        const uint32_t bar = smem_addr(&ct->q_full);
-        mbar_expect_tx(bar, (q.pair ? 1 : 2) * kTileBytes);
-        for (int w = 0; w < (q.pair ? 1 : 2); ++w)
-          for (int h = 0; h < 2; ++h)
-            tma_3d(qbuf + w * kTileBytes + h * (kTileBytes / 2), &maps.q, 64 * h, q.u.g * p.G, q.u.tok0 + w * (kTile / p.G), bar);
-      }
-      if (ok) ++nq;
+      id = next;
       __syncwarp();
-    }
-    if (n > 1) tile(&maps.k, q.t0 + 1);
-    for (int i = 0; i < n; ++i) {
-      tile(&maps.v, q.t0 + i);
-      if (i + 2 < n) tile(&maps.k, q.t0 + i + 2);
+      if (IS_K && t == q.t0 && wait(&ct->q_empty, (nq + 1) & 1)) {
+        const uint32_t bar = smem_addr(&ct->q_full);
+        const int tiles = q.pair ? 1 : 2;
+        if (lane == 0) mbar_expect_tx(bar, tiles * kTileBytes);
+        __syncwarp();
+        if (lane < 2 * tiles)
+          tma_3d(qbuf + lane * (kTileBytes / 2), &maps.q, 64 * (lane & 1), q.u.g * p.G, q.u.tok0 + (lane >> 1) * (kTile / p.G), bar);
+        ++nq;
+        __syncwarp();
+      }
     }
   }
   // After a wait ran out, copies may still be in flight: let them land
   // before the CTA gives its shared memory up.
   if (*(volatile int *)&ct->abort) {
     const int dummy = 0;
-    for (int u = use > kNSt ? use - kNSt : 0; u < use; ++u)
-      mbar_wait_bounded(smem_addr(&ct->full[u % kNSt]), (u / kNSt) & 1, (volatile int *)&dummy, p.wait_limit);
+    for (int u = use > NST ? use - NST : 0; u < use; ++u)
+      mbar_wait_bounded(smem_addr(&ct->full[ST0 + u % NST]), (u / NST) & 1, (volatile int *)&dummy, p.wait_limit);
     if (nq) mbar_wait_bounded(smem_addr(&ct->q_full), (nq - 1) & 1, (volatile int *)&dummy, p.wait_limit);
   }
 }
 
-// ---- products (warp 9, one thread) ---------------------------------------------
+// ---- products (warp 9) -----------------------------------------------------------
+// The tensor cores work through what is issued in order and hold only a few
+// products ahead, so whatever this warp does between the last product of one
+// group and the first of the other must be short: waits come where products
+// are still running, and one whose phase has already come costs one test.
+struct RingPos {
+  uint32_t st, phase;  // stage, parity of its next completion
+  __device__ void step(uint32_t first, uint32_t n) {
+    if (++st == first + n) {
+      st = first;
+      phase ^= 1;
+    }
+  }
+};
+
 __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, Control *ct, Walk walk, uint32_t tmem) {
   Waiter wait{ct, p.status, p.wait_limit, false};
-  int base = 0;
-  uint32_t nq = 0, np[2] = {0, 0}, nfix = 0;
+  RingPos k = {0, 0}, v = {kStK, 0};
+  uint32_t q_phase = 0, fix_phase = 0, p_phase[2] = {0, 0};
   Piece q = {};
-  auto stage = [&](int use) { return stages + (use % kNSt) * kTileBytes; };
-  auto loaded = [&](int use) { return wait(&ct->full[use % kNSt], (use / kNSt) & 1); };
-  auto release = [&](int use) {
-    if (!wait.dead) tc_commit(smem_addr(&ct->empty[use % kNSt]));
+  auto addr = [&](uint32_t st) { return stages + st * kTileBytes; };
+  auto commit = [&](unsigned long long *bar) {
+    if (!wait.dead) tc_commit(smem_addr(bar));
   };
-  auto scores = [&](int w, uint32_t k) {  // S_w = Q K^T, then tell group w
+  auto scores = [&](uint32_t w, uint32_t qa) {  // S_w = Q K^T, then tell group w
     if (wait.dead) return;
-    const uint32_t qa = qbuf + (q.pair ? 0 : w) * kTileBytes;
-#pragma unroll
-    for (int s = 0; s < kHeadDim / 16; ++s) {
-      const uint32_t off = (s >> 2) * (kTileBytes / 2) + (s & 3) * 32;
-      tc_mma_ss(tmem + w * kTile, smem_desc(qa + off, 16, 1024), smem_desc(k + off, 16, 1024), idesc(false), s > 0);
-    }
-    tc_commit(smem_addr(&ct->s_full[w]));
+    tc_scores(tmem + w * kTile, desc_lo(qa, 16), desc_lo(addr(k.st), 16), idesc(false), smem_addr(&ct->s_full[w]));
   };
-  auto values = [&](int w, uint32_t v, bool add) {  // O_w (+)= P_w V
-    if (wait.dead) return;
-#pragma unroll
-    for (int s = 0; s < kTile / 16; ++s)
-      tc_mma_ts(tmem + 2 * kTile + w * kTile, tmem + w * kTile + s * 8, smem_desc(v + s * 2048, kTileBytes / 2, 1024), idesc(true),
-                add || s > 0);
-  };
-  auto weights = [&](int w) {  // P_w is there (and O_w rescaled)
-    if (wait(&ct->p_full[w], np[w] & 1)) ++np[w];
+  auto values = [&](uint32_t w, uint32_t add) {  // O_w (+)= P_w V, once P_w is there (and O_w rescaled)
+    wait(&ct->p_full[w], w ? p_phase[1] : p_phase[0]);
     tc_fence_after();
+    if (wait.dead) return;
+    tc_values(tmem + 2 * kTile + w * kTile, tmem + w * kTile, desc_lo(addr(v.st), kTileBytes / 2), idesc(true), add);
+    if (w) p_phase[1] ^= 1; else p_phase[0] ^= 1;
+  };
+  auto keys_ready = [&] { wait(&ct->full[k.st], k.phase); };
+  auto free_keys = [&] {
+    commit(&ct->empty[k.st]);
+    k.step(0, kStK);
+  };
+  auto free_values = [&] {
+    commit(&ct->empty[v.st]);
+    v.step(kStK, kStV);
   };
   while (walk.next(p, q)) {
     const int n = q.n();
     // V rows past the end of the sequence are cleared by warp 10
     const bool fix = q.t1 == q.u.tiles && q.t1 * kTile > q.u.a + q.u.n;
-    if (wait(&ct->q_full, nq & 1)) ++nq;
-    auto values_ready = [&](int i) {
-      loaded(base + v_use(i, n));
-      if (fix && i == n - 1) {
-        if (!wait.dead) mbar_arrive(smem_addr(&ct->tail));  // it has landed
-        if (wait(&ct->fixed, nfix & 1)) ++nfix;
+    auto values_ready = [&](bool last) {
+      wait(&ct->full[v.st], v.phase);
+      if (last && fix) {
+        if (!wait.dead && (threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&ct->tail));  // it has landed
+        wait(&ct->fixed, fix_phase);
+        fix_phase ^= 1;
       }
-      tc_fence_after();
     };
+    wait(&ct->q_full, q_phase);
+    q_phase ^= 1;
+    keys_ready();
     if (q.pair) {
-      for (int i = 0; i < 2 && i < n; ++i) {
-        const int use = base + k_use(i);
-        loaded(use);
-        scores(i, stage(use));
-        release(use);
+      // both groups on the same rows, key tiles in turn
+      scores(0, qbuf);
+      free_keys();
+      if (n > 1) {
+        keys_ready();
+        scores(1, qbuf);
+        free_keys();
       }
-      if (n <= 2 && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
+      if (n <= 2) commit(&ct->q_empty);
       for (int i = 0; i < n; ++i) {
-        const int w = i & 1, use = base + v_use(i, n);
-        values_ready(i);
-        weights(w);
-        values(w, stage(use), i >= 2);
-        release(use);
+        const uint32_t w = i & 1;
+        values_ready(i + 1 == n);
+        values(w, i >= 2);
+        free_values();
         if (i + 2 < n) {
-          const int ku = base + k_use(i + 2);
-          loaded(ku);
-          scores(w, stage(ku));
-          release(ku);
-          if (i + 3 == n && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
-        } else if (!wait.dead) {
-          tc_commit(smem_addr(&ct->o_full[w]));
+          keys_ready();
+          scores(w, qbuf);
+          free_keys();
+          if (i + 3 == n) commit(&ct->q_empty);
+        } else {
+          commit(&ct->o_full[w]);
         }
       }
-    } else {
-      loaded(base);
-      for (int w = 0; w < 2; ++w)
-        if (q.t0 < q.end[w]) scores(w, stage(base));
-      release(base);
-      if (n == 1 && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
-      for (int i = 0; i < n; ++i) {
-        const int vu = base + v_use(i, n), ku = base + k_use(i + 1);
-        const bool more = i + 1 < n;
-        if (more) loaded(ku);
-        values_ready(i);
-        for (int w = 0; w < 2; ++w) {
-          if (q.t0 + i >= q.end[w]) continue;
-          weights(w);
-          values(w, stage(vu), i > 0);
-          if (q.t0 + i + 1 < q.end[w]) scores(w, stage(ku));
-          else if (!wait.dead) tc_commit(smem_addr(&ct->o_full[w]));
-        }
-        release(vu);
-        if (more) release(ku);
-        if (i + 2 == n && !wait.dead) tc_commit(smem_addr(&ct->q_empty));
+      continue;
+    }
+    // a row tile each; those of row tile 0 may end before those of row tile 1
+    const int n0 = q.count(0);
+    if (n0 > 0) scores(0, qbuf);
+    scores(1, qbuf + kTileBytes);
+    free_keys();
+    if (n == 1) commit(&ct->q_empty);
+    for (int i = 0; i < n; ++i) {
+      values_ready(i + 1 == n);
+      if (i < n0) {
+        values(0, i > 0);
+        if (i + 1 < n) keys_ready();
+        if (i + 1 < n0) scores(0, qbuf);
+        else commit(&ct->o_full[0]);
+      } else if (i + 1 < n) {
+        keys_ready();
+      }
+      values(1, i > 0);
+      if (i + 1 < n) {
+        scores(1, qbuf + kTileBytes);
+        if (!wait.dead) tc_commit2(smem_addr(&ct->empty[v.st]), smem_addr(&ct->empty[k.st]));
+        v.step(kStK, kStV);
+        k.step(0, kStK);
+        if (i + 2 == n) commit(&ct->q_empty);
+      } else {
+        commit(&ct->o_full[1]);
+        free_values();
       }
     }
-    base += 2 * n;
   }
   // every product has ended before the CTA gives its memory up
   const int dummy = 0;
@@ -401,16 +458,15 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
 __device__ void fix_role(const ChunkParams &p, uint8_t *stages, Control *ct, Walk walk) {
   const int lane = threadIdx.x & 31;
   Waiter wait{ct, p.status, p.wait_limit, false};
-  int base = 0;
+  int uv = 0;
   uint32_t nt = 0;
   Piece q = {};
   while (walk.next(p, q)) {
     const int n = q.n(), m = q.u.a + q.u.n;
     if (q.t1 == q.u.tiles && q.t1 * kTile > m) {
-      const int use = base + v_use(n - 1, n);
       if (wait(&ct->tail, nt & 1)) {
         ++nt;
-        uint8_t *v = stages + (use % kNSt) * kTileBytes;
+        uint8_t *v = stages + (kStK + (uv + n - 1) % kStV) * kTileBytes;
         const int r0 = max(0, m - (q.t1 - 1) * kTile);
         for (int i = r0 * 8 + lane; i < kTile * 8; i += 32) {
           *reinterpret_cast<uint4 *>(v + i * 16) = make_uint4(0, 0, 0, 0);
@@ -422,7 +478,7 @@ __device__ void fix_role(const ChunkParams &p, uint8_t *stages, Control *ct, Wal
       }
       __syncwarp();
     }
-    base += 2 * n;
+    uv += n;
   }
 }
 
@@ -435,7 +491,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
   Waiter wait{ct, p.status, p.wait_limit, false};
   const float scale = p.q_scale, lazy = kLazy / scale;
   const float2 scale2 = make_float2(scale, scale);
-  uint32_t ns = 0, no[2] = {0, 0};
+  uint32_t ns = 0, no = 0;  // scores taken; parity of each group's next output
   uint32_t status = 0;
   Piece q = {};
   while (walk.next(p, q)) {
@@ -455,14 +511,15 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
           bad = bad_page(p, p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + pg]);
         gone = __ballot_sync(0xffffffffu, bad);
       }
-      const bool live = __all_sync(0xffffffffu, wait(&ct->s_full[w], ns & 1));
-      if (!live) continue;
+      if (!wait(&ct->s_full[w], ns & 1)) continue;
       ++ns;
       tc_fence_after();
       float s[kTile];
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
       tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tc_loaded32(s + c);
       if (key0 + kTile > q.u.pos0) {  // some row of the unit does not attend the whole tile
         const int left = lim - key0;
 #pragma unroll
@@ -473,11 +530,11 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
 #pragma unroll
         for (int c = 0; c < kTile; ++c) s[c] = (gone >> (c / kPage)) & 1 ? -INFINITY : s[c];
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+      float mx[4] = {fmaxf(s[0], s[4]), fmaxf(s[1], s[5]), fmaxf(s[2], s[6]), fmaxf(s[3], s[7])};
 #pragma unroll
-      for (int c = 4; c < kTile; c += 4)
+      for (int c = 8; c < kTile; c += 8)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[c + j]);
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(s[c + j], s[c + 4 + j]));  // three-input maximum
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       if (__any_sync(0xffffffffu, top > m + lazy)) {
         const float mn = fmaxf(m, top), ms = mn == -INFINITY ? 0.f : mn;
@@ -492,6 +549,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
             float o[32];
             tc_ld32(o, o_at + c);
             tc_wait_ld();
+            tc_loaded32(o);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] *= corr;
             tc_st32(o_at + c, reinterpret_cast<uint32_t *>(o));
@@ -526,8 +584,8 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     bool live = true;
     for (int x = 0; x < 2; ++x)
       if (q.count(x) > 0) {  // group 0's products end before group 1's
-        if (q.pair || x == w) live &= wait(&ct->o_full[x], no[x] & 1);
-        ++no[x];
+        if (q.pair || x == w) live &= wait(&ct->o_full[x], no >> x & 1);
+        no ^= 1u << x;
       }
     float f[2] = {1.f, 1.f};  // factors of O_w and (pair) of the other group's
     if (q.pair) {
@@ -540,7 +598,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
       l = w == 0 ? fmaf(f[0], l, f[1] * other.y) : fmaf(f[1], other.y, f[0] * l);
       m = mn;
     }
-    live = __all_sync(0xffffffffu, live) && !wait.dead;
+    live = live && !wait.dead;
     tc_fence_after();
     const int row = (q.pair ? 0 : w * kTile) + r;
     const bool whole = q.c0 == q.c1, keep = live && row < n_rows;
@@ -558,6 +616,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
         if (mine > 0) {
           tc_ld32(o, tmem + 2 * kTile + w * kTile + lanes + cc);
           tc_wait_ld();
+          tc_loaded32(o);
         }
         if (q.pair) {
           float o2[32];
@@ -566,6 +625,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
           if (q.count(w ^ 1) > 0) {
             tc_ld32(o2, tmem + 2 * kTile + (w ^ 1) * kTile + lanes + cc);
             tc_wait_ld();
+            tc_loaded32(o2);
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = w == 0 ? fmaf(f[0], o[j], f[1] * o2[j]) : fmaf(f[1], o2[j], f[0] * o[j]);
@@ -668,10 +728,10 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
     softmax_role<PAGED>(p, ct, walk, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) load_role<PAGED>(p, maps, smem_addr(smem), smem_addr(qbuf), ct, walk);
+    if (warp == 8) load_role<PAGED, true>(p, maps, smem_addr(smem), smem_addr(qbuf), ct, walk);
+    else if (warp == 11) load_role<PAGED, false>(p, maps, smem_addr(smem), smem_addr(qbuf), ct, walk);
     else if (warp == 9) {
-      if ((threadIdx.x & 31) == 0) mma_role(p, smem_addr(smem), smem_addr(qbuf), ct, walk, tmem);
-      __syncwarp();
+      mma_role(p, smem_addr(smem), smem_addr(qbuf), ct, walk, tmem);
     } else if (warp == 10) fix_role(p, smem, ct, walk);
   }
   tc_fence_before();
