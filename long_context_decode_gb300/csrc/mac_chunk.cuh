@@ -2,12 +2,15 @@
 // over the CTAs, shared by the bf16 (tensor core) and fp32 kernels.
 //
 // Units are laid end to end in order (request, KV head, row tile) on a cost
-// axis: a unit costs COST0 plus one per tile of KT keys that its last row
-// attends.  CTA c works on positions [c share, (c+1) share): any number of
-// whole units and at most two cut ones, so rows of very different lengths,
-// one long row and many short ones all spread evenly.  A cut unit's pieces
-// leave (o, max, sum) partials; the CTA that finishes the last one merges
-// them in CTA order, so results do not depend on timing.
+// axis: a unit costs COST0 plus W per tile of KT keys that its last row
+// attends (WS for a unit of at most half the rows).  CTA c works on
+// positions [c share, (c+1) share): any number of whole units and at most
+// two cut ones, so rows of very different lengths, one long row and many
+// short ones all spread evenly.  A cut unit's pieces leave (o, max, sum)
+// partials; the CTA that finishes the last one merges them in CTA order, so
+// results do not depend on timing.  When there is a CTA for every unit and
+// all are short (kShort tiles), each CTA takes one whole unit instead: a
+// merge would cost more than the cut saves.
 #pragma once
 
 #include "mac_batch.cuh"
@@ -16,11 +19,13 @@ namespace mac {
 
 #ifdef __CUDACC__
 
-// sum of ceil(j / s), j = 1 .. n
-__device__ __forceinline__ long long ceil_sum(long long n, int s) {
-  const long long q = n / s, r = n % s;
-  return s * (q * (q + 1) / 2) + r * (q + 1);
+// sum of ceil(j / 2^k), j = 1 .. n
+__device__ __forceinline__ long long ceil_sum(long long n, int k) {
+  const long long q = n >> k, r = n - (q << k);
+  return ((q * (q + 1) >> 1) << k) + r * (q + 1);
 }
+
+__host__ __device__ constexpr int log2i(int x) { return x <= 1 ? 0 : 1 + log2i(x >> 1); }
 
 struct ChunkUnit {
   int b, g, i;         // request, KV head, row tile of the request's new tokens
@@ -31,47 +36,60 @@ struct ChunkUnit {
   long long at;        // cost position of its first tile
 };
 
-// One request's work, per KV head.
-template <int ROWS, int KT, int COST0>
+// A CTA's share of a unit.
+struct ChunkPiece {
+  ChunkUnit u;
+  int t0, t1;          // its key tiles
+  __device__ bool cut() const { return t0 > 0 || t1 < u.tiles; }
+};
+
+template <int ROWS, int KT, int COST0, int W, int WS>
 struct ChunkPlan {
-  // tiles attended by the first k units of a request with `a` tokens before
-  // its new ones, all k of them whole (tt tokens each)
-  __device__ static long long tiles_before(int a, int tt, int k) {
-    if (tt <= KT) {
-      const int s = KT / tt;
-      const long long e = (a + (long long)tt - 1) / tt;
-      return ceil_sum(e + k, s) - ceil_sum(e, s);
-    }
-    const int m = tt / KT;
-    return (long long)k * ((a + (long long)KT - 1) / KT) + (long long)m * k * (k + 1) / 2;
-  }
-  // exact because KT divides tt or tt divides KT
-  __device__ static long long cost(int a, int n, int tt) {
-    if (n <= 0) return 0;
-    const int u = (n + tt - 1) / tt;
-    return tiles_before(a, tt, u - 1) + ((long long)a + n + KT - 1) / KT + (long long)u * COST0;
-  }
+  static constexpr int kKt = log2i(KT);
+  static constexpr int kShort = 8;
 
   long long prefix[kMaxUnits + 1];  // cost of all requests before b, all KV heads
   long long warp_tot[32];
   long long share;
-  int any_bad;
+  int any_bad, any_long, whole;
 
-  // All threads of the block (a multiple of 32, at most 1024) call it.
-  // MIN_SHARE: least cost worth a CTA of its own.
-  __device__ void build(const ChunkParams &p, int min_share) {
-    const int tt = ROWS / p.G, n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __device__ static int log_tokens(const ChunkParams &p) { return log2i(ROWS) - (31 - __clz(p.G)); }  // tokens per unit
+  __device__ static int units(int n, int lt) { return (n + (1 << lt) - 1) >> lt; }
+  __device__ static int weight(int n_tok, int lt) { return 2 * n_tok > 1 << lt ? W : WS; }
+
+  // tiles attended by the first k units, all of them full, of a request
+  // with `a` tokens before its new ones; exact because one of KT and the
+  // tokens per unit divides the other
+  __device__ static long long tiles_before(int a, int lt, int k) {
+    if (lt <= kKt) {
+      const long long e = (a + (1LL << lt) - 1) >> lt;
+      return ceil_sum(e + k, kKt - lt) - ceil_sum(e, kKt - lt);
+    }
+    return (long long)k * ((a + (long long)KT - 1) >> kKt) + ((long long)k * (k + 1) << (lt - kKt)) / 2;
+  }
+  // cost of the units before unit k, and of all units of one KV head
+  __device__ static long long before(int a, int lt, int k, bool whole) {
+    return whole ? k : tiles_before(a, lt, k) * W + (long long)k * COST0;
+  }
+  __device__ static long long cost(int a, int n, int lt, bool whole) {
+    if (n <= 0) return 0;
+    const int u = units(n, lt);
+    if (whole) return u;
+    return before(a, lt, u - 1, false) + COST0 + (((long long)a + n + KT - 1) >> kKt) * weight(n - ((u - 1) << lt), lt);
+  }
+
+  // Scan of the requests' costs; returns the sum.
+  __device__ long long scan(const ChunkParams &p, int lt, bool by_units) {
+    const int n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long carry = 0;
-    if (threadIdx.x == 0) any_bad = 0;
-    __syncthreads();
     for (int b0 = 0; b0 < p.B; b0 += n_thr) {
       const int b = b0 + threadIdx.x;
       long long v = 0;
       if (b < p.B) {
         int a, n;
-        const int st = request(p, b, &a, &n);
-        if (st) any_bad = 1;
-        v = cost(a, n, tt) * p.Hkv;
+        if (request(p, b, &a, &n)) any_bad = 1;
+        if (((long long)a + n + KT - 1) >> kKt > kShort && n > 0) any_long = 1;
+        v = cost(a, n, lt, by_units) * p.Hkv;
       }
       for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, v, d);
@@ -80,7 +98,7 @@ struct ChunkPlan {
       if (lane == 31) warp_tot[warp] = v;
       __syncthreads();
       long long add = carry, all = carry;
-      for (int w = 0; w < n_thr / 32; ++w) {
+      for (int w = 0; w < n_thr >> 5 && b0 + w * 32 < p.B; ++w) {
         if (w < warp) add += warp_tot[w];
         all += warp_tot[w];
       }
@@ -88,13 +106,27 @@ struct ChunkPlan {
       carry = all;
       __syncthreads();
     }
+    return carry;
+  }
+
+  // All threads of the block (a multiple of 32, at most 1024) call it.
+  // min_share: least cost worth a CTA of its own.
+  __device__ void build(const ChunkParams &p, int min_share) {
+    const int lt = log_tokens(p);
     if (threadIdx.x == 0) {
+      any_bad = any_long = 0;
       prefix[0] = 0;
-      long long ctas = carry / min_share;
+    }
+    __syncthreads();
+    long long total = scan(p, lt, true);  // units
+    const bool each = !any_long && total <= gridDim.x;
+    if (!each) total = scan(p, lt, false);
+    if (threadIdx.x == 0) {
+      whole = each;
+      long long ctas = (int)min(total, 1LL << 30) / min_share;
       if (ctas > gridDim.x) ctas = gridDim.x;
       if (ctas < 1) ctas = 1;
-      share = (carry + ctas - 1) / ctas;
-      if (share < 1) share = 1;
+      share = each ? 1 : max(1LL, (total + ctas - 1) / ctas);
     }
     __syncthreads();
   }
@@ -119,58 +151,114 @@ struct ChunkPlan {
     return 0;
   }
 
+  // Largest k in [0, n) with f(k) <= x, for a rising f with f(0) <= x: the
+  // lanes of each warp (all of them call it) test 32 places at a time.
+  template <typename F>
+  __device__ static int last_not_above(int n, long long x, F f) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, k = lo + lane * step;
+      const uint32_t yes = __ballot_sync(0xffffffffu, lane * step < n && f(k) <= x);
+      const int hit = 31 - __clz(yes);
+      n = min(step, n - hit * step);
+      lo += hit * step;
+    }
+    return lo;
+  }
+
   // The unit that holds cost position x, 0 <= x < prefix[B].
   __device__ ChunkUnit find(const ChunkParams &p, long long x) const {
     ChunkUnit u;
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= x) lo = mid; else hi = mid;
-    }
-    const int tt = ROWS / p.G;
-    request(p, lo, &u.a, &u.n, &u.row0);
-    const int a = u.a, n = u.n;
-    const long long per = cost(a, n, tt);
-    const long long off = x - prefix[lo];
-    u.b = lo;
-    u.g = (int)(off / per);
-    const long long rem = off - u.g * per;
-    int i0 = 0, i1 = (n + tt - 1) / tt;
-    while (i1 - i0 > 1) {
-      const int mid = (i0 + i1) >> 1;
-      if (tiles_before(a, tt, mid) + (long long)mid * COST0 <= rem) i0 = mid; else i1 = mid;
-    }
-    set(u, p, i0);
-    u.at = prefix[lo] + u.g * per + tiles_before(a, tt, i0) + (long long)i0 * COST0 + COST0;
+    const int lt = log_tokens(p);
+    u.b = last_not_above(p.B, x, [&](int b) { return prefix[b]; });
+    request(p, u.b, &u.a, &u.n, &u.row0);
+    const bool by_units = whole;
+    const int a = u.a;
+    const long long per = cost(a, u.n, lt, by_units);
+    long long rem = x - prefix[u.b];
+    u.g = last_not_above(p.Hkv, rem, [&](int g) { return g * per; });
+    rem -= u.g * per;
+    const int i = last_not_above(units(u.n, lt), rem, [&](int k) { return before(a, lt, k, by_units); });
+    set(u, lt, i);
+    u.at = x - rem + before(a, lt, i, by_units) + (by_units ? 0 : COST0);
     return u;
   }
 
+  __device__ static void set(ChunkUnit &u, int lt, int i) {
+    u.i = i;
+    u.tok0 = u.row0 + (i << lt);
+    u.n_tok = min(1 << lt, u.n - (i << lt));
+    u.pos0 = u.a + (i << lt) + 1;
+    u.tiles = (int)(((long long)u.a + (i << lt) + u.n_tok + KT - 1) >> kKt);
+  }
+};
+
+// A CTA's walk through its pieces (every role of a kernel has its own).
+template <typename PLAN, int COST0, int W, int WS>
+struct ChunkWalk {
+  long long x, end, share;
+  ChunkUnit u;
+  bool first, whole;
+
+  // All threads of the block call it; false: no work.
+  __device__ bool start(const ChunkParams &p, const PLAN &plan) {
+    share = plan.share;
+    whole = plan.whole;
+    x = blockIdx.x * share;
+    end = min(plan.prefix[p.B], x + share);
+    first = true;
+    if (x >= end) return false;
+    u = plan.find(p, x);
+    return true;
+  }
+  __device__ int weight(int lt) const { return PLAN::weight(u.n_tok, lt); }
+  // Next piece with a tile; false when the CTA's work is done.
+  __device__ bool next(const ChunkParams &p, ChunkPiece &q) {
+    const int lt = PLAN::log_tokens(p);
+    while (x < end) {
+      if (!first) advance(p, lt);
+      first = false;
+      int t0 = 0, t1 = u.tiles;
+      if (whole) {
+        x = u.at + 1;
+      } else {
+        const int w = weight(lt);
+        auto first_tile = [&](long long y) { return (int)(w == W ? (y + W - 1) / W : (y + WS - 1) / WS); };
+        if (x > u.at) t0 = first_tile(x - u.at);
+        if (end < u.at + (long long)u.tiles * w) t1 = end > u.at ? first_tile(end - u.at) : 0;
+        x = u.at + (long long)u.tiles * w;
+      }
+      if (t0 >= t1) continue;
+      q.u = u;
+      q.t0 = t0;
+      q.t1 = t1;
+      return true;
+    }
+    return false;
+  }
+  // CTAs that hold the pieces of a cut unit: the one of its first tile, and of its last.
+  __device__ int cta_of(const ChunkParams &p, const ChunkUnit &v, int tile) const {
+    return (int)((v.at + (long long)tile * PLAN::weight(v.n_tok, PLAN::log_tokens(p))) / share);
+  }
+
+ private:
   // The unit after u (there is one).
-  __device__ static void advance(ChunkUnit &u, const ChunkParams &p) {
-    const int tt = ROWS / p.G;
-    const long long at = u.at + u.tiles + COST0;
+  __device__ void advance(const ChunkParams &p, int lt) {
+    const long long at = u.at + (whole ? 1 : (long long)u.tiles * weight(lt) + COST0);
     int i = u.i + 1;
-    if (i * tt >= u.n) {
+    if (i << lt >= u.n) {
       i = 0;
       if (++u.g == p.Hkv) {
         u.g = 0;
         do {
           ++u.b;
-          request(p, u.b, &u.a, &u.n, &u.row0);
+          PLAN::request(p, u.b, &u.a, &u.n, &u.row0);
         } while (u.n == 0);
       }
     }
-    set(u, p, i);
+    PLAN::set(u, lt, i);
     u.at = at;
-  }
-
-  __device__ static void set(ChunkUnit &u, const ChunkParams &p, int i) {
-    const int tt = ROWS / p.G;
-    u.i = i;
-    u.tok0 = u.row0 + i * tt;
-    u.n_tok = min(tt, u.n - i * tt);
-    u.pos0 = u.a + i * tt + 1;
-    u.tiles = (int)(((long long)u.a + i * tt + u.n_tok + KT - 1) / KT);
   }
 };
 
@@ -205,35 +293,90 @@ __device__ __forceinline__ void store_out(uint16_t *dst, float4 v) {
   *reinterpret_cast<uint2 *>(dst) = w;
 }
 
-// Pieces c0 .. c1 of a unit into its output rows: a warp per row, four dims
-// per lane, the pieces in CTA order.  All `n_thr` threads (from `tid` 0) of
-// the CTA that finished the last piece call it.
+// Pieces c0 .. c1 of a unit into its output rows, in CTA order.  All `n_thr`
+// threads (from `tid` 0) of the CTA that finished the last piece call it.  A
+// warp takes a row, four dims per lane: lane j holds piece j's maximum and
+// sum, so the weights are known before the outputs are read, eight at a
+// time.  A unit with many rows has few pieces: then a warp takes four rows at once.
+// (One row at a time, a cut unit of 256 rows took 55 us; this way 5.)
 template <typename T>
 __device__ void chunk_merge(const ChunkParams &p, const ChunkUnit &u, int c0, int c1, int n_rows, int tid, int n_thr) {
-  const int lane = tid & 31;
-  for (int r = tid >> 5; r < n_rows; r += n_thr >> 5) {
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0 + lane; c <= c1; c += 32)
-      m = fmaxf(m, __ldcg(p.part + ((int64_t)(2 * c + (c == c0)) * p.part_rows + r) * kPartStride + kHeadDim));
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float *src = p.part + ((int64_t)(2 * c + (c == c0)) * p.part_rows + r) * kPartStride;
-      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + kHeadDim));
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
-      const float w = ex2(ml.x - ms);
-      l = fmaf(w, ml.y, l);
-      o.x = fmaf(w, v.x, o.x);
-      o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z);
-      o.w = fmaf(w, v.w, o.w);
-    }
+  const int lane = tid & 31, warp = tid >> 5, n_warps = n_thr >> 5, n = c1 - c0 + 1;
+  const int64_t slot = (int64_t)p.part_rows * kPartStride;  // floats per partial
+  auto piece = [&](int j, int r) { return p.part + (2 * (c0 + j) + (j == 0)) * slot + (int64_t)r * kPartStride; };
+  auto put = [&](int r, float4 o, float m, float l) {
     const int64_t row = (int64_t)(u.tok0 + r / p.G) * p.Hq + u.g * p.G + r % p.G;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     store_out((T *)p.out + row * kHeadDim + lane * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : ms * kLn2 + logf(l);
+    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+  };
+  auto add = [](float4 &o, float w, float4 v) {
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  };
+  constexpr int R = 4, P = 4;
+  if (n <= P) {
+    for (int r0 = warp * R; r0 < n_rows; r0 += n_warps * R) {
+      float2 ml[R][P];
+      float4 v[R][P];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          ml[i][j] = make_float2(-INFINITY, 0.f);
+          v[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j < n && r0 + i < n_rows) {
+            const float *src = piece(j, r0 + i);
+            ml[i][j] = __ldcg(reinterpret_cast<const float2 *>(src + kHeadDim));
+            v[i][j] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (r0 + i >= n_rows) break;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) m = fmaxf(m, ml[i][j].x);
+        if (m == -INFINITY) m = 0.f;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float w = ex2(ml[i][j].x - m);
+          l = fmaf(w, ml[i][j].y, l);
+          add(o, w, v[i][j]);
+        }
+        put(r0 + i, o, m, l);
+      }
+    }
+    return;
+  }
+  for (int r = warp; r < n_rows; r += n_warps) {
+    float m = -INFINITY;
+    for (int j = lane; j < n; j += 32) m = fmaxf(m, __ldcg(piece(j, r) + kHeadDim));
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (m == -INFINITY) m = 0.f;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      float w = 0.f;
+      if (j0 + lane < n) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(piece(j0 + lane, r) + kHeadDim));
+        w = ex2(ml.x - m);
+        l = fmaf(w, ml.y, l);
+      }
+      const int k = min(32, n - j0);
+      for (int j = 0; j < k; j += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4 *>(piece(j0 + min(j + e, k - 1), r)) + lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) add(o, j + e < k ? __shfl_sync(0xffffffffu, w, (j + e) & 31) : 0.f, v[e]);
+      }
+    }
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    put(r, o, m, l);
   }
 }
 

@@ -30,14 +30,17 @@ namespace mac {
 namespace {
 
 constexpr int kTile = 128;                    // rows of a row tile, keys of a key tile
-constexpr int kCost0 = 2, kMinShare = 4;
+// Costs in quarters of a full unit's key tile.  A unit of at most 128 rows
+// computes half as much per tile, but copies as much; a unit's start and end
+// cost as much as three tiles.
+constexpr int kCost0 = 12, kW = 4, kWs = 3, kMinShare = 16;
 constexpr int kThr = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;  // registers per thread once the roles have split
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThr * 168, "the split comes out of the launch's registers");
 constexpr int kStK = 2, kStV = 3, kNSt = kStK + kStV;  // stages of the K ring and of the V ring
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr float kLazy = 8.f;                  // growth of the maximum (base 2) that moves the reference
-using Plan = ChunkPlan<kChunkRowsBf16, kTile, kCost0>;
+using Plan = ChunkPlan<kChunkRowsBf16, kTile, kCost0, kW, kWs>;
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -48,7 +51,6 @@ struct Control {
   unsigned long long q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, fixed, drain;
   uint32_t tmem;
   int abort, last;
-  long long share, total;
   float2 ml[2][kTile];                        // states of the two groups that share rows
 };
 constexpr int kSmemBytes = (kNSt + 2) * kTileBytes + (int)sizeof(Control);
@@ -184,6 +186,19 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *m, int x
       : "memory");
 }
 
+// 32 bytes: a whole sector at once where dst allows it (rows are 256 bytes
+// apart, so all of a launch's do or none).
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v) {
+  if (((uintptr_t)dst & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+    *(reinterpret_cast<uint4 *>(dst) + 1) = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // ---- packed fp32 -----------------------------------------------------------
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -203,41 +218,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // ---- the pieces of a CTA, as every role walks them ---------------------------
-struct Piece {
-  ChunkUnit u;
-  int t0, t1;       // its key tiles
+struct Piece : ChunkPiece {
   int pair;         // both groups on row tile 0, key tiles in turn
   int end0;         // normal: key tiles of row tile 0 end here (those of row tile 1 at t1)
-  int c0, c1;       // CTAs that hold the unit's pieces
   __device__ int n() const { return t1 - t0; }
   // key tiles of group w
-  __device__ int end(int w) const { return w ? t1 : end0; }
-  __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : max(0, end(w) - t0); }
+  __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : w ? t1 - t0 : max(0, end0 - t0); }
 };
 
-struct Walk {
-  long long x, end, share;
-  ChunkUnit u;
-  bool first;
-  // Next piece with a tile; false when the CTA's work is done.
+struct Walk : ChunkWalk<Plan, kCost0, kW, kWs> {
   __device__ bool next(const ChunkParams &p, Piece &q) {
-    while (x < end) {
-      if (!first) Plan::advance(u, p);
-      first = false;
-      const long long u_end = u.at + u.tiles;
-      q.t0 = (int)max(0LL, x - u.at);
-      q.t1 = (int)min((long long)u.tiles, end - u.at);
-      x = u_end;
-      if (q.t0 >= q.t1) continue;
-      q.u = u;
-      q.pair = u.n_tok * p.G <= kTile;
-      const int tok = kTile / p.G;  // tokens of row tile 0
-      q.end0 = min(q.t1, (u.pos0 + tok - 1 + kTile - 1) / kTile);
-      q.c0 = (int)(u.at / share);
-      q.c1 = (int)((u_end - 1) / share);
-      return true;
-    }
-    return false;
+    if (!ChunkWalk::next(p, q)) return false;
+    q.pair = q.u.n_tok * p.G <= kTile;
+    q.end0 = min(q.t1, (q.u.pos0 + kTile / p.G - 1 + kTile - 1) / kTile);
+    return true;
   }
 };
 
@@ -601,9 +595,9 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     live = live && !wait.dead;
     tc_fence_after();
     const int row = (q.pair ? 0 : w * kTile) + r;
-    const bool whole = q.c0 == q.c1, keep = live && row < n_rows;
-    const int c = blockIdx.x;
-    float *part = p.part + ((int64_t)(2 * c + (c == q.c0 ? 1 : 0)) * p.part_rows + row) * kPartStride;
+    const bool whole = !q.cut(), keep = live && row < n_rows;
+    const int c = blockIdx.x, c0 = whole ? 0 : walk.cta_of(p, q.u, 0), c1 = whole ? 0 : walk.cta_of(p, q.u, q.u.tiles - 1);
+    float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + row) * kPartStride;
     const int64_t out_row = (int64_t)(q.u.tok0 + row / p.G) * p.Hq + q.u.g * p.G + row % p.G;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     // a pair's groups take half of the columns each
@@ -635,13 +629,12 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
       if (whole) {
         uint16_t *dst = (uint16_t *)p.out + out_row * kHeadDim + cc;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint4 v;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(o[j + 1] * inv), "f"(o[j] * inv));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(o[j + 3] * inv), "f"(o[j + 2] * inv));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.z) : "f"(o[j + 5] * inv), "f"(o[j + 4] * inv));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.w) : "f"(o[j + 7] * inv), "f"(o[j + 6] * inv));
-          *reinterpret_cast<uint4 *>(dst + j) = v;
+        for (int j = 0; j < 32; j += 16) {
+          uint32_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[e]) : "f"(o[j + 2 * e + 1] * inv), "f"(o[j + 2 * e] * inv));
+          store32(dst + j, v);
         }
       } else {
 #pragma unroll
@@ -660,15 +653,15 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     if (tid == 0) {
       ct->last = 0;
       if (!*(volatile int *)&ct->abort) {
-        const uint32_t n = q.c1 - q.c0 + 1;
-        ct->last = add_acq_rel(p.count + q.c0, 1) == n - 1;
-        if (ct->last) p.count[q.c0] = 0;  // for the next launch
+        const uint32_t n = c1 - c0 + 1;
+        ct->last = add_acq_rel(p.count + c0, 1) == n - 1;
+        if (ct->last) p.count[c0] = 0;  // for the next launch
       }
     }
     named_sync(2, 256);
     const int last = ct->last;
     named_sync(2, 256);  // read before the next piece writes it
-    if (last) chunk_merge<uint16_t>(p, q.u, q.c0, q.c1, n_rows, tid, 256);
+    if (last) chunk_merge<uint16_t>(p, q.u, c0, c1, n_rows, tid, 256);
   }
   if (status) set_status(p.status, status);
 }
@@ -683,19 +676,10 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
     if (threadIdx.x == 0) set_status(p.status, MAC_DEV_BAD_COPY);
     return;
   }
-  // this CTA's part of the work, the plan made where the stages go
-  Walk walk;
-  {
-    Plan &plan = *reinterpret_cast<Plan *>(smem);
-    plan.build(p, kMinShare);
-    if (plan.any_bad) chunk_bad_requests<uint16_t, Plan>(p);
-    walk.share = plan.share;
-    walk.x = blockIdx.x * plan.share;
-    walk.end = min(plan.prefix[p.B], walk.x + plan.share);
-    walk.first = true;
-    if (walk.x < walk.end) walk.u = plan.find(p, walk.x);
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ct->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (walk.x >= walk.end) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNSt; ++i) {
       mbar_init(smem_addr(&ct->full[i]), 1);
@@ -714,15 +698,21 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
     ct->abort = 0;
     mbar_fence_init();
   }
-  if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ct->tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-  fence_proxy_async();  // the plan was in the stages' memory
+  // this CTA's part of the work, the plan made where the stages go
+  Walk walk;
+  Plan &plan = *reinterpret_cast<Plan *>(smem);
+  plan.build(p, kMinShare);
+  if (plan.any_bad) chunk_bad_requests<uint16_t, Plan>(p);
+  const bool work = walk.start(p, plan);
+  fence_proxy_async();  // copies into the stages come after this
   tc_fence_before();
   block_sync();
   tc_fence_after();
   const uint32_t tmem = ct->tmem;
+  if (!work) {
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    return;
+  }
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     softmax_role<PAGED>(p, ct, walk, tmem);

@@ -14,10 +14,11 @@
 namespace mac {
 namespace {
 
-constexpr int kRows = kChunkRowsF32, kKeys = 64, kThr = 256, kCost0 = 2, kMinShare = 4;
+constexpr int kRows = kChunkRowsF32, kKeys = 64, kThr = 256, kCost0 = 2, kMinShare = 4;  // costs in key tiles
 constexpr int kPad = kHeadDim + 4;   // floats per Q/K row: neighbouring rows start 4 banks apart
 constexpr int kPPad = kKeys + 4;     // floats per row of probabilities
-using Plan = ChunkPlan<kRows, kKeys, kCost0>;
+using Plan = ChunkPlan<kRows, kKeys, kCost0, 1, 1>;
+using Walk = ChunkWalk<Plan, kCost0, 1, 1>;
 
 struct Shared {
   float q[kRows][kPad];
@@ -59,17 +60,14 @@ __global__ void __launch_bounds__(kThr, 2) chunk_kernel(const __grid_constant__ 
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   sm.plan.build(p, kMinShare);
   if (sm.plan.any_bad) chunk_bad_requests<T, Plan>(p);
-  const long long total = sm.plan.prefix[p.B], share = sm.plan.share;
-  long long x = blockIdx.x * share;
-  const long long end = min(total, x + share);
+  Walk walk;
+  if (!walk.start(p, sm.plan)) return;
   uint32_t status = 0;
+  ChunkPiece piece;
 
-  while (x < end) {
-    const ChunkUnit u = sm.plan.find(p, x);
-    const long long u_end = u.at + u.tiles;
-    const int t0 = (int)max(0LL, x - u.at), t1 = (int)min((long long)u.tiles, end - u.at);
-    x = u_end;
-    if (t0 >= t1) continue;
+  while (walk.next(p, piece)) {
+    const ChunkUnit &u = piece.u;
+    const int t0 = piece.t0, t1 = piece.t1;
     const int n_rows = u.n_tok * p.G;
     __syncthreads();  // the last unit's shared memory has been read
     for (int i = tid; i < kRows * (kHeadDim / 4); i += kThr) {
@@ -193,8 +191,7 @@ __global__ void __launch_bounds__(kThr, 2) chunk_kernel(const __grid_constant__ 
       }
     }
     // a whole unit goes out; a piece of one leaves its state
-    const int c0 = (int)(u.at / share), c1 = (int)((u_end - 1) / share);
-    if (c0 == c1) {
+    if (!piece.cut()) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = ty + 16 * i;
@@ -208,7 +205,7 @@ __global__ void __launch_bounds__(kThr, 2) chunk_kernel(const __grid_constant__ 
       }
       continue;
     }
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, c0 = walk.cta_of(p, u, 0), c1 = walk.cta_of(p, u, u.tiles - 1);
     float *part = p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows * kPartStride;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
