@@ -190,16 +190,19 @@ __global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ Ta
 }
 
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t s) {
+  // one thread per request at least; several CTAs once there are rows for
+  // them (one CTA: 4.0 us for 16 rows, launched without the attribute 0.8 us sooner)
+  if (p.T <= 1024) {
+    tables_kernel<<<1, p.B <= 256 ? 256 : (p.B + 31) / 32 * 32, 0, s>>>(p);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
-  // one thread per request at least; several CTAs once there are rows for them
-  const int per = p.B <= 256 ? 256 : (p.B + 31) / 32 * 32;
-  const int ctas = p.T <= 1024 ? 1 : kTablesCluster;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(ctas > 1 ? 1024 : per);
+  cfg.gridDim = dim3(kTablesCluster);
+  cfg.blockDim = dim3(1024);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.x = kTablesCluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -2,6 +2,8 @@
 // new tokens: page tables and slots, the cache writer, chunk attention.
 #pragma once
 
+#include <atomic>
+
 #include "mac_common.cuh"
 
 namespace mac {
@@ -59,6 +61,25 @@ struct ChunkParams {
 constexpr int kChunkGrid = 512;   // most CTAs of a launch
 constexpr int kChunkRowsBf16 = 256, kChunkRowsF32 = 64;  // rows per unit
 constexpr int kMaxTokens = 1 << 24;
+
+// Shared memory limit of a chunk kernel, set once per device; `smem` bytes and
+// at least `regs` registers per thread are what its launch counts on.
+// `done`: the kernel's own flags, one per device.
+using DeviceFlags = std::atomic<bool>[64];
+template <typename K>
+cudaError_t prepare_chunk(K *kernel, DeviceFlags &done, int smem, int regs) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
+      (e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess)
+    return e;
+  if (fa.numRegs < regs) return cudaErrorInvalidValue;
+  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return cudaSuccess;
+}
 
 cudaError_t launch_chunk_f32(const ChunkParams &p, int sms, cudaStream_t s);
 cudaError_t launch_chunk_bf16(const ChunkParams &p, int sms, cudaStream_t s);

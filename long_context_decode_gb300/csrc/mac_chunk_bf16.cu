@@ -757,11 +757,10 @@ bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, 
 
 template <bool PAGED>
 cudaError_t launch(const ChunkParams &p, const Maps &maps, int grid, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  // with fewer registers at launch the split between the roles would wait forever
+  static DeviceFlags done;
+  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED>, done, kSmemBytes, (256 * kRegsSoftmax + 128 * kRegsOther) / kThr);
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, chunk_kernel<PAGED>)) != cudaSuccess) return e;
-  if (fa.numRegs * kThr < 256 * kRegsSoftmax + 128 * kRegsOther) return cudaErrorInvalidValue;  // the split would wait forever
   chunk_kernel<PAGED><<<grid, kThr, kSmemBytes, s>>>(p, maps);
   return cudaGetLastError();
 }

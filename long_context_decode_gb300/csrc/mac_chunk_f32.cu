@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kThr, 2) chunk_kernel(const __grid_constant__ 
 
 cudaError_t launch_chunk_f32(const ChunkParams &p, int sms, cudaStream_t s) {
   static_assert(2 * sizeof(Shared) <= 227 * 1024, "two CTAs per SM");
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+  static DeviceFlags done;
+  const cudaError_t e = prepare_chunk(chunk_kernel<float>, done, sizeof(Shared), 0);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sms < kChunkGrid ? 2 * sms : kChunkGrid;
   chunk_kernel<float><<<grid, kThr, sizeof(Shared), s>>>(p);

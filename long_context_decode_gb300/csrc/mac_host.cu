@@ -166,10 +166,19 @@ int step_grid(const mac_config *c) {
 
 cudaError_t launch_step(StepParams p, const mac_config *c, cudaStream_t s);
 
+// RoPE frequencies as 64-bit fractions of a turn per position.  The table
+// depends on the base alone; a thread keeps the last one (64 calls of pow
+// cost about a microsecond, as much as the rest of a small call).
 void rope_table(const mac_config *c, unsigned long long *f) {
-  for (int j = 0; j < kHeadDim / 2; ++j)
-    f[j] = (unsigned long long)ldexp(
-        pow(c->rope_base, -2.0 * (double)j / (double)c->head_dim) / 6.283185307179586, 64);
+  thread_local double base = 0.0;  // no valid base
+  thread_local unsigned long long table[kHeadDim / 2];
+  if (base != c->rope_base) {
+    for (int j = 0; j < kHeadDim / 2; ++j)
+      table[j] = (unsigned long long)ldexp(
+          pow(c->rope_base, -2.0 * (double)j / (double)c->head_dim) / 6.283185307179586, 64);
+    base = c->rope_base;
+  }
+  memcpy(f, table, sizeof table);
 }
 
 // Common part of every step launch: shapes, constants, K/V, scratch.

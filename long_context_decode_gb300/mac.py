@@ -116,9 +116,7 @@ def _check(code: int, what: str) -> None:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -244,7 +242,7 @@ def _row_stride(t, heads, head_dim) -> int:
     if t is None or isinstance(t, int):
         return heads * head_dim
     st = t.stride()
-    if st[1:] != (head_dim, 1) and not (t.shape[1] == 1 and st[2] == 1):
+    if (st[1] != head_dim and t.shape[1] != 1) or st[2] != 1:
         raise MacError("mac_write_kv: a row's heads must lie end to end")
     return st[0]
 
