@@ -78,6 +78,8 @@ struct TablesShared {
 
 __global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ TablesParams p) {
   __shared__ TablesShared sm;
+  griddep_launch_dependents();
+  griddep_wait();
   const int b = threadIdx.x;
   const bool has = b < p.B;
   uint32_t status = 0;
@@ -190,22 +192,20 @@ __global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ Ta
 }
 
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t s) {
-  // one thread per request at least; several CTAs once there are rows for
-  // them (one CTA: 4.0 us for 16 rows, launched without the attribute 0.8 us sooner)
-  if (p.T <= 1024) {
-    tables_kernel<<<1, p.B <= 256 ? 256 : (p.B + 31) / 32 * 32, 0, s>>>(p);
-    return cudaGetLastError();
-  }
+  // one thread per request at least; several CTAs once there are rows for them
+  if (p.T <= 1024) return launch_dependent(tables_kernel, 1, p.B <= 256 ? 256 : (p.B + 31) / 32 * 32, 0, s, p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kTablesCluster);
   cfg.blockDim = dim3(1024);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kTablesCluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, tables_kernel, p);
 }
 
@@ -244,6 +244,8 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
   __shared__ float cs[TOK][kHeadDim / 2], sn[TOK][kHeadDim / 2];
   __shared__ int64_t place[TOK], step[TOK];          // element of head 0's row in the cache (-1: skip), and between heads
   const int t0 = blockIdx.x * TOK;
+  griddep_launch_dependents();
+  griddep_wait();
   if (threadIdx.x < TOK) {
     const int t = t0 + threadIdx.x;
     int64_t at = -1, st = 0;
@@ -338,10 +340,9 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
 template <typename T, int TOK>
 static cudaError_t launch_write_t(const WriteParams &p, cudaStream_t s) {
   const int grid = (p.T + TOK - 1) / TOK;
-  if (p.rope_mode == MAC_ROPE_HALF) write_kernel<T, MAC_ROPE_HALF, TOK><<<grid, kWriteThreads, 0, s>>>(p);
-  else if (p.rope_mode == MAC_ROPE_INTERLEAVED) write_kernel<T, MAC_ROPE_INTERLEAVED, TOK><<<grid, kWriteThreads, 0, s>>>(p);
-  else write_kernel<T, MAC_ROPE_NONE, TOK><<<grid, kWriteThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (p.rope_mode == MAC_ROPE_HALF) return launch_dependent(write_kernel<T, MAC_ROPE_HALF, TOK>, grid, kWriteThreads, 0, s, p);
+  if (p.rope_mode == MAC_ROPE_INTERLEAVED) return launch_dependent(write_kernel<T, MAC_ROPE_INTERLEAVED, TOK>, grid, kWriteThreads, 0, s, p);
+  return launch_dependent(write_kernel<T, MAC_ROPE_NONE, TOK>, grid, kWriteThreads, 0, s, p);
 }
 
 cudaError_t launch_write(const WriteParams &p, int dtype, cudaStream_t s) {

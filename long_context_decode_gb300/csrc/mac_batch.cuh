@@ -62,6 +62,24 @@ constexpr int kChunkGrid = 512;   // most CTAs of a launch
 constexpr int kChunkRowsBf16 = 256, kChunkRowsF32 = 64;  // rows per unit
 constexpr int kMaxTokens = 1 << 24;
 
+// Launch with programmatic stream serialization: the kernel may start while
+// the previous one on the stream finishes, and waits (griddep_wait) before it
+// touches global memory.
+template <typename K, typename... A>
+cudaError_t launch_dependent(K *kernel, int grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Shared memory limit of a chunk kernel, set once per device; `smem` bytes and
 // at least `regs` registers per thread are what its launch counts on.
 // `done`: the kernel's own flags, one per device.

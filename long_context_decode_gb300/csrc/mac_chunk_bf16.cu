@@ -171,6 +171,9 @@ __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sy
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---- TMA -------------------------------------------------------------------
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -493,6 +496,10 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     const int lim = q.u.pos0 + tok;                         // it attends keys [0, lim)
     const int mine = q.count(w), step = q.pair ? 2 : 1, first = q.t0 + (q.pair ? w : 0);
     const int n_keys = q.u.pos0 + q.u.n_tok - 1;
+    const int n_rows = q.u.n_tok * p.G;
+    // a warp without a row of the unit only keeps the order of the tiles:
+    // its weights are whatever TMEM holds, and so are its rows of O
+    const bool idle = (q.pair ? 0 : w * kTile) + (r & ~31) >= n_rows;
     float m = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f);
     for (int i = 0; i < mine; ++i) {
@@ -508,6 +515,12 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
       if (!wait(&ct->s_full[w], ns & 1)) continue;
       ++ns;
       tc_fence_after();
+      if (idle) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ct->p_full[w]));
+        continue;
+      }
       float s[kTile];
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
@@ -574,7 +587,6 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     }
     // ---- the piece's rows
     float l = l2.x + l2.y;
-    const int n_rows = q.u.n_tok * p.G;
     bool live = true;
     for (int x = 0; x < 2; ++x)
       if (q.count(x) > 0) {  // group 0's products end before group 1's
@@ -670,9 +682,11 @@ template <bool PAGED>
 __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
+  griddep_launch_dependents();
   uint8_t *qbuf = smem + kNSt * kTileBytes;
   Control *ct = reinterpret_cast<Control *>(qbuf + 2 * kTileBytes);
   if (smem_addr(smem) & 1023) {  // the swizzled tiles need it; dynamic shared memory starts there
+    griddep_wait();
     if (threadIdx.x == 0) set_status(p.status, MAC_DEV_BAD_COPY);
     return;
   }
@@ -698,6 +712,12 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
     ct->abort = 0;
     mbar_fence_init();
   }
+  if (threadIdx.x == 32) {
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+  }
+  griddep_wait();  // from here on the previous kernel's writes are read
   // this CTA's part of the work, the plan made where the stages go
   Walk walk;
   Plan &plan = *reinterpret_cast<Plan *>(smem);
@@ -761,8 +781,7 @@ cudaError_t launch(const ChunkParams &p, const Maps &maps, int grid, cudaStream_
   static DeviceFlags done;
   const cudaError_t e = prepare_chunk(chunk_kernel<PAGED>, done, kSmemBytes, (256 * kRegsSoftmax + 128 * kRegsOther) / kThr);
   if (e != cudaSuccess) return e;
-  chunk_kernel<PAGED><<<grid, kThr, kSmemBytes, s>>>(p, maps);
-  return cudaGetLastError();
+  return launch_dependent(chunk_kernel<PAGED>, grid, kThr, kSmemBytes, s, p, maps);
 }
 
 }  // namespace

@@ -58,6 +58,8 @@ __global__ void __launch_bounds__(kThr, 2) chunk_kernel(const __grid_constant__ 
   extern __shared__ __align__(16) uint8_t raw[];
   Shared &sm = *reinterpret_cast<Shared *>(raw);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  griddep_launch_dependents();
+  griddep_wait();
   sm.plan.build(p, kMinShare);
   if (sm.plan.any_bad) chunk_bad_requests<T, Plan>(p);
   Walk walk;
@@ -237,8 +239,7 @@ cudaError_t launch_chunk_f32(const ChunkParams &p, int sms, cudaStream_t s) {
   const cudaError_t e = prepare_chunk(chunk_kernel<float>, done, sizeof(Shared), 0);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sms < kChunkGrid ? 2 * sms : kChunkGrid;
-  chunk_kernel<float><<<grid, kThr, sizeof(Shared), s>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(chunk_kernel<float>, grid, kThr, sizeof(Shared), s, p);
 }
 
 }  // namespace mac

@@ -495,6 +495,34 @@ def test_chunk_infinite_and_nan_rows_stay_in_their_row():
     assert b.out[13, 3].isnan().all() and not clean.isnan().any()
 
 
+@pytest.mark.parametrize("new", [1, 200])
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("use", [0, 1])
+def test_chunk_wait_runs_out(use, paged, new):
+    # the copy of key stage use `use` is never issued: the wait for it gives up after 2^16 cycles, the
+    # launch reports it and returns, and one on a fresh workspace is clean and right
+    b = Batch([3000, 1500], [new, new], 8, 2, BF16, paged, seed=9)
+    mac.mac_test_wait_budget(1 << 16, use)
+    b.run()
+    torch.cuda.synchronize()
+    assert b.status() & mac.MAC_DEV_WAIT_TIMEOUT
+    b.ws = workspace(b.cfg, b.T)
+    b.run()
+    assert b.status() == 0
+    b.check()
+
+
+def test_chunk_output_on_any_16_byte_boundary():
+    b = Batch([50], [70], 8, 2, BF16, True, seed=6)
+    b.run()
+    ref = b.out.clone()
+    raw = torch.zeros(b.out.numel() + 64, device=DEV, dtype=BF16)
+    for off in (8, 24):  # rows start at odd multiples of 16 bytes
+        b.out = raw[off:off + ref.numel()].view(ref.shape)
+        b.run()
+        assert torch.equal(ref, b.out)
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
