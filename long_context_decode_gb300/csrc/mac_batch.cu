@@ -10,13 +10,19 @@ namespace mac {
 // ---------------------------------------------------------------------------
 // One cluster.  Every CTA loads the B <= 1024 requests (one per thread) and
 // scans them itself, so the requests' pages, rows and places in the stack of
-// free pages are in its shared memory after two block scans; then pages and
-// rows, flattened over the requests, are dealt to all threads of the cluster
-// (a binary search over the B + 1 starts finds an item's request).  Two
-// cluster barriers order what the arguments may alias and what depends on
+// free pages are in its shared memory after two block scans; then pages,
+// flattened over the requests, are dealt to all threads of the cluster
+// (a binary search over the B + 1 starts finds an item's request).  The
+// cluster barrier orders what the arguments may alias and what depends on
 // the stack: inputs are read before any output is written, and pages given
 // back are on the stack before any page is taken.
-constexpr int kTablesCluster = 8;
+// Rows: in a single CTA (up to kOneCta rows) a thread finds each row's page
+// for itself (16 requests of one token: 3.2 us).  In the cluster they go a
+// page's worth at a time: a lane finds its page (the search, the load of the
+// id), then the warp writes the rows of its 32 pages, two pages at once.  A
+// search per row, 100 instructions, made 104K rows of 128 requests take 18.3
+// us on the cluster's eight SMs; this way the call takes 12 (and the 16 requests 4.4).
+constexpr int kTablesCluster = 8, kOneCta = 1024;
 
 __device__ __forceinline__ void cluster_sync_all() {
   __syncwarp();  // aligned: the warp arrives as one
@@ -72,8 +78,8 @@ struct TablesShared {
   int base[kMaxUnits];             // tokens it holds before the new ones
   int take[kMaxUnits + 1];         // new pages asked for before it
   int give[kMaxUnits + 1];         // pages given back before it
+  int block[kMaxUnits + 1];        // pages that new tokens before its own lie on
   long long tot[32][3];
-  int n_free;                      // stack entries once the resets' pages are back
 };
 
 __global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ TablesParams p) {
@@ -125,16 +131,18 @@ __global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ Ta
   const long long n_avail = n_free + n_back;
   const bool in = want > 0 && v[0] <= p.T && (need == 0 || v[1] <= n_avail);
   if (want > 0 && !in) status |= MAC_DEV_NO_ROOM;
-  long long w[3] = {in ? want : 0, in ? need : 0, 0};
-  const long long rows = w[0], pages = w[1];
+  long long w[3] = {in ? want : 0, in ? need : 0, in ? (base + want - 1) / kPage - base / kPage + 1 : 0};
+  const long long rows = w[0], pages = w[1], blocks = w[2];
   block_scan3(w, sm.tot);
   if (has) {
     sm.row[b] = (int)(w[0] - rows);
     sm.take[b] = (int)(w[1] - pages);
+    sm.block[b] = (int)(w[2] - blocks);
     sm.base[b] = (int)base;
     if (b == p.B - 1) {
       sm.row[p.B] = (int)w[0];
       sm.take[p.B] = (int)w[1];
+      sm.block[p.B] = (int)w[2];
     }
   }
   __syncthreads();
@@ -168,32 +176,58 @@ __global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ Ta
     }
     p.table[(int64_t)r * p.max_pages + (sm.base[r] + kPage - 1) / kPage + (x - sm.take[r])] = id;
   }
-  for (int t = first; t < p.T; t += stride) {
-    int32_t pos = 0;
-    int64_t slot = -1;
-    if (t < n_rows) {
-      const int r = request_of(sm.row, p.B, t);
-      const int at = sm.base[r] + (t - sm.row[r]);  // position - 1
-      pos = at + 1;
-      if (!p.paged) {
-        slot = (int64_t)r * p.capacity + at;
-      } else {
-        const int k = at / kPage, held = (sm.base[r] + kPage - 1) / kPage;
-        const int32_t id = k < held ? p.table[(int64_t)r * p.max_pages + k]
-                                    : __ldcg(p.free_pages + (n_avail - 1 - (sm.take[r] + k - held)));
-        if (id >= 0 && id < p.n_pages) slot = (int64_t)id * kPage + at % kPage;
-        else status |= MAC_DEV_BAD_PAGE;
+  // page k of request r's tokens, or r itself for a contiguous cache: the slot of its first token
+  auto first_slot = [&](int r, int k) -> long long {
+    if (!p.paged) return (int64_t)r * p.capacity + (int64_t)k * kPage;
+    const int held = (sm.base[r] + kPage - 1) / kPage;
+    const int32_t id = k < held ? p.table[(int64_t)r * p.max_pages + k] : __ldcg(p.free_pages + (n_avail - 1 - (sm.take[r] + k - held)));
+    if (id >= 0 && id < p.n_pages) return (int64_t)id * kPage;
+    status |= MAC_DEV_BAD_PAGE;
+    return -1;
+  };
+  const int n_blocks = p.T > kOneCta ? sm.block[p.B] : 0, lane = threadIdx.x & 31;
+  if (p.T <= kOneCta)
+    for (int t = first; t < n_rows; t += stride) {
+      const int r = request_of(sm.row, p.B, t), at = sm.base[r] + (t - sm.row[r]);
+      const long long s0 = first_slot(r, at / kPage);
+      p.pos[t] = at + 1;
+      p.slot[t] = s0 < 0 ? -1 : s0 + at % kPage;
+    }
+  for (int x0 = first - lane; x0 < n_blocks; x0 += stride) {
+    const int x = x0 + lane;
+    int lo = 0, hi = 0, shift = 0;  // positions - 1 of this page's new tokens; row of a token minus its position
+    long long slot0 = -1;           // slot of the page's first token
+    if (x < n_blocks) {
+      const int r = request_of(sm.block, p.B, x);
+      const int base = sm.base[r], k = base / kPage + (x - sm.block[r]), n = sm.row[r + 1] - sm.row[r];
+      lo = max(base, k * kPage);
+      hi = (int)min((long long)base + n, (long long)(k + 1) * kPage);
+      shift = sm.row[r] - base;
+      slot0 = first_slot(r, k);
+    }
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const int src = 2 * i + (lane >> 4);
+      const int l = __shfl_sync(0xffffffffu, lo, src), h = __shfl_sync(0xffffffffu, hi, src);
+      const int sh = __shfl_sync(0xffffffffu, shift, src);
+      const long long s0 = __shfl_sync(0xffffffffu, slot0, src);
+      const int at = l / kPage * kPage + (lane & 15);
+      if (at >= l && at < h) {
+        p.pos[at + sh] = at + 1;
+        p.slot[at + sh] = s0 < 0 ? -1 : s0 + (lane & 15);
       }
     }
-    p.pos[t] = pos;
-    p.slot[t] = slot;
+  }
+  for (long long t = (long long)n_rows + first; t < p.T; t += stride) {
+    p.pos[t] = 0;
+    p.slot[t] = -1;
   }
   if (status) set_status(p.status, status);
 }
 
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t s) {
-  // one thread per request at least; several CTAs once there are rows for them
-  if (p.T <= 1024) return launch_dependent(tables_kernel, 1, p.B <= 256 ? 256 : (p.B + 31) / 32 * 32, 0, s, p);
+  // one thread per request at least
+  if (p.T <= kOneCta) return launch_dependent(tables_kernel, 1, p.B <= 256 ? 256 : (p.B + 31) / 32 * 32, 0, s, p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kTablesCluster);
   cfg.blockDim = dim3(1024);
@@ -218,7 +252,7 @@ cudaError_t launch_tables(const TablesParams &p, cudaStream_t s) {
 // (j, j + 64 for half-split pairs; neighbours for interleaved ones), and
 // walks the row's heads with the sines and cosines in registers.  Bound by
 // HBM: every element is read and written once.
-constexpr int kWriteThreads = 256;
+constexpr int kWriteThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ uint4 pack16(const float *f);
@@ -346,10 +380,13 @@ static cudaError_t launch_write_t(const WriteParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_write(const WriteParams &p, int dtype, cudaStream_t s) {
-  // few rows: one per CTA, so that a row's heads are all in flight at once
-  const bool few = p.T <= 608;
-  if (dtype == MAC_F32) return few ? launch_write_t<float, 1>(p, s) : launch_write_t<float, 4>(p, s);
-  return few ? launch_write_t<uint16_t, 1>(p, s) : launch_write_t<uint16_t, 4>(p, s);
+  // Eight heads of a row in flight: two bf16 rows per CTA, one fp32 row.
+  // 8679 rows of 32 + 2 x 8 bf16 heads: 34.8 us (6.1 TB/s); with four rows of
+  // 256 threads 36.4, two rows of 256 threads 39.5, one row of 256 threads 53.
+  // 2160 rows of 32 + 2 x 4 fp32 heads: 15.9 us; two rows per CTA 17.0.
+  // Few rows leave SMs idle either way and take one CTA each.
+  if (dtype == MAC_F32) return launch_write_t<float, 1>(p, s);
+  return p.T <= 608 ? launch_write_t<uint16_t, 1>(p, s) : launch_write_t<uint16_t, 2>(p, s);
 }
 
 }  // namespace mac
