@@ -51,24 +51,25 @@ struct ChunkParams {
   void *out;
   float *lse;                     // or null
   uint32_t *status;
-  uint32_t *count;                // [kChunkGrid] finished pieces of the split unit that starts in a CTA
+  int4 *notes;                    // [kChunkGrid] the cut unit whose first tile a CTA holds
   float *part;                    // [2 * grid][part_rows][kPartStride]
   int part_rows;
   long long wait_limit;           // bf16 kernel: cycles a wait may take
   int withhold;                   // run-out test only: the stage use (>= 0) whose copy is never issued
 };
 
-constexpr int kChunkGrid = 512;   // most CTAs of a launch
-constexpr int kChunkRowsBf16 = 256, kChunkRowsF32 = 64;  // rows per unit
+constexpr int kChunkGrid = 256;   // most CTAs of a launch (one per SM)
+constexpr int kChunkRowsBf16 = 256, kChunkRowsF32 = 128;  // rows per unit
 constexpr int kMaxTokens = 1 << 24;
+constexpr int kChunkShort = 8;    // key tiles of a short unit
 
 // Launch with programmatic stream serialization: the kernel may start while
 // the previous one on the stream finishes, and waits (griddep_wait) before it
 // touches global memory.
 template <typename K, typename... A>
-cudaError_t launch_dependent(K *kernel, int grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
+cudaError_t launch_dependent(K *kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -99,8 +100,11 @@ cudaError_t prepare_chunk(K *kernel, DeviceFlags &done, int smem, int regs) {
   return cudaSuccess;
 }
 
-cudaError_t launch_chunk_f32(const ChunkParams &p, int sms, cudaStream_t s);
-cudaError_t launch_chunk_bf16(const ChunkParams &p, int sms, cudaStream_t s);
+// The attention kernels, `grid` CTAs (one per SM).
+cudaError_t launch_chunk_f32(const ChunkParams &p, int grid, cudaStream_t s);
+cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s);
+// The cut units of an attention launch of `grid` CTAs.
+cudaError_t launch_chunk_merge(const ChunkParams &p, int grid, bool f32, cudaStream_t s);
 
 cudaError_t launch_tables(const TablesParams &p, cudaStream_t s);
 cudaError_t launch_write(const WriteParams &p, int dtype, cudaStream_t s);

@@ -7,9 +7,9 @@
 // positions [c share, (c+1) share): any number of whole units and at most
 // two cut ones, so rows of very different lengths, one long row and many
 // short ones all spread evenly.  A cut unit's pieces leave (o, max, sum)
-// partials; the CTA that finishes the last one merges them in CTA order, so
-// results do not depend on timing.  When there is a CTA for every unit and
-// all are short (kShort tiles), each CTA takes one whole unit instead: a
+// partials and the CTA of its first tile a note of them; a second kernel
+// merges them in CTA order, so results do not depend on timing.  When there is a CTA for every unit and
+// all are short (kChunkShort tiles), each CTA takes one whole unit instead: a
 // merge would cost more than the cut saves.
 #pragma once
 
@@ -46,7 +46,6 @@ struct ChunkPiece {
 template <int ROWS, int KT, int COST0, int W, int WS>
 struct ChunkPlan {
   static constexpr int kKt = log2i(KT);
-  static constexpr int kShort = 8;
 
   long long prefix[kMaxUnits + 1];  // cost of all requests before b, all KV heads
   long long warp_tot[32];
@@ -88,7 +87,7 @@ struct ChunkPlan {
       if (b < p.B) {
         int a, n;
         if (request(p, b, &a, &n)) any_bad = 1;
-        if (((long long)a + n + KT - 1) >> kKt > kShort && n > 0) any_long = 1;
+        if (((long long)a + n + KT - 1) >> kKt > kChunkShort && n > 0) any_long = 1;
         v = cost(a, n, lt, by_units) * p.Hkv;
       }
       for (int d = 1; d < 32; d <<= 1) {
@@ -279,11 +278,9 @@ __device__ void chunk_bad_requests(const ChunkParams &p) {
   }
 }
 
-__device__ __forceinline__ uint32_t add_acq_rel(uint32_t *p, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
+// The note of a cut unit: its first token, KV head, rows, and the CTA of its
+// last tile.  Every CTA leaves one (no rows: none of its units is cut after it).
+__device__ __forceinline__ void leave_note(const ChunkParams &p, int4 note) { p.notes[blockIdx.x] = note; }
 
 __device__ __forceinline__ void store_out(float *dst, float4 v) { *reinterpret_cast<float4 *>(dst) = v; }
 __device__ __forceinline__ void store_out(uint16_t *dst, float4 v) {
@@ -291,93 +288,6 @@ __device__ __forceinline__ void store_out(uint16_t *dst, float4 v) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v.y), "f"(v.x));
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v.w), "f"(v.z));
   *reinterpret_cast<uint2 *>(dst) = w;
-}
-
-// Pieces c0 .. c1 of a unit into its output rows, in CTA order.  All `n_thr`
-// threads (from `tid` 0) of the CTA that finished the last piece call it.  A
-// warp takes a row, four dims per lane: lane j holds piece j's maximum and
-// sum, so the weights are known before the outputs are read, eight at a
-// time.  A unit with many rows has few pieces: then a warp takes four rows at once.
-// (One row at a time, a cut unit of 256 rows took 55 us; this way 5.)
-template <typename T>
-__device__ void chunk_merge(const ChunkParams &p, const ChunkUnit &u, int c0, int c1, int n_rows, int tid, int n_thr) {
-  const int lane = tid & 31, warp = tid >> 5, n_warps = n_thr >> 5, n = c1 - c0 + 1;
-  const int64_t slot = (int64_t)p.part_rows * kPartStride;  // floats per partial
-  auto piece = [&](int j, int r) { return p.part + (2 * (c0 + j) + (j == 0)) * slot + (int64_t)r * kPartStride; };
-  auto put = [&](int r, float4 o, float m, float l) {
-    const int64_t row = (int64_t)(u.tok0 + r / p.G) * p.Hq + u.g * p.G + r % p.G;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store_out((T *)p.out + row * kHeadDim + lane * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-  };
-  auto add = [](float4 &o, float w, float4 v) {
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
-  };
-  constexpr int R = 4, P = 4;
-  if (n <= P) {
-    for (int r0 = warp * R; r0 < n_rows; r0 += n_warps * R) {
-      float2 ml[R][P];
-      float4 v[R][P];
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          ml[i][j] = make_float2(-INFINITY, 0.f);
-          v[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j < n && r0 + i < n_rows) {
-            const float *src = piece(j, r0 + i);
-            ml[i][j] = __ldcg(reinterpret_cast<const float2 *>(src + kHeadDim));
-            v[i][j] = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
-          }
-        }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (r0 + i >= n_rows) break;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < P; ++j) m = fmaxf(m, ml[i][j].x);
-        if (m == -INFINITY) m = 0.f;
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float w = ex2(ml[i][j].x - m);
-          l = fmaf(w, ml[i][j].y, l);
-          add(o, w, v[i][j]);
-        }
-        put(r0 + i, o, m, l);
-      }
-    }
-    return;
-  }
-  for (int r = warp; r < n_rows; r += n_warps) {
-    float m = -INFINITY;
-    for (int j = lane; j < n; j += 32) m = fmaxf(m, __ldcg(piece(j, r) + kHeadDim));
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (m == -INFINITY) m = 0.f;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      float w = 0.f;
-      if (j0 + lane < n) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(piece(j0 + lane, r) + kHeadDim));
-        w = ex2(ml.x - m);
-        l = fmaf(w, ml.y, l);
-      }
-      const int k = min(32, n - j0);
-      for (int j = 0; j < k; j += 8) {
-        float4 v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4 *>(piece(j0 + min(j + e, k - 1), r)) + lane);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) add(o, j + e < k ? __shfl_sync(0xffffffffu, w, (j + e) & 31) : 0.f, v[e]);
-      }
-    }
-    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    put(r, o, m, l);
-  }
 }
 
 #endif  // __CUDACC__

@@ -24,7 +24,7 @@
 #include <cuda.h>
 #include <math.h>
 
-#include "mac_chunk.cuh"
+#include "mac_tc.cuh"
 
 namespace mac {
 namespace {
@@ -50,34 +50,14 @@ struct Control {
   unsigned long long full[kNSt], empty[kNSt];
   unsigned long long q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, fixed, drain;
   uint32_t tmem;
-  int abort, last;
+  int abort;
   float2 ml[2][kTile];                        // states of the two groups that share rows
 };
 constexpr int kSmemBytes = (kNSt + 2) * kTileBytes + (int)sizeof(Control);
 static_assert(kSmemBytes <= (int)kMaxSmem, "shared memory of a CTA");
 static_assert(sizeof(Plan) <= kNSt * kTileBytes, "the plan is made where the stages go");
 
-// ---- tcgen05 ---------------------------------------------------------------
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// One arrival on `bar` once the products issued so far have ended.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
-// Shared memory descriptor, 128-byte swizzle: address / 16 and leading byte
-// offset / 16 (bit 16) in the low word; in the high one, stride byte offset
-// / 16 (groups of eight rows are 1024 bytes apart), version 1 (bit 46) and
-// swizzle mode 2 (bit 61).  A tile is two halves of 64 columns, 128-byte rows: Q and K
-// step 16 columns along a row (32 bytes); V, whose columns are the
-// product's N, steps 16 rows (2048 bytes), its halves a leading offset apart.
-constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
-
+// ---- products ----------------------------------------------------------------
 // The products of a tile, D[128 x 128] (+)= A B in eight steps of depth 16;
 // bf16 inputs, fp32 sums.  a, b: low words of shared memory descriptors (a of
 // tc_values: TMEM).  The whole warp runs them and one lane issues: with its
@@ -116,60 +96,6 @@ __device__ __forceinline__ void tc_values(uint32_t d, uint32_t a, uint32_t b, ui
       "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(add)
       : "memory");
 }
-// Two arrivals at once (the stages of a key and a value tile).
-__device__ __forceinline__ void tc_commit2(uint32_t bar0, uint32_t bar1) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(bar0), "r"(bar1)
-      : "memory");
-}
-
-// Instruction descriptor: fp32 sums (bit 4), bf16 A and B (bits 7, 10), B
-// along N where asked (bit 16), N/8 from bit 17, M/16 from bit 24.
-__host__ __device__ constexpr uint32_t idesc(bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
-}
-
-__device__ __forceinline__ void tc_ld32(float *r, uint32_t addr) {
-  uint32_t *u = reinterpret_cast<uint32_t *>(r);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
-        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *u) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]),
-      "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
-      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
-      "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
-      "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *u) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15};" ::"r"(u[0]),
-      "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
-      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
-      : "memory");
-}
-// Registers that a load has filled are used after the wait only.
-__device__ __forceinline__ void tc_loaded32(float *r) {
-  asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-               "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]));
-  asm volatile("" : "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
-               "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
-}
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // ---- TMA -------------------------------------------------------------------
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -202,24 +128,6 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *v) {
   }
 }
 
-// ---- packed fp32 -----------------------------------------------------------
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // ---- the pieces of a CTA, as every role walks them ---------------------------
 struct Piece : ChunkPiece {
   int pair;         // both groups on row tile 0, key tiles in turn
@@ -238,34 +146,6 @@ struct Walk : ChunkWalk<Plan, kCost0, kW, kWs> {
   }
 };
 
-// Waits that every role makes, a whole warp at a time.  After one has run out (or another role's
-// has: ct->abort) all return false at once; the roles then walk through
-// their loops without touching anything, so that their barriers still meet.
-struct Waiter {
-  Control *ct;
-  uint32_t *status;
-  long long limit;
-  bool dead;
-  __device__ __forceinline__ bool operator()(unsigned long long *bar, uint32_t parity) {
-    if (!__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity)) || dead) return slow(smem_addr(bar), parity);
-    return true;
-  }
-  __device__ __forceinline__ bool slow(uint32_t bar, uint32_t parity) {
-    if (dead) return false;
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, (volatile int *)&ct->abort, limit))) {
-      dead = true;
-      *(volatile int *)&ct->abort = 1;
-      set_status(status, MAC_DEV_WAIT_TIMEOUT);
-      return false;
-    }
-    return true;
-  }
-};
-
-__device__ __forceinline__ bool bad_page(const ChunkParams &p, int id) {
-  return id < 0 || id >= p.kv.n_pages;
-}
-
 // ---- copies (warps 8 and 11) ---------------------------------------------------
 // One ring's copies: key or value tiles into stages st0 .. st0 + NST - 1, and
 // (K) the Q tiles.  A paged tile is 8 pages of two 64-column halves, one copy each.
@@ -274,7 +154,7 @@ __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stage
   constexpr int NST = IS_K ? kStK : kStV, ST0 = IS_K ? 0 : kStK;
   const CUtensorMap *map = IS_K ? &maps.k : &maps.v;
   const int lane = threadIdx.x & 31, half = lane >> 3 & 1, pg = lane & 7;
-  Waiter wait{ct, p.status, p.wait_limit, false};
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
   int use = 0;       // stage uses so far
   uint32_t nq = 0;   // Q tiles so far
   Piece q = {};
@@ -342,7 +222,7 @@ struct RingPos {
 };
 
 __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, Control *ct, Walk walk, uint32_t tmem) {
-  Waiter wait{ct, p.status, p.wait_limit, false};
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
   RingPos k = {0, 0}, v = {kStK, 0};
   uint32_t q_phase = 0, fix_phase = 0, p_phase[2] = {0, 0};
   Piece q = {};
@@ -352,13 +232,13 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
   };
   auto scores = [&](uint32_t w, uint32_t qa) {  // S_w = Q K^T, then tell group w
     if (wait.dead) return;
-    tc_scores(tmem + w * kTile, desc_lo(qa, 16), desc_lo(addr(k.st), 16), idesc(false), smem_addr(&ct->s_full[w]));
+    tc_scores(tmem + w * kTile, desc_lo(qa, 16), desc_lo(addr(k.st), 16), idesc(kTile, false), smem_addr(&ct->s_full[w]));
   };
   auto values = [&](uint32_t w, uint32_t add) {  // O_w (+)= P_w V, once P_w is there (and O_w rescaled)
     wait(&ct->p_full[w], w ? p_phase[1] : p_phase[0]);
     tc_fence_after();
     if (wait.dead) return;
-    tc_values(tmem + 2 * kTile + w * kTile, tmem + w * kTile, desc_lo(addr(v.st), kTileBytes / 2), idesc(true), add);
+    tc_values(tmem + 2 * kTile + w * kTile, tmem + w * kTile, desc_lo(addr(v.st), kTileBytes / 2), idesc(kTile, true), add);
     if (w) p_phase[1] ^= 1; else p_phase[0] ^= 1;
   };
   auto keys_ready = [&] { wait(&ct->full[k.st], k.phase); };
@@ -454,7 +334,7 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
 // the rows are cleared in shared memory before the product reads them.
 __device__ void fix_role(const ChunkParams &p, uint8_t *stages, Control *ct, Walk walk) {
   const int lane = threadIdx.x & 31;
-  Waiter wait{ct, p.status, p.wait_limit, false};
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
   int uv = 0;
   uint32_t nt = 0;
   Piece q = {};
@@ -485,9 +365,10 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
   const int tid = threadIdx.x, w = tid >> 7, r = tid & 127, lane = tid & 31;
   const uint32_t lanes = (uint32_t)((tid >> 5) & 3) << 21;  // this warp's 32 TMEM lanes
   const uint32_t s_at = tmem + w * kTile + lanes;
-  Waiter wait{ct, p.status, p.wait_limit, false};
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
   const float scale = p.q_scale, lazy = kLazy / scale;
   const float2 scale2 = make_float2(scale, scale);
+  int4 note = make_int4(0, 0, 0, 0);
   uint32_t ns = 0, no = 0;  // scores taken; parity of each group's next output
   uint32_t status = 0;
   Piece q = {};
@@ -657,24 +538,13 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
       if (!whole) *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(m * scale, l);  // base 2, as the merge takes it
       else if (p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : m * scale * kLn2 + logf(l);
     }
-    if (q.pair || !whole) {
+    if (q.pair) {
       tc_fence_before();
-      named_sync(2, 256);  // O has been read by both groups, the partial is complete
+      named_sync(2, 256);  // O has been read by both groups
     }
-    if (whole) continue;
-    if (tid == 0) {
-      ct->last = 0;
-      if (!*(volatile int *)&ct->abort) {
-        const uint32_t n = c1 - c0 + 1;
-        ct->last = add_acq_rel(p.count + c0, 1) == n - 1;
-        if (ct->last) p.count[c0] = 0;  // for the next launch
-      }
-    }
-    named_sync(2, 256);
-    const int last = ct->last;
-    named_sync(2, 256);  // read before the next piece writes it
-    if (last) chunk_merge<uint16_t>(p, q.u, c0, c1, n_rows, tid, 256);
+    if (!whole && c == c0 && live) note = make_int4(q.u.tok0, q.u.g, n_rows, c1);
   }
+  if (tid == 0) leave_note(p, wait.dead ? make_int4(0, 0, 0, 0) : note);
   if (status) set_status(p.status, status);
 }
 
@@ -687,7 +557,10 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   Control *ct = reinterpret_cast<Control *>(qbuf + 2 * kTileBytes);
   if (smem_addr(smem) & 1023) {  // the swizzled tiles need it; dynamic shared memory starts there
     griddep_wait();
-    if (threadIdx.x == 0) set_status(p.status, MAC_DEV_BAD_COPY);
+    if (threadIdx.x == 0) {
+      set_status(p.status, MAC_DEV_BAD_COPY);
+      leave_note(p, make_int4(0, 0, 0, 0));
+    }
     return;
   }
   if (warp == 9) {
@@ -730,6 +603,7 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = ct->tmem;
   if (!work) {
+    if (threadIdx.x == 0) leave_note(p, make_int4(0, 0, 0, 0));
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
@@ -786,7 +660,7 @@ cudaError_t launch(const ChunkParams &p, const Maps &maps, int grid, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_chunk_bf16(const ChunkParams &p, int sms, cudaStream_t s) {
+cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s) {
   Maps maps;
   const cuuint64_t row = kHeadDim * 2;
   const cuuint32_t G = p.G;
@@ -810,7 +684,6 @@ cudaError_t launch_chunk_bf16(const ChunkParams &p, int sms, cudaStream_t s) {
       if (!encode(m, base, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
   }
-  const int grid = sms < kChunkGrid ? sms : kChunkGrid;
   return p.kv.paged ? launch<true>(p, maps, grid, s) : launch<false>(p, maps, grid, s);
 }
 

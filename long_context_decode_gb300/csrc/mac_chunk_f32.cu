@@ -1,264 +1,468 @@
-// mac_chunk_f32.cu -- chunk attention in fp32 on the CUDA cores.
+// mac_chunk_f32.cu -- chunk attention in fp32 on the bf16 tensor cores.
 //
-// For a row with rotated query q at position p:
-//   x_j = q . k_j log2(e)/sqrt(d), j <= p;  m = max x_j;
-//   l = sum 2^(x_j - m);  out = sum 2^(x_j - m) v_j / l;  lse = m ln 2 + ln l
-// in one pass over the keys with a running m, l and o.  (The tensor cores
-// keep no more than 10 bits of an fp32 factor.)
+// For a row with rotated query q at position p, over key tiles of 64:
+//   x_j = q . k_j log2(e)/sqrt(d), j <= p;  m the running maximum;
+//   l = sum 2^(x_j - m);  o = sum 2^(x_j - m) v_j;
+//   out = o / l;  lse = m ln 2 + ln l.
+// An fp32 number is the exact sum of three bf16 ones, a = a0 + a1 + a2, eight
+// bits of its significand each (cut off, not rounded), so a product is
+//   a b = a0 b0 + (a0 b1 + a1 b0) + (a1 b1 + a0 b2 + a2 b0) + terms below 2^-23 |a b|:
+// six bf16 products for one in fp32, each exact in the tensor cores' fp32
+// sums.  The small ones are summed first, so that what the sums cut off is
+// small against the result, and a tile's P V is added to o in registers
+// (rounded to nearest): errors do not pile up over a long context.
 //
-// A CTA of 256 threads takes 16 I packed rows and keys 64 at a time; a thread
-// owns I rows (ty + 16 i) x 4 keys (tx + 16 j) of the scores and the same
-// rows x 8 dims of the output.  The multiply-adds are packed in pairs
-// (fma.rn.f32x2: over even and odd dims for the scores, over two dims for
-// the output, the weights stored twice), which halves the instructions; a
-// loop of them alone reaches 102 multiply-adds per cycle and SM, this kernel
-// 63 (4096 tokens, 8 heads: 945 us, 36 TFLOP/s) with shared memory 73% busy.
-// The weights overwrite K and are made and used by the same half warp.  Two
-// CTAs share an SM: one computes while the other waits for its copies or
-// takes its maxima.  (One CTA with 8 x 4 microtiles: 870 us, but 35 us
-// instead of 25 for seven rows; two of 128 threads with 8 x 4: 982 us.)
-//   I = 4: 64 rows, for batches of many rows per request (the multiply-adds
-//          are the bound); I = 1: 16 rows, for a few (reading shared memory is).
+// One CTA per SM, 128 packed rows (token-major, the G heads of a token
+// together), sixteen warps (registers are split by four warps):
+//   warps 0-3    softmax, o: a thread owns a row;
+//   warps 4-7, 8-11  read K, and V (and Q together), split them and store the
+//                parts, swizzled, in shared memory (rows that are not there
+//                as zeros), each warp the rows of one page of a tile;
+//   warp 12      issues the products: S (64 columns of TMEM) from shared
+//                memory, P V (128 columns) with P's parts (96) in TMEM.
+// The roles' loops are kept short: unrolled in full they did not fit the
+// instruction cache together, and its misses took two thirds of the time.
+// S of the next tile is made while the softmax runs; K is stored while the
+// products of the last weights run, V while the scores do.  A tile's 72
+// products (S 48 of 48 cycles, bound by reading Q from shared memory, P V 24
+// of 64) are the bound: MEASURED
 #include <math.h>
 
-#include "mac_chunk.cuh"
+#include "mac_tc.cuh"
 
 namespace mac {
 namespace {
 
-constexpr int kKeys = 64, kThr = 256, kCost0 = 1, kMinShare = 2;  // costs in key tiles
-constexpr int kPad = kHeadDim + 4;   // floats per Q/K row: neighbouring rows start 4 banks apart
-constexpr int kPPad = 2 * kKeys + 4; // floats per row of doubled weights
-template <int I>
-using Plan = ChunkPlan<16 * I, kKeys, kCost0, 1, 1>;
+constexpr int kRows = kChunkRowsF32, kKeys = 64;
+constexpr int kCost0 = 3, kMinShare = 4;            // costs in key tiles
+constexpr int kThr = 512, kConv = kKeys / kPage;    // threads; warps that split K (V): one for each page of a tile
+constexpr int kRegsLaunch = 128, kRegsSoft = 232, kRegsSplit = 104, kRegsMma = 72;  // registers per thread
+static_assert(kRegsSoft + 2 * kRegsSplit + kRegsMma <= 4 * kRegsLaunch && kThr * kRegsLaunch <= 65536, "the split comes out of the launch's registers");
+constexpr int kQPart = kRows * kHeadDim * 2, kKvPart = kKeys * kHeadDim * 2;  // bytes of one bf16 part of a tile
+constexpr uint32_t kColS = 0, kColS1 = 64, kColP = 128, kColO = 256;  // TMEM columns: S twice, P, P V
+using Plan = ChunkPlan<kRows, kKeys, kCost0, 1, 1>;
+using Walk = ChunkWalk<Plan, kCost0, 1, 1>;
 
-template <int I>
-struct Shared {
-  float q[16 * I][kPad];
-  union {
-    float k[kKeys][kPad];
-    float pr[16 * I][kPPad];  // once the scores are done with K
-  };
-  float v[kKeys][kHeadDim];
-  Plan<I> plan;
-  int last;
+struct Control {
+  unsigned long long k_full, k_free, v_full, v_free, q_full, q_free;
+  unsigned long long s_full, s_free[2], p_full, o_full, o_free, drain;
+  uint32_t tmem;
+  int abort;
 };
+constexpr int kSmemBytes = 3 * kQPart + 6 * kKvPart + (int)sizeof(Control);
+static_assert(kSmemBytes <= (int)kMaxSmem && sizeof(Plan) <= 6 * kKvPart, "shared memory of a CTA");
 
-__device__ __forceinline__ void fma2(float2 &d, float2 a, float2 b) {
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
-      "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "+f"(d.x), "+f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+// ---- products ----------------------------------------------------------------
+// 128 x 64 (+)= 128 x 128 . 128 x 64 of one part of Q and one of K; 128 x 128
+// (+)= 128 x 64 . 64 x 128 of one part of P and one of V.  The whole warp runs
+// them and one lane issues.
+__device__ __forceinline__ void tc_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t add) {
+#define MAC_S(AO, BO, P)                                                                                                  \
+  "add.u32 x, %1, " AO ";\n\tadd.u32 y, %2, " BO ";\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"                    \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " P ";\n\t"
+  asm volatile(
+      "{\n\t.reg .pred q, t, e;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t" MAC_S("0", "0", "q") MAC_S("2", "2", "t") MAC_S("4", "4", "t") MAC_S("6", "6", "t")
+          MAC_S("1024", "512", "t") MAC_S("1026", "514", "t") MAC_S("1028", "516", "t") MAC_S("1030", "518", "t") "}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc(kKeys, false)), "n"(kDescHi), "r"(add)
+      : "memory");
+#undef MAC_S
+}
+static_assert(kQPart / 2 >> 4 == 1024 && kKvPart / 2 >> 4 == 512, "second halves of Q and K tiles");
+__device__ __forceinline__ void tc_values(uint32_t d, uint32_t a, uint32_t b, uint32_t add) {
+#define MAC_V(AO, BO, P)                                                                     \
+  "add.u32 x, %1, " AO ";\n\tadd.u32 y, %2, " BO ";\n\tmov.b64 b, {y, %4};\n\t"              \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, " P ";\n\t"
+  asm volatile(
+      "{\n\t.reg .pred q, t, e;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t" MAC_V("0", "0", "q") MAC_V("8", "128", "t") MAC_V("16", "256", "t")
+          MAC_V("24", "384", "t") "}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc(kHeadDim, true)), "n"(kDescHi), "r"(add)
+      : "memory");
+#undef MAC_V
 }
 
-// 16 bytes into shared memory, asynchronously; zeros where !ok.
-__device__ __forceinline__ void copy16(float *dst, const float *src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+// (part of the first factor | part of the second << 2), 4 bits each, smallest products first: 2 0, 0 2, 1 1, 1 0, 0 1, 0 0
+constexpr uint32_t kPairs = 0x2 | 0x8 << 4 | 0x5 << 8 | 0x1 << 12 | 0x4 << 16 | 0x0 << 20;
 
-// Row of token `key` (0-based) of request b, KV head g; -1: on no page.
-__device__ __forceinline__ int64_t cache_row(const ChunkParams &p, int b, int g, int key) {
-  if (!p.kv.paged) return ((int64_t)b * p.Hkv + g) * p.kv.capacity + key;
-  const int id = p.kv.page_table[(int64_t)b * p.kv.max_pages + key / kPage];
-  if (id < 0 || id >= p.kv.n_pages) return -1;
-  return ((int64_t)id * p.Hkv + g) * kPage + key % kPage;
-}
-
-template <int I>
-__global__ void __launch_bounds__(kThr, 2) chunk_kernel(const __grid_constant__ ChunkParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Shared<I> &sm = *reinterpret_cast<Shared<I> *>(raw);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  griddep_launch_dependents();
-  griddep_wait();
-  sm.plan.build(p, kMinShare);
-  if (sm.plan.any_bad) chunk_bad_requests<float, Plan<I>>(p);
-  ChunkWalk<Plan<I>, kCost0, 1, 1> walk;
-  if (!walk.start(p, sm.plan)) return;
-  uint32_t status = 0;
-  ChunkPiece piece;
-
-  while (walk.next(p, piece)) {
-    const ChunkUnit &u = piece.u;
-    const int t0 = piece.t0, t1 = piece.t1;
-    const int n_rows = u.n_tok * p.G, n_keys = u.pos0 + u.n_tok - 1;
-    // a warp copies whole rows
-    auto copy_tile = [&](float *dst, int pitch, const void *src, int t) {
-#pragma unroll
-      for (int i = 0; i < kKeys / 8; ++i) {
-        const int r = i * 8 + (tid >> 5), c = (tid & 31) * 4, key = t * kKeys + r;
-        int64_t row = -1;
-        if (key < n_keys) {
-          row = cache_row(p, u.b, u.g, key);
-          if (row < 0) status |= MAC_DEV_BAD_PAGE;
+__device__ void mma_role(const ChunkParams &p, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, Control *ct, Walk walk, uint32_t tmem) {
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
+  uint32_t nt = 0, ns = 0, nq = 0;  // tiles of P V, of S, and Q tiles so far
+  const uint32_t qd = desc_lo(qbuf, 16), kd = desc_lo(kbuf, 16), vd = desc_lo(vbuf, kKvPart / 2);
+  ChunkPiece q = {};
+  while (walk.next(p, q)) {
+    const int n = q.t1 - q.t0;
+    wait(&ct->q_full, nq & 1);
+    ++nq;
+    for (int j = 0; j <= n; ++j) {
+      if (j < n) {  // S of tile j
+        const uint32_t buf = ns & 1;
+        wait(&ct->k_full, ns & 1);
+        wait(&ct->s_free[buf], ((ns >> 1) + 1) & 1);
+        ++ns;
+        tc_fence_after();
+        if (!wait.dead) {
+#pragma unroll 1
+          for (uint32_t i = 0; i < 6; ++i) {
+            const uint32_t w = kPairs >> 4 * i;
+            tc_scores(tmem + kColS + buf * kColS1, qd + (w & 3) * (kQPart >> 4), kd + (w >> 2 & 3) * (kKvPart >> 4), i);
+          }
+          tc_commit(smem_addr(&ct->s_full));
+          tc_commit(smem_addr(&ct->k_free));
+          if (j + 1 == n) tc_commit(smem_addr(&ct->q_free));
         }
-        copy16(dst + r * pitch + c, (const float *)src + (row < 0 ? 0 : row) * kHeadDim + c, row >= 0);
+      }
+      if (j > 0) {  // P V of tile j - 1
+        wait(&ct->v_full, nt & 1);
+        wait(&ct->p_full, nt & 1);
+        wait(&ct->o_free, (nt + 1) & 1);
+        ++nt;
+        tc_fence_after();
+        if (!wait.dead) {
+#pragma unroll 1
+          for (uint32_t i = 0; i < 6; ++i) {
+            const uint32_t w = kPairs >> 4 * i;
+            tc_values(tmem + kColO, tmem + kColP + (w & 3) * (kKeys / 2), vd + (w >> 2 & 3) * (kKvPart >> 4), i);
+          }
+          tc_commit(smem_addr(&ct->o_full));
+          tc_commit(smem_addr(&ct->v_free));
+        }
+      }
+    }
+  }
+  // every product has ended before the CTA gives its memory up
+  const int dummy = 0;
+  tc_commit(smem_addr(&ct->drain));
+  if (!mbar_wait_bounded(smem_addr(&ct->drain), 0, (volatile int *)&dummy, p.wait_limit)) {
+    *(volatile int *)&ct->abort = 1;
+    set_status(p.status, MAC_DEV_WAIT_TIMEOUT);
+  }
+}
+
+// ---- splitting (warps 4-11) -----------------------------------------------------
+// Two neighbours' next parts, packed, and what is left of them.  FIRST: what
+// an infinity leaves is nothing (its first part says it all).
+template <bool FIRST>
+__device__ __forceinline__ uint32_t split2(float &x, float &y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  x -= __uint_as_float(a & 0xffff0000u);
+  y -= __uint_as_float(b & 0xffff0000u);
+  if (FIRST) {
+    x = x == x ? x : 0.f;
+    y = y == y ? y : 0.f;
+  }
+  return __byte_perm(a, b, 0x7632);
+}
+
+// Four floats of row r, columns 4 lane .. 4 lane + 3, as three bf16 parts into a tile of ROWS rows.
+template <int ROWS>
+__device__ __forceinline__ void put_parts(uint8_t *tile, int r, int lane, float4 f) {
+  const int half = lane >> 4, chunk = lane >> 1 & 7;
+  uint8_t *dst = tile + half * (ROWS * 128) + r * 128 + ((chunk ^ (r & 7)) << 4) + (lane & 1) * 8;
+  constexpr int kPart = ROWS * kHeadDim * 2;
+  uint2 w = make_uint2(split2<true>(f.x, f.y), split2<true>(f.z, f.w));
+  *reinterpret_cast<uint2 *>(dst) = w;
+  w = make_uint2(split2<false>(f.x, f.y), split2<false>(f.z, f.w));
+  *reinterpret_cast<uint2 *>(dst + kPart) = w;
+  w = make_uint2(split2<false>(f.x, f.y), split2<false>(f.z, f.w));
+  *reinterpret_cast<uint2 *>(dst + 2 * kPart) = w;
+}
+
+template <bool PAGED>
+__device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, uint8_t *vbuf, Control *ct, Walk walk) {
+  const int lane = threadIdx.x & 31, me_q = (threadIdx.x >> 5) - 4, me = me_q & (kConv - 1);
+  const bool is_k = me_q < kConv;  // one copy of the code for both: see above
+  const float *src = (const float *)(is_k ? p.kv.k : p.kv.v) + lane * 4;
+  unsigned long long *full = is_k ? &ct->k_full : &ct->v_full, *free = is_k ? &ct->k_free : &ct->v_free;
+  uint8_t *tile = is_k ? kbuf : vbuf;
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
+  uint32_t nt = 0, nq = 0;  // tiles and Q tiles so far
+  ChunkPiece q = {};
+  auto hand_over = [&](unsigned long long *bar) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(bar));
+  };
+  while (walk.next(p, q)) {
+    const int n_rows = q.u.n_tok * p.G, n_keys = q.u.pos0 + q.u.n_tok - 1;
+    // this warp's 16 rows of tile t: the element of their first one (-1: no
+    // page), and how many of them are keys of the unit
+    auto at = [&](int t) -> int64_t {
+      if (!PAGED) return (((int64_t)q.u.b * p.Hkv + q.u.g) * p.kv.capacity + t * kKeys + me * kPage) * kHeadDim;
+      const int k = t * (kKeys / kPage) + me;
+      const int id = t < q.t1 && (int64_t)k * kPage < n_keys ? p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + k] : -1;
+      return id >= 0 && id < p.kv.n_pages ? ((int64_t)id * p.Hkv + q.u.g) * kPage * kHeadDim : -1;
+    };
+    float4 f[kPage];
+    auto load = [&](int t, int64_t first) {
+      const int n = first < 0 ? 0 : n_keys - (t * kKeys + me * kPage);
+      const float *row = src + (first < 0 ? 0 : first);
+#pragma unroll
+      for (int i = 0; i < kPage; ++i) {
+        f[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) f[i] = *reinterpret_cast<const float4 *>(row + i * kHeadDim);
       }
     };
-    __syncthreads();  // the last unit's shared memory has been read
-#pragma unroll
-    for (int i = 0; i < 2 * I; ++i) {
-      const int r = i * 8 + (tid >> 5), c = (tid & 31) * 4;
-      const bool ok = r < n_rows;
-      const int64_t row = ok ? (int64_t)(u.tok0 + r / p.G) * p.Hq + u.g * p.G + r % p.G : 0;
-      copy16(&sm.q[r][c], (const float *)p.q + row * kHeadDim + c, ok);
-    }
-    copy_tile(&sm.k[0][0], kPad, p.kv.k, t0);
-    copy_commit();
-    copy_tile(&sm.v[0][0], kHeadDim, p.kv.v, t0);
-    copy_commit();
-    float m[I], l[I];
-    float2 o[I][4];
-    int lim[I];  // keys [0, lim) are the row's
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      lim[i] = u.pos0 + (ty + 16 * i) / p.G;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = make_float2(0.f, 0.f);
-    }
-    for (int t = t0; t < t1; ++t) {
-      const int key0 = t * kKeys;
-      copy_wait<1>();  // K (and Q); V may be on its way
-      __syncthreads();
-      float2 s2[I][4];
-#pragma unroll
-      for (int i = 0; i < I; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
+    load(q.t0, at(q.t0));
+    if (wait(&ct->q_free, (nq + 1) & 1)) {
+      ++nq;
 #pragma unroll 2
-      for (int d = 0; d < kHeadDim; d += 4) {
-        float4 b[4];
+      for (int r = me_q; r < kRows; r += 2 * kConv) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n_rows)
+          x = *reinterpret_cast<const float4 *>((const float *)p.q + ((int64_t)(q.u.tok0 + r / p.G) * p.Hq + q.u.g * p.G + r % p.G) * kHeadDim + lane * 4);
+        put_parts<kRows>(qbuf, r, lane, x);
+      }
+      hand_over(&ct->q_full);
+    }
+    int64_t next = at(q.t0 + 1);  // a tile ahead of its use
+    for (int t = q.t0; t < q.t1; ++t, ++nt) {
+      if (wait(free, (nt + 1) & 1)) {
+#pragma unroll 1
+        for (int c = 0; c < kPage; c += 4) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][d]);
+          for (int i = 0; i < 4; ++i) put_parts<kKeys>(tile, me * kPage + c + i, lane, f[i]);
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-          const float4 a = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][d]);
+          for (int i = 0; i < kPage - 4; ++i) f[i] = f[i + 4];
+        }
+        hand_over(full);
+      }
+      // only now: the fence of the hand-over would wait for loads in flight
+      if (t + 1 < q.t1) load(t + 1, next);
+      next = at(t + 2);
+    }
+  }
+}
+
+// ---- softmax and output (warps 0-3) -----------------------------------------------
+template <bool PAGED>
+__device__ void row_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t tmem) {
+  const int tid = threadIdx.x, r = tid, lane = tid & 31;
+  const uint32_t lanes = (uint32_t)(tid >> 5) << 21;  // this warp's 32 TMEM lanes
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
+  const float scale = p.q_scale;
+  uint32_t nt = 0, status = 0;
+  int4 note = make_int4(0, 0, 0, 0);
+  ChunkPiece q = {};
+  auto arrive = [&](unsigned long long *bar) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(bar));
+  };
+  while (walk.next(p, q)) {
+    const int lim = q.u.pos0 + r / p.G;  // keys [0, lim) are the row's
+    const int n = q.t1 - q.t0, n_rows = q.u.n_tok * p.G, n_keys = q.u.pos0 + q.u.n_tok - 1;
+    const bool idle = (r & ~31) >= n_rows;  // no row of this warp: it only keeps the order of the tiles
+    float m = -INFINITY, l = 0.f, o[kHeadDim];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) fma2(s2[i][j], make_float2(a.x, a.y), make_float2(b[j].x, b[j].y));
+    for (int c = 0; c < kHeadDim; ++c) o[c] = 0.f;
+    // o = o corr + P V of the last tile
+    auto accumulate = [&](float corr) {
+      tc_fence_after();
+      if (!idle) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) fma2(s2[i][j], make_float2(a.z, a.w), make_float2(b[j].z, b[j].w));
+        for (int c = 0; c < kHeadDim; c += 16) {
+          float v[16];
+          tc_ld16(v, tmem + kColO + c + lanes);
+          tc_wait_ld();
+          tc_loaded16(v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[c + j] = fmaf(o[c + j], corr, v[j]);
         }
       }
-      __syncthreads();  // K has been read
-      bool on[4];  // keys tx + 16 j lie on page j of the tile
-#pragma unroll
-      for (int j = 0; j < 4; ++j) on[j] = key0 + 16 * j < n_keys && cache_row(p, u.b, u.g, key0 + 16 * j) >= 0;
-#pragma unroll
-      for (int i = 0; i < I; ++i) {
-        float s[4], mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[j] = on[j] && key0 + tx + 16 * j < lim[i] ? (s2[i][j].x + s2[i][j].y) * p.q_scale : -INFINITY;
-          mx = fmaxf(mx, s[j]);
+      arrive(&ct->o_free);
+    };
+    {
+      float corr_before = 0.f;
+      for (int j = 0; j < n; ++j, ++nt) {
+        const int key0 = (q.t0 + j) * kKeys;
+        uint32_t gone = 0;  // pages of the tile that do not exist
+        if (PAGED) {
+          bool bad = false;
+          const int pg = key0 / kPage + lane;
+          if (lane < kKeys / kPage && pg * kPage < n_keys) {
+            const int id = p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + pg];
+            bad = id < 0 || id >= p.kv.n_pages;
+          }
+          gone = __ballot_sync(0xffffffffu, bad);
+          if (gone) status |= MAC_DEV_BAD_PAGE;
         }
+        if (!wait(&ct->s_full, nt & 1)) continue;
+        tc_fence_after();
+        const uint32_t s_at = tmem + kColS + (nt & 1) * kColS1 + lanes;
+        const int left = key0 + kKeys > q.u.pos0 ? lim - key0 : kKeys;  // keys of the tile that the row attends
+        // 32 scores at a time, those that are not the row's at -inf
+        auto scores = [&](float *s, int c0) {
+          tc_ld32(s, s_at + c0);
+          tc_wait_ld();
+          tc_loaded32(s);
+          if (left < c0 + 32) {
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float mn = fmaxf(m[i], mx), ms = mn == -INFINITY ? 0.f : mn;
-        const float corr = ex2(m[i] - ms);
-        m[i] = mn;
-        float sum = 0.f;
+            for (int c = 0; c < 32; ++c) s[c] = c0 + c < left ? s[c] : -INFINITY;
+          }
+          if (PAGED && gone) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[j] = ex2(s[j] - ms);
-          sum += s[j];
-          *reinterpret_cast<float2 *>(&sm.pr[ty + 16 * i][2 * (tx + 16 * j)]) = make_float2(s[j], s[j]);
+            for (int c = 0; c < 32; ++c) s[c] = (gone >> ((c0 + c) / kPage)) & 1 ? -INFINITY : s[c];
+          }
+        };
+        float corr = 0.f, ms = 0.f;
+        if (!idle) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += 32) {
+            float s[32];
+            scores(s, c0);
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 32; c += 4)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          }
+          // the maximum in base 2, rounded once: every weight and the lse go by the same number
+          const float mn = fmaxf(m, top * scale);
+          ms = mn == -INFINITY ? 0.f : mn;
+          corr = ex2(m - ms);
+          m = mn;
+          l *= corr;
         }
-        l[i] = l[i] * corr + sum;  // this lane's keys; the lanes are summed at the end
+        if (j > 0 && !wait(&ct->o_full, (nt - 1) & 1)) continue;  // the last tile's P has been read
+        tc_fence_after();
+        if (!idle) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += 32) {
+            float s[32];
+            scores(s, c0);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          o[i][j].x *= corr;
-          o[i][j].y *= corr;
-        }
-      }
-      copy_wait<0>();   // V
-      __syncthreads();  // (and the half warp's weights)
-#pragma unroll 4
-      for (int k = 0; k < kKeys; k += 2) {
-        float4 v[2][2];
+            for (int c = 0; c < 32; c += 2) {
+              const float2 x = fma2(make_float2(s[c], s[c + 1]), make_float2(scale, scale), make_float2(-ms, -ms));
+              s[c] = ex2(x.x);
+              s[c + 1] = ex2(x.y);
+              acc[c >> 1 & 1] = add2(acc[c >> 1 & 1], make_float2(s[c], s[c + 1]));
+            }
+            acc[0] = add2(acc[0], acc[1]);
+            l += acc[0].x + acc[0].y;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v[e][0] = *reinterpret_cast<const float4 *>(&sm.v[k + e][tx * 4]);
-          v[e][1] = *reinterpret_cast<const float4 *>(&sm.v[k + e][64 + tx * 4]);
-        }
+            for (int part = 0; part < 3; ++part) {
+              uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-          const float4 w = *reinterpret_cast<const float4 *>(&sm.pr[ty + 16 * i][2 * k]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 w2 = e ? make_float2(w.z, w.w) : make_float2(w.x, w.y);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              fma2(o[i][2 * h], w2, make_float2(v[e][h].x, v[e][h].y));
-              fma2(o[i][2 * h + 1], w2, make_float2(v[e][h].z, v[e][h].w));
+              for (int c = 0; c < 32; c += 2) {
+                const uint32_t a = __float_as_uint(s[c]), b = __float_as_uint(s[c + 1]);
+                w[c / 2] = __byte_perm(a, b, 0x7632);
+                s[c] -= __uint_as_float(a & 0xffff0000u);
+                s[c + 1] -= __uint_as_float(b & 0xffff0000u);
+              }
+              tc_st16(tmem + kColP + part * (kKeys / 2) + c0 / 2 + lanes, w);
             }
           }
+          tc_wait_st();
         }
+        arrive(&ct->p_full);
+        if (lane == 0) mbar_arrive(smem_addr(&ct->s_free[nt & 1]));
+        if (j > 0) accumulate(corr_before);
+        corr_before = corr;
       }
-      __syncthreads();  // V and the weights have been read
-      if (t + 1 < t1) {
-        copy_tile(&sm.k[0][0], kPad, p.kv.k, t + 1);
-        copy_commit();
-        copy_tile(&sm.v[0][0], kHeadDim, p.kv.v, t + 1);
-        copy_commit();
-      }
+      if (wait(&ct->o_full, (nt - 1) & 1)) accumulate(corr_before);
     }
+    // ---- the piece's rows: a whole unit goes out, a piece of one leaves its state
+    const bool whole = !q.cut(), keep = !wait.dead && r < n_rows;
+    const int c = blockIdx.x, c0 = whole ? c : walk.cta_of(p, q.u, 0), c1 = whole ? c : walk.cta_of(p, q.u, q.u.tiles - 1);
+    if (keep) {
+      const int64_t row = (int64_t)(q.u.tok0 + r / p.G) * p.Hq + q.u.g * p.G + r % p.G;
+      const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + r) * kPartStride;
+      float *dst = (whole ? (float *)p.out + row * kHeadDim : part);
 #pragma unroll
-    for (int i = 0; i < I; ++i)
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-    // a whole unit goes out; a piece of one leaves its state
-    const bool whole = !piece.cut();
-    const int c = blockIdx.x, c0 = whole ? c : walk.cta_of(p, u, 0), c1 = whole ? c : walk.cta_of(p, u, u.tiles - 1);
-    float *part = p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows * kPartStride;
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int r = ty + 16 * i;
-      if (r >= n_rows) continue;
-      const int64_t row = (int64_t)(u.tok0 + r / p.G) * p.Hq + u.g * p.G + r % p.G;
-      const float f = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
-      float *dst = whole ? (float *)p.out + row * kHeadDim : part + r * kPartStride;
-      store_out(dst + tx * 4, make_float4(o[i][0].x * f, o[i][0].y * f, o[i][1].x * f, o[i][1].y * f));
-      store_out(dst + 64 + tx * 4, make_float4(o[i][2].x * f, o[i][2].y * f, o[i][3].x * f, o[i][3].y * f));
-      if (tx == 0) {
-        if (!whole) store_out(dst + kHeadDim, make_float4(m[i], l[i], 0.f, 0.f));
-        else if (p.lse) p.lse[row] = l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
-      }
+      for (int e = 0; e < kHeadDim; e += 4) store_out(dst + e, make_float4(o[e] * f, o[e + 1] * f, o[e + 2] * f, o[e + 3] * f));
+      if (!whole) *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(m, l);
+      else if (p.lse) p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
-    if (whole) continue;
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t n = c1 - c0 + 1, old = add_acq_rel(p.count + c0, 1);
-      sm.last = old == n - 1;
-      if (sm.last) p.count[c0] = 0;  // for the next launch
-    }
-    __syncthreads();
-    if (sm.last) chunk_merge<float>(p, u, c0, c1, n_rows, tid, kThr);
+    if (!whole && c == c0) note = make_int4(q.u.tok0, q.u.g, n_rows, c1);
   }
+  if (tid == 0) leave_note(p, wait.dead ? make_int4(0, 0, 0, 0) : note);
   if (status) set_status(p.status, status);
 }
 
-template <int I>
-cudaError_t launch(const ChunkParams &p, int ctas, cudaStream_t s) {
+template <bool PAGED>
+__global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  griddep_launch_dependents();
+  uint8_t *qbuf = smem, *kbuf = smem + 3 * kQPart, *vbuf = kbuf + 3 * kKvPart;
+  Control *ct = reinterpret_cast<Control *>(vbuf + 3 * kKvPart);
+  if (smem_addr(smem) & 1023) {  // the swizzled tiles need it; dynamic shared memory starts there
+    griddep_wait();
+    if (threadIdx.x == 0) {
+      set_status(p.status, MAC_DEV_BAD_COPY);
+      leave_note(p, make_int4(0, 0, 0, 0));
+    }
+    return;
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ct->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(smem_addr(&ct->k_full), kConv);
+    mbar_init(smem_addr(&ct->v_full), kConv);
+    mbar_init(smem_addr(&ct->q_full), 2 * kConv);
+    mbar_init(smem_addr(&ct->k_free), 1);
+    mbar_init(smem_addr(&ct->v_free), 1);
+    mbar_init(smem_addr(&ct->q_free), 1);
+    mbar_init(smem_addr(&ct->s_full), 1);
+    mbar_init(smem_addr(&ct->o_full), 1);
+    mbar_init(smem_addr(&ct->drain), 1);
+    mbar_init(smem_addr(&ct->s_free[0]), 4);
+    mbar_init(smem_addr(&ct->s_free[1]), 4);
+    mbar_init(smem_addr(&ct->p_full), 4);
+    mbar_init(smem_addr(&ct->o_free), 4);
+    ct->abort = 0;
+    mbar_fence_init();
+  }
+  griddep_wait();  // from here on the previous kernel's writes are read
+  Walk walk;
+  Plan &plan = *reinterpret_cast<Plan *>(kbuf);  // made where the K and V tiles go
+  plan.build(p, kMinShare);
+  if (plan.any_bad) chunk_bad_requests<float, Plan>(p);
+  const bool work = walk.start(p, plan);
+  tc_fence_before();
+  block_sync();
+  tc_fence_after();
+  const uint32_t tmem = ct->tmem;
+  if (!work) {
+    if (threadIdx.x == 0) leave_note(p, make_int4(0, 0, 0, 0));
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    return;
+  }
+  if (warp < 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    row_role<PAGED>(p, ct, walk, tmem);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSplit));
+    split_role<PAGED>(p, qbuf, kbuf, vbuf, ct, walk);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (warp == 12) mma_role(p, smem_addr(qbuf), smem_addr(kbuf), smem_addr(vbuf), ct, walk, tmem);
+  }
+  tc_fence_before();
+  block_sync();
+  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <bool PAGED>
+cudaError_t launch(const ChunkParams &p, int grid, cudaStream_t s) {
+  // with fewer registers at launch the split between the roles would wait forever
   static DeviceFlags done;
-  const cudaError_t e = prepare_chunk(chunk_kernel<I>, done, sizeof(Shared<I>), 0);
+  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED>, done, kSmemBytes, kRegsLaunch);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_kernel<I>, ctas < kChunkGrid ? ctas : kChunkGrid, kThr, sizeof(Shared<I>), s, p);
+  return launch_dependent(chunk_kernel<PAGED>, grid, kThr, kSmemBytes, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_f32(const ChunkParams &p, int sms, cudaStream_t s) {
-  static_assert(2 * (sizeof(Shared<4>) + 1024) <= 228 * 1024, "two CTAs per SM");
-  static_assert(kChunkRowsF32 == 16 * 4, "rows of the largest unit");
-  // the lengths are on the device: go by the mean rows per request and KV head
-  return (int64_t)p.T * p.G <= 16LL * p.B ? launch<1>(p, 2 * sms, s) : launch<4>(p, 2 * sms, s);
+cudaError_t launch_chunk_f32(const ChunkParams &p, int grid, cudaStream_t s) {
+  return p.kv.paged ? launch<true>(p, grid, s) : launch<false>(p, grid, s);
 }
 
 }  // namespace mac

@@ -241,10 +241,10 @@ AppendParams append_params(const mac_config *c, const mac_ring_layout &R, uint8_
 }
 
 // Chunk workspace: the status word first (where mac_last_status reads a
-// scratch's), the counts of the split units' pieces, then the pieces.  The
-// counts start at zero and a clean launch leaves them so.
+// scratch's), the CTAs' notes of cut units, then the units' pieces.  Only
+// the status word outlives a call.
 struct ChunkLayout {
-  size_t ctl, count, part, total;
+  size_t ctl, notes, part, total;
   int part_rows;
 };
 
@@ -256,7 +256,7 @@ ChunkLayout chunk_layout(const mac_config *c, int32_t n_tokens) {
   L.part_rows = (int)(rows < unit ? rows : unit);
   size_t off = 0;
   L.ctl = off;    off = align_up(off + 64 * 4, 256);
-  L.count = off;  off = align_up(off + (size_t)kChunkGrid * 4, 256);
+  L.notes = off;  off = align_up(off + (size_t)kChunkGrid * sizeof(int4), 256);
   L.part = off;   off = align_up(off + 2 * (size_t)kChunkGrid * L.part_rows * kPartStride * 4, 256);
   L.total = off;
   return L;
@@ -716,7 +716,7 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
   p.out = out;
   p.lse = lse;
   p.status = (uint32_t *)(ws + L.ctl);
-  p.count = (uint32_t *)(ws + L.count);
+  p.notes = (int4 *)(ws + L.notes);
   p.part = (float *)(ws + L.part);
   p.part_rows = L.part_rows;
   p.wait_limit = t_wait_limit > 0 ? t_wait_limit : kWaitLimit;
@@ -727,8 +727,15 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
   const int sms = num_sms();
   if (sms < 1) return MAC_ERR_CUDA;
   note_launch(s, nullptr, nullptr);
-  const cudaError_t e = cfg->dtype == MAC_F32 ? launch_chunk_f32(p, sms, s) : launch_chunk_bf16(p, sms, s);
-  return e == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+  const bool f32 = cfg->dtype == MAC_F32;
+  const int grid = sms < kChunkGrid ? sms : kChunkGrid;
+  if ((f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s)) != cudaSuccess) return MAC_ERR_CUDA;
+  // No unit can be cut when a CTA is there for each and none is long,
+  // whatever the lengths on the device: then nothing needs merging.
+  const int64_t unit_tokens = (f32 ? kChunkRowsF32 : kChunkRowsBf16) / p.G, tile = f32 ? 64 : 128;
+  const int64_t units = (n_tokens / unit_tokens + p.B) * p.Hkv;
+  if (units <= grid && p.max_len <= kChunkShort * tile) return MAC_OK;
+  return launch_chunk_merge(p, grid, f32, s) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
 }
 
 int mac_join_aux(void *ring_ws, void *stream_main) {
