@@ -298,11 +298,12 @@ int mac_write_kv(const mac_config *cfg, void *chunk_ws, const void *q, int64_t q
  * to attend gets out 0 and lse -inf, and so does every row of a request
  * whose seq_len is below n or beyond the cache (MAC_DEV_BAD_SEQ_LEN);
  * a request whose rows q_start puts outside [0, n_tokens] is passed over
- * (MAC_DEV_BAD_SEQ_LEN).  Cache rows beyond seq_len may hold anything.  K
- * and V of positions up to seq_len must be finite where a row of the same
- * call does not attend them yet: they meet its zero weights.  dtype bf16:
+ * (MAC_DEV_BAD_SEQ_LEN).  Cache rows beyond seq_len may hold anything.  V of
+ * positions up to seq_len must be finite even where a row of the same call
+ * does not attend them yet: they meet its zero weights (K may be anything).  dtype bf16:
  * products of bf16, sums and statistics in fp32, the probabilities rounded
- * to bf16 before they meet V. */
+ * to bf16 before they meet V.  dtype f32: products and sums to fp32; a row
+ * that attends an infinite element is NaN. */
 int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
                         const int32_t *q_start, const int32_t *seq_len, int32_t n_tokens,
                         const mac_kv *kv, void *out, float *lse, void *stream);
@@ -326,12 +327,12 @@ int mac_join_aux(void *ring_ws, void *stream_main);
 int mac_reset_requests(const mac_config *cfg, void *ring_ws, int32_t *reset_flags, void *stream);
 
 /* Test hook for the bounded waits (no counterpart on the pages): the next
- * step or chunk-attention kernel launched by the calling thread gives every wait (a stage's
- * copy, a flag, the grid barrier, a piece count) `cycles` SM cycles instead
- * of about a second, and, if withhold_use >= 0, never issues the copy of
- * that stage use (per CTA; per warp in the ring kernel),
- * so the wait for it runs out: the kernel sets MAC_DEV_WAIT_TIMEOUT, stops
- * its work, lets its other copies land and returns.  The launch's outputs
+ * step or chunk-attention kernel launched by the calling thread gives every
+ * wait (a stage's copy, a flag, the grid barrier, a piece count) `cycles` SM
+ * cycles instead of about a second, and, if withhold_use >= 0, never issues
+ * the copy of that stage use (per CTA; per warp in the ring kernel; of the K
+ * ring in chunk attention), so the wait for it runs out: the kernel sets
+ * MAC_DEV_WAIT_TIMEOUT, stops its work, lets its other copies land and returns.  The launch's outputs
  * are then undefined; its scratch workspace must be cleared (or replaced)
  * before the next launch.  1 <= cycles <= 2^31, withhold_use >= -1; the
  * hook clears itself. */

@@ -144,7 +144,8 @@ __device__ void mma_role(const ChunkParams &p, uint32_t qbuf, uint32_t kbuf, uin
 }
 
 // ---- splitting (warps 4-11) -----------------------------------------------------
-// The next parts of four neighbours, packed, and what is left of them.
+// The next parts of four neighbours, packed, and what is left of them (of an
+// infinity NaN: a row that attends one is NaN).
 __device__ __forceinline__ uint2 split4(float4 &f) {
   const uint32_t a = __float_as_uint(f.x), b = __float_as_uint(f.y), c = __float_as_uint(f.z), d = __float_as_uint(f.w);
   const float2 lo = add2(make_float2(f.x, f.y), make_float2(-__uint_as_float(a & 0xffff0000u), -__uint_as_float(b & 0xffff0000u)));
@@ -160,9 +161,6 @@ __device__ __forceinline__ void put_parts(uint8_t *tile, int r, int lane, float4
   const int half = lane >> 4, chunk = lane >> 1 & 7;
   uint8_t *dst = tile + half * (ROWS * 128) + r * 128 + ((chunk ^ (r & 7)) << 4) + (lane & 1) * 8;
   *reinterpret_cast<uint2 *>(dst) = split4(f);
-  // an infinity's first part says it all, what it leaves (NaN) is nothing
-  const float sum = (f.x + f.y) + (f.z + f.w);
-  if (sum != sum) f = make_float4(f.x == f.x ? f.x : 0.f, f.y == f.y ? f.y : 0.f, f.z == f.z ? f.z : 0.f, f.w == f.w ? f.w : 0.f);
   *reinterpret_cast<uint2 *>(dst + kPart) = split4(f);
   *reinterpret_cast<uint2 *>(dst + 2 * kPart) = split4(f);
 }
@@ -232,7 +230,7 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
 #pragma unroll
           for (int i = 0; i < kPage / 2; ++i) f[i] = f[i + kPage / 2];
         }
-        hand_over(full);
+        if (!is_k || (int)nt != p.withhold) hand_over(full);
       }
       // only now: the fence of the hand-over would wait for loads in flight
       if (t + 1 < q.t1) load(t + 1, next);

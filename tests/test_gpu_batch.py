@@ -407,7 +407,11 @@ def test_chunk(lengths, Hq, Hkv, dt, paged):
     (BF16, 32, 4, [20000], [1], True),                           # one row over every CTA
     (BF16, 4, 4, [131071, 70], [1, 1], False),
     (BF16, 1, 1, [0], [4096], False),
+    (BF16, 8, 2, [30000], [64], True),                           # whole row tiles in many pieces
+    (BF16, 1, 1, [40000], [3], False),                           # more pieces than a warp has lanes
     (F32, 8, 2, [3000, 10], [500, 700], True),
+    (F32, 8, 2, [9000], [40], True),
+    (F32, 1, 1, [20000], [2], False),
     (F32, 1, 1, [4096], [64], False)])
 def test_chunk_over_many_ctas(dt, Hq, Hkv, ctx, new, paged):
     b = Batch(ctx, new, Hq, Hkv, dt, paged, seed=5)
@@ -415,13 +419,28 @@ def test_chunk_over_many_ctas(dt, Hq, Hkv, ctx, new, paged):
     assert b.status() == 0
     b.check()
     first = b.out.clone(), b.lse.clone()
-    for _ in range(3):  # the counts are back at zero, and the order of the sums does not depend on timing
+    for _ in range(3):  # the order of the sums does not depend on timing
         b.out.fill_(7)
         b.lse.fill_(7)
         b.run()
         assert torch.equal(b.out, first[0]) and torch.equal(b.lse, first[1])
     b.run(lse=False)
     assert torch.equal(b.out, first[0])
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_chunk_drawn(seed):
+    rng = random.Random(seed)
+    Hq, Hkv = rng.choice([(8, 8), (8, 4), (8, 2), (16, 2), (1, 1), (24, 3)])
+    B = rng.randint(1, 9)
+    hi, n = rng.choice([10, 200, 3000, 9000]), rng.choice([1, 4, 70, 600])
+    new = [rng.choice([0, 1, rng.randint(0, n)]) for _ in range(B)]
+    new[0] = max(new[0], 1)
+    b = Batch([rng.randint(0, hi) for _ in range(B)], new, Hq, Hkv, rng.choice([BF16, F32]), rng.random() < 0.5,
+              seed=seed, pad=rng.randint(0, 3))
+    b.run()
+    assert b.status() == 0
+    b.check()
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
@@ -481,9 +500,9 @@ def test_chunk_bad_lengths(dt):
     assert (b.out[33:] == 7).all() and (b.lse[:33] > -math.inf).all()
 
 
-def test_chunk_infinite_and_nan_rows_stay_in_their_row():
-    b = Batch([100], [70], 8, 2, BF16, True, seed=6)
-    clean = b.q.clone()
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_chunk_infinite_and_nan_rows_stay_in_their_row(dt):
+    b = Batch([100], [70], 8, 2, dt, True, seed=6)
     b.run()
     ref = b.out.clone()
     b.q[13, 3] = float("nan")
@@ -492,16 +511,44 @@ def test_chunk_infinite_and_nan_rows_stay_in_their_row():
     keep = torch.ones(70, 8, dtype=torch.bool, device=DEV)
     keep[13, 3] = keep[14, 5] = False
     assert torch.equal(b.out[keep], ref[keep])
-    assert b.out[13, 3].isnan().all() and not clean.isnan().any()
+    assert b.out[13, 3].isnan().all() and not ref.isnan().any()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_chunk_infinite_and_nan_keys_not_yet_attended(dt):
+    # a key that later rows of the same chunk attend may be anything for the rows before it
+    b = Batch([100], [70], 8, 2, dt, False, seed=6)
+    b.run()
+    ref = b.out.clone()
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        b.k[0, :, 140] = bad  # position 141: rows 40 and on
+        b.run()
+        assert torch.equal(b.out[:40], ref[:40])
+
+
+def test_chunk_an_infinite_key_weighs_nothing_or_all():
+    # scores of -inf leave a key out; those of +inf make the row NaN, as inf - inf does
+    b = Batch([40], [1], 2, 1, BF16, False, seed=7)
+    b.q.zero_()
+    b.q[0, 0, 5], b.q[0, 1, 5] = 1.0, -1.0
+    b.k[0, 0, 17] = 0
+    b.k[0, 0, 17, 5] = float("-inf")
+    b.run()
+    x = (b.kd[0, 0, :41, 5].double() / math.sqrt(D)).where(torch.arange(41, device=DEV) != 17, -math.inf)
+    w = torch.softmax(x, 0)
+    want, A = w @ b.vd[0, 0, :41].double(), w @ b.vd[0, 0, :41].double().abs()
+    near(b.out[0, 0], want, 2.0 ** -8 * (A + want.abs()) + 2.0 ** -14 * A)
+    assert b.out[0, 1].isnan().all()
 
 
 @pytest.mark.parametrize("new", [1, 200])
 @pytest.mark.parametrize("paged", [True, False])
 @pytest.mark.parametrize("use", [0, 1])
-def test_chunk_wait_runs_out(use, paged, new):
-    # the copy of key stage use `use` is never issued: the wait for it gives up after 2^16 cycles, the
-    # launch reports it and returns, and one on a fresh workspace is clean and right
-    b = Batch([3000, 1500], [new, new], 8, 2, BF16, paged, seed=9)
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_chunk_wait_runs_out(dt, use, paged, new):
+    # key stage use `use` is never filled: the wait for it gives up after 2^16 cycles, the launch reports
+    # it and returns, and one on a fresh workspace is clean and right
+    b = Batch([3000, 1500], [new, new], 8, 2, dt, paged, seed=9)
     mac.mac_test_wait_budget(1 << 16, use)
     b.run()
     torch.cuda.synchronize()
