@@ -52,7 +52,7 @@ struct ChunkParams {
   float *lse;                     // or null
   uint32_t *status;
   int4 *notes;                    // [kChunkGrid] the cut unit whose first tile a CTA holds
-  float *part;                    // [2 * grid][part_rows][kPartStride]
+  float *part;                    // [2 * grid][part_rows][kChunkStride]
   int part_rows;
   long long wait_limit;           // bf16 kernel: cycles a wait may take
   int withhold;                   // run-out test only: the stage use (>= 0) whose copy is never issued
@@ -60,6 +60,7 @@ struct ChunkParams {
 
 constexpr int kChunkGrid = 256;   // most CTAs of a launch (one per SM)
 constexpr int kChunkRowsBf16 = 256, kChunkRowsF32 = 128;  // rows per unit
+constexpr int kChunkStride = kHeadDim + 8;  // floats per row of a partial: o[d], m, l, and to a multiple of 32 bytes
 constexpr int kMaxTokens = 1 << 24;
 constexpr int kChunkShort = 8;    // key tiles of a short unit
 

@@ -47,10 +47,10 @@ template <int ROWS, int KT, int COST0, int W, int WS>
 struct ChunkPlan {
   static constexpr int kKt = log2i(KT);
 
-  long long prefix[kMaxUnits + 1];  // cost of all requests before b, all KV heads
-  long long warp_tot[32];
+  long long prefix[2][kMaxUnits + 1];  // cost (and units) of all requests before b, all KV heads
+  long long warp_tot[2][32];
   long long share;
-  int any_bad, any_long, whole;
+  int any_bad, whole;
 
   __device__ static int log_tokens(const ChunkParams &p) { return log2i(ROWS) - (31 - __clz(p.G)); }  // tokens per unit
   __device__ static int units(int n, int lt) { return (n + (1 << lt) - 1) >> lt; }
@@ -77,55 +77,52 @@ struct ChunkPlan {
     return before(a, lt, u - 1, false) + COST0 + (((long long)a + n + KT - 1) >> kKt) * weight(n - ((u - 1) << lt), lt);
   }
 
-  // Scan of the requests' costs; returns the sum.
-  __device__ long long scan(const ChunkParams &p, int lt, bool by_units) {
-    const int n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += n_thr) {
-      const int b = b0 + threadIdx.x;
-      long long v = 0;
-      if (b < p.B) {
-        int a, n;
-        if (request(p, b, &a, &n)) any_bad = 1;
-        if (((long long)a + n + KT - 1) >> kKt > kChunkShort && n > 0) any_long = 1;
-        v = cost(a, n, lt, by_units) * p.Hkv;
-      }
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += o;
-      }
-      if (lane == 31) warp_tot[warp] = v;
-      __syncthreads();
-      long long add = carry, all = carry;
-      for (int w = 0; w < n_thr >> 5 && b0 + w * 32 < p.B; ++w) {
-        if (w < warp) add += warp_tot[w];
-        all += warp_tot[w];
-      }
-      if (b < p.B) prefix[b + 1] = v + add;
-      carry = all;
-      __syncthreads();
-    }
-    return carry;
-  }
-
   // All threads of the block (a multiple of 32, at most 1024) call it.
   // min_share: least cost worth a CTA of its own.
   __device__ void build(const ChunkParams &p, int min_share) {
-    const int lt = log_tokens(p);
-    if (threadIdx.x == 0) {
-      any_bad = any_long = 0;
-      prefix[0] = 0;
+    const int lt = log_tokens(p), n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long sum[2] = {0, 0};  // cost, units
+    int bad = 0, is_long = 0;
+    if (threadIdx.x == 0) prefix[0][0] = prefix[1][0] = 0;
+    for (int b0 = 0; b0 < p.B; b0 += n_thr) {
+      const int b = b0 + threadIdx.x;
+      long long v[2] = {0, 0};
+      if (b < p.B) {
+        int a, n;
+        bad |= request(p, b, &a, &n) != 0;
+        is_long |= n > 0 && (((long long)a + n + KT - 1) >> kKt) > kChunkShort;
+        v[0] = cost(a, n, lt, false) * p.Hkv;
+        v[1] = cost(a, n, lt, true) * p.Hkv;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long o = __shfl_up_sync(0xffffffffu, v[i], d);
+          if (lane >= d) v[i] += o;
+        }
+        if (lane == 31) warp_tot[i][warp] = v[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        long long add = sum[i], all = sum[i];
+        for (int w = 0; w < n_thr >> 5 && b0 + w * 32 < p.B; ++w) {
+          if (w < warp) add += warp_tot[i][w];
+          all += warp_tot[i][w];
+        }
+        if (b < p.B) prefix[i][b + 1] = v[i] + add;
+        sum[i] = all;
+      }
+      if (b0 + n_thr < p.B) __syncthreads();
     }
-    __syncthreads();
-    long long total = scan(p, lt, true);  // units
-    const bool each = !any_long && total <= gridDim.x;
-    if (!each) total = scan(p, lt, false);
+    any_bad = __syncthreads_or(bad);  // (every thread writes the same; the barrier is the last one's too)
+    const bool each = !__syncthreads_or(is_long) && sum[1] <= gridDim.x;
     if (threadIdx.x == 0) {
       whole = each;
-      long long ctas = (int)min(total, 1LL << 30) / min_share;
+      long long ctas = (int)min(sum[0], 1LL << 30) / min_share;
       if (ctas > gridDim.x) ctas = gridDim.x;
       if (ctas < 1) ctas = 1;
-      share = each ? 1 : max(1LL, (total + ctas - 1) / ctas);
+      share = each ? 1 : max(1LL, (sum[0] + ctas - 1) / ctas);
     }
     __syncthreads();
   }
@@ -166,16 +163,17 @@ struct ChunkPlan {
     return lo;
   }
 
-  // The unit that holds cost position x, 0 <= x < prefix[B].
+  // The unit that holds position x of the axis in use.
   __device__ ChunkUnit find(const ChunkParams &p, long long x) const {
     ChunkUnit u;
     const int lt = log_tokens(p);
-    u.b = last_not_above(p.B, x, [&](int b) { return prefix[b]; });
-    request(p, u.b, &u.a, &u.n, &u.row0);
     const bool by_units = whole;
+    const long long *pre = prefix[by_units];
+    u.b = last_not_above(p.B, x, [&](int b) { return pre[b]; });
+    request(p, u.b, &u.a, &u.n, &u.row0);
     const int a = u.a;
     const long long per = cost(a, u.n, lt, by_units);
-    long long rem = x - prefix[u.b];
+    long long rem = x - pre[u.b];
     u.g = last_not_above(p.Hkv, rem, [&](int g) { return g * per; });
     rem -= u.g * per;
     const int i = last_not_above(units(u.n, lt), rem, [&](int k) { return before(a, lt, k, by_units); });
@@ -205,7 +203,7 @@ struct ChunkWalk {
     share = plan.share;
     whole = plan.whole;
     x = blockIdx.x * share;
-    end = min(plan.prefix[p.B], x + share);
+    end = min(plan.prefix[whole][p.B], x + share);
     first = true;
     if (x >= end) return false;
     u = plan.find(p, x);

@@ -490,7 +490,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     const int row = (q.pair ? 0 : w * kTile) + r;
     const bool whole = !q.cut(), keep = live && row < n_rows;
     const int c = blockIdx.x, c0 = whole ? 0 : walk.cta_of(p, q.u, 0), c1 = whole ? 0 : walk.cta_of(p, q.u, q.u.tiles - 1);
-    float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + row) * kPartStride;
+    float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + row) * kChunkStride;
     const int64_t out_row = (int64_t)(q.u.tok0 + row / p.G) * p.Hq + q.u.g * p.G + row % p.G;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     // a pair's groups take half of the columns each
@@ -531,7 +531,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) store_out(part + cc + j, make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]));
+        for (int j = 0; j < 32; j += 8) store32(part + cc + j, reinterpret_cast<const uint32_t *>(o + j));
       }
     }
     if (keep && !(q.pair && w == 1)) {

@@ -49,7 +49,7 @@ using Walk = ChunkWalk<Plan, kCost0, 1, 1>;
 
 struct Control {
   unsigned long long k_full, k_free, v_full, v_free, q_full, q_free;
-  unsigned long long s_full, s_free[2], p_full, o_full, o_free, drain;
+  unsigned long long s_full[2], s_free[2], p_full, o_full, o_free, drain;
   uint32_t tmem;
   int abort;
 };
@@ -111,7 +111,7 @@ __device__ void mma_role(const ChunkParams &p, uint32_t qbuf, uint32_t kbuf, uin
             const uint32_t w = kPairs >> 4 * i;
             tc_scores(tmem + kColS + buf * kColS1, qd + (w & 3) * (kQPart >> 4), kd + (w >> 2 & 3) * (kKvPart >> 4), i);
           }
-          tc_commit(smem_addr(&ct->s_full));
+          tc_commit(smem_addr(&ct->s_full[buf]));
           tc_commit(smem_addr(&ct->k_free));
           if (j + 1 == n) tc_commit(smem_addr(&ct->q_free));
         }
@@ -292,7 +292,8 @@ __device__ void row_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t 
           gone = __ballot_sync(0xffffffffu, bad);
           if (gone) status |= MAC_DEV_BAD_PAGE;
         }
-        if (!wait(&ct->s_full, nt & 1)) continue;
+        // (a barrier for each of the two: both may be there before this warp looks at the first)
+        if (!wait(&ct->s_full[nt & 1], nt >> 1 & 1)) continue;
         tc_fence_after();
         const uint32_t s_at = tmem + kColS + (nt & 1) * kColS1 + lanes;
         const int left = key0 + kKeys > q.u.pos0 ? lim - key0 : kKeys;  // keys of the tile that the row attends
@@ -376,7 +377,7 @@ __device__ void row_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t 
     if (keep) {
       const int64_t row = (int64_t)(q.u.tok0 + r / p.G) * p.Hq + q.u.g * p.G + r % p.G;
       const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + r) * kPartStride;
+      float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + r) * kChunkStride;
       float *dst = (whole ? (float *)p.out + row * kHeadDim : part);
 #pragma unroll
       for (int e = 0; e < kHeadDim; e += 4) store_out(dst + e, make_float4(o[e] * f, o[e + 1] * f, o[e + 2] * f, o[e + 3] * f));
@@ -415,7 +416,8 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
     mbar_init(smem_addr(&ct->k_free), 1);
     mbar_init(smem_addr(&ct->v_free), 1);
     mbar_init(smem_addr(&ct->q_free), 1);
-    mbar_init(smem_addr(&ct->s_full), 1);
+    mbar_init(smem_addr(&ct->s_full[0]), 1);
+    mbar_init(smem_addr(&ct->s_full[1]), 1);
     mbar_init(smem_addr(&ct->o_full), 1);
     mbar_init(smem_addr(&ct->drain), 1);
     mbar_init(smem_addr(&ct->s_free[0]), 4);

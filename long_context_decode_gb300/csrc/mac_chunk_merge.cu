@@ -25,8 +25,8 @@ __global__ void __launch_bounds__(kThr) merge_kernel(const __grid_constant__ Chu
   const int4 note = __ldcg(p.notes + c0);  // first token, KV head, rows, last CTA
   if (r0 >= note.z) return;
   const int n = note.w - c0 + 1;
-  const int64_t slot = (int64_t)p.part_rows * kPartStride;  // floats per partial
-  auto piece = [&](int j, int i) { return p.part + (2 * (c0 + j) + (j == 0)) * slot + (int64_t)min(r0 + i, note.z - 1) * kPartStride; };
+  const int64_t slot = (int64_t)p.part_rows * kChunkStride;  // floats per partial
+  auto piece = [&](int j, int i) { return p.part + (2 * (c0 + j) + (j == 0)) * slot + (int64_t)min(r0 + i, note.z - 1) * kChunkStride; };
   float m[kR], l[kR];
   float4 o[kR];
 #pragma unroll

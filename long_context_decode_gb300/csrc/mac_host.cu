@@ -257,7 +257,7 @@ ChunkLayout chunk_layout(const mac_config *c, int32_t n_tokens) {
   size_t off = 0;
   L.ctl = off;    off = align_up(off + 64 * 4, 256);
   L.notes = off;  off = align_up(off + (size_t)kChunkGrid * sizeof(int4), 256);
-  L.part = off;   off = align_up(off + 2 * (size_t)kChunkGrid * L.part_rows * kPartStride * 4, 256);
+  L.part = off;   off = align_up(off + 2 * (size_t)kChunkGrid * L.part_rows * kChunkStride * 4, 256);
   L.total = off;
   return L;
 }

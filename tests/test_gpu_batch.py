@@ -428,6 +428,18 @@ def test_chunk_over_many_ctas(dt, Hq, Hkv, ctx, new, paged):
     assert torch.equal(b.out, first[0])
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_chunk_several_pieces_per_cta_many_times(dt):
+    # the products run ahead into a CTA's next piece while the last one's rows are written
+    b = Batch([2000, 700] * 8, [1, 40] * 8, 32, 8, dt, True, seed=12)
+    b.run()
+    b.check()
+    ref = b.out.clone()
+    for _ in range(60):
+        b.run()
+    assert b.status() == 0 and torch.equal(b.out, ref)
+
+
 @pytest.mark.parametrize("seed", range(16))
 def test_chunk_drawn(seed):
     rng = random.Random(seed)
