@@ -369,7 +369,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
   const float scale = p.q_scale, lazy = kLazy / scale;
   const float2 scale2 = make_float2(scale, scale);
   int4 note = make_int4(0, 0, 0, 0);
-  uint32_t ns = 0, no = 0;  // scores taken; parity of each group's next output
+  uint32_t ns = 0, no = 0;  // scores and outputs taken
   uint32_t status = 0;
   Piece q = {};
   while (walk.next(p, q)) {
@@ -468,12 +468,12 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     }
     // ---- the piece's rows
     float l = l2.x + l2.y;
+    // this group's products have ended; in a pair the barrier below says so of the other's
     bool live = true;
-    for (int x = 0; x < 2; ++x)
-      if (q.count(x) > 0) {  // group 0's products end before group 1's
-        if (q.pair || x == w) live &= wait(&ct->o_full[x], no >> x & 1);
-        no ^= 1u << x;
-      }
+    if (mine > 0) {
+      live = wait(&ct->o_full[w], no & 1);
+      ++no;
+    }
     float f[2] = {1.f, 1.f};  // factors of O_w and (pair) of the other group's
     if (q.pair) {
       ct->ml[w][r] = make_float2(m, l);
