@@ -127,6 +127,8 @@ struct ChunkPlan {
     __syncthreads();
   }
 
+  __device__ bool has_work(const ChunkParams &p) const { return blockIdx.x * share < prefix[whole][p.B]; }
+
   // Lengths of request b: tokens before the new ones, new tokens (0: nothing
   // to attend).  Returns the status bits of a bad request; *rows, where
   // given, is the number of its rows that lie in the batch.
@@ -191,23 +193,21 @@ struct ChunkPlan {
   }
 };
 
-// A CTA's walk through its pieces (every role of a kernel has its own).
+// A CTA's walk through its pieces.
 template <typename PLAN, int COST0, int W, int WS>
 struct ChunkWalk {
   long long x, end, share;
   ChunkUnit u;
   bool first, whole;
 
-  // All threads of the block call it; false: no work.
-  __device__ bool start(const ChunkParams &p, const PLAN &plan) {
+  // A whole warp calls it, of a CTA with work.
+  __device__ void start(const ChunkParams &p, const PLAN &plan) {
     share = plan.share;
     whole = plan.whole;
     x = blockIdx.x * share;
     end = min(plan.prefix[whole][p.B], x + share);
     first = true;
-    if (x >= end) return false;
     u = plan.find(p, x);
-    return true;
   }
   __device__ int weight(int lt) const { return PLAN::weight(u.n_tok, lt); }
   // Next piece with a tile; false when the CTA's work is done.

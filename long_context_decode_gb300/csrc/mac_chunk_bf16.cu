@@ -14,7 +14,8 @@
 //   warps 8, 11     copy Q and K, and V, by TMA into swizzled shared memory;
 //   warp 9          issues the products: S into TMEM from shared memory, and
 //                   O += P V with P read back from TMEM;
-//   warp 10         clears V rows past the end of the sequence.
+//   warp 10         works out the CTA's pieces, and clears V rows past the
+//                   end of the sequence.
 // A unit has up to 256 packed rows (token-major, the G heads of a token
 // together), two row tiles of 128.  With 128 rows or fewer both softmax
 // groups work on the same rows and take the key tiles in turn.  While one
@@ -46,11 +47,28 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
+// A piece of a unit, as the roles see it.
+struct Piece {
+  int b, g;           // request, KV head
+  int tok0, n_tok;    // first token (row of the batch), tokens
+  int pos0;           // keys that the first token attends
+  int t0, t1;         // key tiles
+  int end0;           // normal: key tiles of row tile 0 end here (those of row tile 1 at t1)
+  int pair;           // both groups on row tile 0, key tiles in turn
+  int clear;          // keys of the last tile that exist, if V is to be cleared after them; else kTile
+  int c0, c1;         // a cut unit's first and last CTA; else -1
+  __device__ int n() const { return t1 - t0; }
+  __device__ bool cut() const { return c0 >= 0; }
+  // key tiles of group w
+  __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : w ? t1 - t0 : max(0, end0 - t0); }
+};
+
 struct Control {
   unsigned long long full[kNSt], empty[kNSt];
-  unsigned long long q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, fixed, drain;
+  unsigned long long q_full, q_empty, s_full[2], p_full[2], o_full[2], pair_ml, pair_read, tail, fixed, drain;
   uint32_t tmem;
   int abort;
+  PieceRing<Piece> pieces;
   float2 ml[2][kTile];                        // states of the two groups that share rows
 };
 constexpr int kSmemBytes = (kNSt + 2) * kTileBytes + (int)sizeof(Control);
@@ -128,41 +146,23 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *v) {
   }
 }
 
-// ---- the pieces of a CTA, as every role walks them ---------------------------
-struct Piece : ChunkPiece {
-  int pair;         // both groups on row tile 0, key tiles in turn
-  int end0;         // normal: key tiles of row tile 0 end here (those of row tile 1 at t1)
-  __device__ int n() const { return t1 - t0; }
-  // key tiles of group w
-  __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : w ? t1 - t0 : max(0, end0 - t0); }
-};
-
-struct Walk : ChunkWalk<Plan, kCost0, kW, kWs> {
-  __device__ bool next(const ChunkParams &p, Piece &q) {
-    if (!ChunkWalk::next(p, q)) return false;
-    q.pair = q.u.n_tok * p.G <= kTile;
-    q.end0 = min(q.t1, (q.u.pos0 + kTile / p.G - 1 + kTile - 1) / kTile);
-    return true;
-  }
-};
-
 // ---- copies (warps 8 and 11) ---------------------------------------------------
 // One ring's copies: key or value tiles into stages st0 .. st0 + NST - 1, and
 // (K) the Q tiles.  A paged tile is 8 pages of two 64-column halves, one copy each.
 template <bool PAGED, bool IS_K>
-__device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stages, uint32_t qbuf, Control *ct, Walk walk) {
+__device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stages, uint32_t qbuf, Control *ct) {
   constexpr int NST = IS_K ? kStK : kStV, ST0 = IS_K ? 0 : kStK;
   const CUtensorMap *map = IS_K ? &maps.k : &maps.v;
   const int lane = threadIdx.x & 31, half = lane >> 3 & 1, pg = lane & 7;
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
   int use = 0;       // stage uses so far
-  uint32_t nq = 0;   // Q tiles so far
+  uint32_t nq = 0, np = 0;  // Q tiles, pieces so far
   Piece q = {};
-  while (walk.next(p, q)) {
-    const int n_pages = (q.u.pos0 + q.u.n_tok - 1 + kPage - 1) / kPage;  // of the unit's keys
+  while (ct->pieces.take(wait, np, q)) {
+    const int n_pages = (q.pos0 + q.n_tok - 1 + kPage - 1) / kPage;  // of the unit's keys
     auto page = [&](int t) {  // page of this lane's copy; out of range where there is none: the copy fills with zeros
       const int k = t * (kTile / kPage) + pg;
-      int id = k < n_pages ? p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + k] : -1;
+      int id = k < n_pages ? p.kv.page_table[(int64_t)q.b * p.kv.max_pages + k] : -1;
       return bad_page(p, id) ? p.kv.n_pages : id;
     };
     int id = PAGED ? page(q.t0) : 0;
@@ -175,9 +175,9 @@ __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stage
         __syncwarp();
         if (!IS_K || use != p.withhold) {
           if (PAGED) {
-            if (lane < 16) tma_4d(dst + half * (kTileBytes / 2) + pg * (kPage * 128), map, 64 * half, 0, q.u.g, id, bar);
+            if (lane < 16) tma_4d(dst + half * (kTileBytes / 2) + pg * (kPage * 128), map, 64 * half, 0, q.g, id, bar);
           } else if (lane < 2) {
-            tma_3d(dst + lane * (kTileBytes / 2), map, 64 * lane, t * kTile, q.u.b * p.Hkv + q.u.g, bar);
+            tma_3d(dst + lane * (kTileBytes / 2), map, 64 * lane, t * kTile, q.b * p.Hkv + q.g, bar);
           }
         }
         ++use;
@@ -190,7 +190,7 @@ __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stage
         if (lane == 0) mbar_expect_tx(bar, tiles * kTileBytes);
         __syncwarp();
         if (lane < 2 * tiles)
-          tma_3d(qbuf + lane * (kTileBytes / 2), &maps.q, 64 * (lane & 1), q.u.g * p.G, q.u.tok0 + (lane >> 1) * (kTile / p.G), bar);
+          tma_3d(qbuf + lane * (kTileBytes / 2), &maps.q, 64 * (lane & 1), q.g * p.G, q.tok0 + (lane >> 1) * (kTile / p.G), bar);
         ++nq;
         __syncwarp();
       }
@@ -221,10 +221,10 @@ struct RingPos {
   }
 };
 
-__device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, Control *ct, Walk walk, uint32_t tmem) {
+__device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, Control *ct, uint32_t tmem) {
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
   RingPos k = {0, 0}, v = {kStK, 0};
-  uint32_t q_phase = 0, fix_phase = 0, p_phase[2] = {0, 0};
+  uint32_t np = 0, q_phase = 0, fix_phase = 0, p_phase[2] = {0, 0};
   Piece q = {};
   auto addr = [&](uint32_t st) { return stages + st * kTileBytes; };
   auto commit = [&](unsigned long long *bar) {
@@ -250,10 +250,9 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
     commit(&ct->empty[v.st]);
     v.step(kStK, kStV);
   };
-  while (walk.next(p, q)) {
+  while (ct->pieces.take(wait, np, q)) {
     const int n = q.n();
-    // V rows past the end of the sequence are cleared by warp 10
-    const bool fix = q.t1 == q.u.tiles && q.t1 * kTile > q.u.a + q.u.n;
+    const bool fix = q.clear < kTile;  // V rows past the end of the sequence are cleared by warp 10
     auto values_ready = [&](bool last) {
       wait(&ct->full[v.st], v.phase);
       if (last && fix) {
@@ -329,39 +328,60 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
   }
 }
 
-// ---- V rows past the end (warp 10) ----------------------------------------------
-// Zero weights meet whatever the cache holds there: it may be anything, so
-// the rows are cleared in shared memory before the product reads them.
-__device__ void fix_role(const ChunkParams &p, uint8_t *stages, Control *ct, Walk walk) {
+// ---- the walk, and V rows past the end (warp 10) ---------------------------------
+// Zero weights meet whatever the cache holds past the end of a sequence: it
+// may be anything, so those rows are cleared in shared memory before the
+// product reads them.  That waits for the products, so it comes one piece
+// behind the walk.
+__device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, const Plan &plan) {
   const int lane = threadIdx.x & 31;
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
-  int uv = 0;
-  uint32_t nt = 0;
-  Piece q = {};
-  while (walk.next(p, q)) {
-    const int n = q.n(), m = q.u.a + q.u.n;
-    if (q.t1 == q.u.tiles && q.t1 * kTile > m) {
-      if (wait(&ct->tail, nt & 1)) {
-        ++nt;
-        uint8_t *v = stages + (kStK + (uv + n - 1) % kStV) * kTileBytes;
-        const int r0 = max(0, m - (q.t1 - 1) * kTile);
-        for (int i = r0 * 8 + lane; i < kTile * 8; i += 32) {
-          *reinterpret_cast<uint4 *>(v + i * 16) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(v + kTileBytes / 2 + i * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ct->fixed));
-      }
-      __syncwarp();
+  ChunkWalk<Plan, kCost0, kW, kWs> walk;
+  walk.start(p, plan);
+  fence_proxy_async();  // the plan has been read: its place is the stages'
+  uint32_t nt = 0, last_v = 0;  // tiles cleared; V uses before the next piece
+  int clear = kTile;            // of the piece posted last
+  for (uint32_t i = 0;; ++i) {
+    ChunkPiece x = {};
+    const bool more = walk.next(p, x);
+    Piece q = {};
+    if (more) {
+      const ChunkUnit &u = x.u;
+      const bool cut = x.cut();
+      q.b = u.b;
+      q.g = u.g;
+      q.tok0 = u.tok0;
+      q.n_tok = u.n_tok;
+      q.pos0 = u.pos0;
+      q.t0 = x.t0;
+      q.t1 = x.t1;
+      q.end0 = min(x.t1, (u.pos0 + kTile / p.G - 1 + kTile - 1) / kTile);
+      q.pair = u.n_tok * p.G <= kTile;
+      q.clear = x.t1 == u.tiles ? min(kTile, u.a + u.n - (x.t1 - 1) * kTile) : kTile;
+      q.c0 = cut ? walk.cta_of(p, u, 0) : -1;
+      q.c1 = cut ? walk.cta_of(p, u, u.tiles - 1) : -1;
     }
-    uv += n;
+    ct->pieces.post(wait, i, q);
+    if (clear < kTile && wait(&ct->tail, nt & 1)) {
+      ++nt;
+      uint8_t *v = stages + (kStK + (last_v + kStV - 1) % kStV) * kTileBytes;
+      for (int e = clear * 8 + lane; e < kTile * 8; e += 32) {
+        *reinterpret_cast<uint4 *>(v + e * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(v + kTileBytes / 2 + e * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ct->fixed));
+    }
+    if (!more || wait.dead) return;
+    clear = q.clear;
+    last_v = (last_v + q.n()) % kStV;
   }
 }
 
 // ---- softmax, output (warps 0-7) --------------------------------------------------
 template <bool PAGED>
-__device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t tmem) {
+__device__ void softmax_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   const int tid = threadIdx.x, w = tid >> 7, r = tid & 127, lane = tid & 31;
   const uint32_t lanes = (uint32_t)((tid >> 5) & 3) << 21;  // this warp's 32 TMEM lanes
   const uint32_t s_at = tmem + w * kTile + lanes;
@@ -369,15 +389,15 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
   const float scale = p.q_scale, lazy = kLazy / scale;
   const float2 scale2 = make_float2(scale, scale);
   int4 note = make_int4(0, 0, 0, 0);
-  uint32_t ns = 0, no = 0;  // scores and outputs taken
+  uint32_t np = 0, ns = 0, no = 0, n_pair = 0;  // pieces, scores, outputs taken, shared row tiles
   uint32_t status = 0;
   Piece q = {};
-  while (walk.next(p, q)) {
+  while (ct->pieces.take(wait, np, q)) {
     const int tok = ((q.pair ? 0 : w * kTile) + r) / p.G;   // token of this row
-    const int lim = q.u.pos0 + tok;                         // it attends keys [0, lim)
+    const int lim = q.pos0 + tok;                         // it attends keys [0, lim)
     const int mine = q.count(w), step = q.pair ? 2 : 1, first = q.t0 + (q.pair ? w : 0);
-    const int n_keys = q.u.pos0 + q.u.n_tok - 1;
-    const int n_rows = q.u.n_tok * p.G;
+    const int n_keys = q.pos0 + q.n_tok - 1;
+    const int n_rows = q.n_tok * p.G;
     // a warp without a row of the unit only keeps the order of the tiles:
     // its weights are whatever TMEM holds, and so are its rows of O
     const bool idle = (q.pair ? 0 : w * kTile) + (r & ~31) >= n_rows;
@@ -390,7 +410,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
         bool bad = false;
         const int pg = key0 / kPage + lane;
         if (lane < kTile / kPage && pg * kPage < n_keys)
-          bad = bad_page(p, p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + pg]);
+          bad = bad_page(p, p.kv.page_table[(int64_t)q.b * p.kv.max_pages + pg]);
         gone = __ballot_sync(0xffffffffu, bad);
       }
       if (!wait(&ct->s_full[w], ns & 1)) continue;
@@ -408,7 +428,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
       tc_wait_ld();
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) tc_loaded32(s + c);
-      if (key0 + kTile > q.u.pos0) {  // some row of the unit does not attend the whole tile
+      if (key0 + kTile > q.pos0) {  // some row of the unit does not attend the whole tile
         const int left = lim - key0;
 #pragma unroll
         for (int c = 0; c < kTile; ++c) s[c] = c < left ? s[c] : -INFINITY;
@@ -476,8 +496,11 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     }
     float f[2] = {1.f, 1.f};  // factors of O_w and (pair) of the other group's
     if (q.pair) {
+      // (bounded waits instead of a block barrier: a group may give up)
       ct->ml[w][r] = make_float2(m, l);
-      named_sync(2, 256);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ct->pair_ml));
+      live &= wait(&ct->pair_ml, n_pair & 1);
       const float2 other = ct->ml[w ^ 1][r];
       const float mn = fmaxf(m, other.x), ms = mn == -INFINITY ? 0.f : mn;
       f[0] = ex2((m - ms) * scale);
@@ -489,9 +512,9 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
     tc_fence_after();
     const int row = (q.pair ? 0 : w * kTile) + r;
     const bool whole = !q.cut(), keep = live && row < n_rows;
-    const int c = blockIdx.x, c0 = whole ? 0 : walk.cta_of(p, q.u, 0), c1 = whole ? 0 : walk.cta_of(p, q.u, q.u.tiles - 1);
-    float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + row) * kChunkStride;
-    const int64_t out_row = (int64_t)(q.u.tok0 + row / p.G) * p.Hq + q.u.g * p.G + row % p.G;
+    const int c = blockIdx.x;
+    float *part = p.part + ((int64_t)(2 * c + (c == q.c0 ? 1 : 0)) * p.part_rows + row) * kChunkStride;
+    const int64_t out_row = (int64_t)(q.tok0 + row / p.G) * p.Hq + q.g * p.G + row % p.G;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     // a pair's groups take half of the columns each
 #pragma unroll 1
@@ -538,11 +561,14 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, Walk walk, uint3
       if (!whole) *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(m * scale, l);  // base 2, as the merge takes it
       else if (p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : m * scale * kLn2 + logf(l);
     }
-    if (q.pair) {
+    if (q.pair) {  // go on once O has been read by both groups
       tc_fence_before();
-      named_sync(2, 256);  // O has been read by both groups
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ct->pair_read));
+      wait(&ct->pair_read, n_pair & 1);
+      ++n_pair;
     }
-    if (!whole && c == c0 && live) note = make_int4(q.u.tok0, q.u.g, n_rows, c1);
+    if (c == q.c0) note = make_int4(q.tok0, q.g, n_rows, q.c1);
   }
   if (tid == 0) leave_note(p, wait.dead ? make_int4(0, 0, 0, 0) : note);
   if (status) set_status(p.status, status);
@@ -579,6 +605,9 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
       mbar_init(smem_addr(&ct->p_full[w]), 4);
       mbar_init(smem_addr(&ct->o_full[w]), 1);
     }
+    mbar_init(smem_addr(&ct->pair_ml), 8);
+    mbar_init(smem_addr(&ct->pair_read), 8);
+    ct->pieces.init(11);  // warps 0-9 and 11
     mbar_init(smem_addr(&ct->tail), 1);
     mbar_init(smem_addr(&ct->fixed), 1);
     mbar_init(smem_addr(&ct->drain), 1);
@@ -592,11 +621,10 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   }
   griddep_wait();  // from here on the previous kernel's writes are read
   // this CTA's part of the work, the plan made where the stages go
-  Walk walk;
   Plan &plan = *reinterpret_cast<Plan *>(smem);
   plan.build(p, kMinShare);
   if (plan.any_bad) chunk_bad_requests<uint16_t, Plan>(p);
-  const bool work = walk.start(p, plan);
+  const bool work = plan.has_work(p);
   fence_proxy_async();  // copies into the stages come after this
   tc_fence_before();
   block_sync();
@@ -609,14 +637,14 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   }
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_role<PAGED>(p, ct, walk, tmem);
+    softmax_role<PAGED>(p, ct, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) load_role<PAGED, true>(p, maps, smem_addr(smem), smem_addr(qbuf), ct, walk);
-    else if (warp == 11) load_role<PAGED, false>(p, maps, smem_addr(smem), smem_addr(qbuf), ct, walk);
+    if (warp == 8) load_role<PAGED, true>(p, maps, smem_addr(smem), smem_addr(qbuf), ct);
+    else if (warp == 11) load_role<PAGED, false>(p, maps, smem_addr(smem), smem_addr(qbuf), ct);
     else if (warp == 9) {
-      mma_role(p, smem_addr(smem), smem_addr(qbuf), ct, walk, tmem);
-    } else if (warp == 10) fix_role(p, smem, ct, walk);
+      mma_role(p, smem_addr(smem), smem_addr(qbuf), ct, tmem);
+    } else walk_role(p, smem, ct, plan);
   }
   tc_fence_before();
   block_sync();

@@ -19,7 +19,8 @@
 //                parts, swizzled, in shared memory (rows that are not there
 //                as zeros), each warp the rows of one page of a tile;
 //   warp 12      issues the products: S (64 columns of TMEM) from shared
-//                memory, P V (128 columns) with P's parts (96) in TMEM.
+//                memory, P V (128 columns) with P's parts (96) in TMEM;
+//   warp 13      works out the CTA's pieces.
 // The roles' loops are kept short: unrolled in full they did not fit the
 // instruction cache together, and its misses took two thirds of the time.
 // S of the next tile is made while the softmax runs; K is stored while the
@@ -45,13 +46,22 @@ static_assert(kRegsSoft + 2 * kRegsSplit + kRegsMma <= 4 * kRegsLaunch && kThr *
 constexpr int kQPart = kRows * kHeadDim * 2, kKvPart = kKeys * kHeadDim * 2;  // bytes of one bf16 part of a tile
 constexpr uint32_t kColS = 0, kColS1 = 64, kColP = 128, kColO = 256;  // TMEM columns: S twice, P, P V
 using Plan = ChunkPlan<kRows, kKeys, kCost0, 1, 1>;
-using Walk = ChunkWalk<Plan, kCost0, 1, 1>;
+
+// A piece of a unit, as the roles see it.
+struct Piece {
+  int b, g;           // request, KV head
+  int tok0, n_tok;    // first token (row of the batch), tokens
+  int pos0;           // keys that the first token attends
+  int t0, t1;         // key tiles
+  int c0, c1;         // a cut unit's first and last CTA; else -1
+};
 
 struct Control {
   unsigned long long k_full, k_free, v_full, v_free, q_full, q_free;
   unsigned long long s_full[2], s_free[2], p_full, o_full, o_free, drain;
   uint32_t tmem;
   int abort;
+  PieceRing<Piece> pieces;
 };
 constexpr int kSmemBytes = 3 * kQPart + 6 * kKvPart + (int)sizeof(Control);
 static_assert(kSmemBytes <= (int)kMaxSmem && sizeof(Plan) <= 6 * kKvPart, "shared memory of a CTA");
@@ -89,12 +99,12 @@ __device__ __forceinline__ void tc_values(uint32_t d, uint32_t a, uint32_t b, ui
 // (part of the first factor | part of the second << 2), 4 bits each, smallest products first: 2 0, 0 2, 1 1, 1 0, 0 1, 0 0
 constexpr uint32_t kPairs = 0x2 | 0x8 << 4 | 0x5 << 8 | 0x1 << 12 | 0x4 << 16 | 0x0 << 20;
 
-__device__ void mma_role(const ChunkParams &p, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, Control *ct, Walk walk, uint32_t tmem) {
+__device__ void mma_role(const ChunkParams &p, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, Control *ct, uint32_t tmem) {
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
-  uint32_t nt = 0, ns = 0, nq = 0;  // tiles of P V, of S, and Q tiles so far
+  uint32_t np = 0, nt = 0, ns = 0, nq = 0;  // pieces, tiles of P V, of S, and Q tiles so far
   const uint32_t qd = desc_lo(qbuf, 16), kd = desc_lo(kbuf, 16), vd = desc_lo(vbuf, kKvPart / 2);
-  ChunkPiece q = {};
-  while (walk.next(p, q)) {
+  Piece q = {};
+  while (ct->pieces.take(wait, np, q)) {
     const int n = q.t1 - q.t0;
     wait(&ct->q_full, nq & 1);
     ++nq;
@@ -177,29 +187,29 @@ __device__ __forceinline__ float4 load_if(const float *src, bool ok) {
 }
 
 template <bool PAGED>
-__device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, uint8_t *vbuf, Control *ct, Walk walk) {
+__device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, uint8_t *vbuf, Control *ct) {
   const int lane = threadIdx.x & 31, me_q = (threadIdx.x >> 5) - 4, me = me_q & (kConv - 1);
   const bool is_k = me_q < kConv;  // one copy of the code for both: see above
   const float *src = (const float *)(is_k ? p.kv.k : p.kv.v) + lane * 4;
   unsigned long long *full = is_k ? &ct->k_full : &ct->v_full, *free = is_k ? &ct->k_free : &ct->v_free;
   uint8_t *tile = is_k ? kbuf : vbuf;
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
-  uint32_t nt = 0, nq = 0;  // tiles and Q tiles so far
-  ChunkPiece q = {};
+  uint32_t np = 0, nt = 0, nq = 0;  // pieces, tiles and Q tiles so far
+  Piece q = {};
   auto hand_over = [&](unsigned long long *bar) {
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(bar));
   };
-  while (walk.next(p, q)) {
-    const int n_rows = q.u.n_tok * p.G, n_keys = q.u.pos0 + q.u.n_tok - 1;
+  while (ct->pieces.take(wait, np, q)) {
+    const int n_rows = q.n_tok * p.G, n_keys = q.pos0 + q.n_tok - 1;
     // this warp's 16 rows of tile t: the element of their first one (-1: no
     // page), and how many of them are keys of the unit
     auto at = [&](int t) -> int64_t {
-      if (!PAGED) return (((int64_t)q.u.b * p.Hkv + q.u.g) * p.kv.capacity + t * kKeys + me * kPage) * kHeadDim;
+      if (!PAGED) return (((int64_t)q.b * p.Hkv + q.g) * p.kv.capacity + t * kKeys + me * kPage) * kHeadDim;
       const int k = t * (kKeys / kPage) + me;
-      const int id = t < q.t1 && (int64_t)k * kPage < n_keys ? p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + k] : -1;
-      return id >= 0 && id < p.kv.n_pages ? ((int64_t)id * p.Hkv + q.u.g) * kPage * kHeadDim : -1;
+      const int id = t < q.t1 && (int64_t)k * kPage < n_keys ? p.kv.page_table[(int64_t)q.b * p.kv.max_pages + k] : -1;
+      return id >= 0 && id < p.kv.n_pages ? ((int64_t)id * p.Hkv + q.g) * kPage * kHeadDim : -1;
     };
     float4 f[kPage];
     auto load = [&](int t, int64_t first) {
@@ -215,7 +225,7 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
       for (int r = me_q; r < kRows; r += 2 * kConv) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < n_rows)
-          x = *reinterpret_cast<const float4 *>((const float *)p.q + ((int64_t)(q.u.tok0 + r / p.G) * p.Hq + q.u.g * p.G + r % p.G) * kHeadDim + lane * 4);
+          x = *reinterpret_cast<const float4 *>((const float *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim + lane * 4);
         put_parts<kRows>(qbuf, r, lane, x);
       }
       hand_over(&ct->q_full);
@@ -239,24 +249,43 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
   }
 }
 
+// ---- the walk (warp 13) -----------------------------------------------------------
+__device__ void walk_role(const ChunkParams &p, Control *ct, const Plan &plan) {
+  Waiter wait{&ct->abort, p.status, p.wait_limit, false};
+  ChunkWalk<Plan, kCost0, 1, 1> walk;
+  walk.start(p, plan);
+  for (uint32_t i = 0;; ++i) {
+    ChunkPiece x = {};
+    const bool more = walk.next(p, x);
+    Piece q = {};
+    if (more) {
+      const ChunkUnit &u = x.u;
+      const bool cut = x.cut();
+      q = {u.b, u.g, u.tok0, u.n_tok, u.pos0, x.t0, x.t1, cut ? walk.cta_of(p, u, 0) : -1, cut ? walk.cta_of(p, u, u.tiles - 1) : -1};
+    }
+    ct->pieces.post(wait, i, q);
+    if (!more || wait.dead) return;
+  }
+}
+
 // ---- softmax and output (warps 0-3) -----------------------------------------------
 template <bool PAGED>
-__device__ void row_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t tmem) {
+__device__ void row_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   const int tid = threadIdx.x, r = tid, lane = tid & 31;
   const uint32_t lanes = (uint32_t)(tid >> 5) << 21;  // this warp's 32 TMEM lanes
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
   const float scale = p.q_scale;
-  uint32_t nt = 0, status = 0;
+  uint32_t np = 0, nt = 0, status = 0;
   int4 note = make_int4(0, 0, 0, 0);
-  ChunkPiece q = {};
+  Piece q = {};
   auto arrive = [&](unsigned long long *bar) {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(bar));
   };
-  while (walk.next(p, q)) {
-    const int lim = q.u.pos0 + r / p.G;  // keys [0, lim) are the row's
-    const int n = q.t1 - q.t0, n_rows = q.u.n_tok * p.G, n_keys = q.u.pos0 + q.u.n_tok - 1;
+  while (ct->pieces.take(wait, np, q)) {
+    const int lim = q.pos0 + r / p.G;  // keys [0, lim) are the row's
+    const int n = q.t1 - q.t0, n_rows = q.n_tok * p.G, n_keys = q.pos0 + q.n_tok - 1;
     const bool idle = (r & ~31) >= n_rows;  // no row of this warp: it only keeps the order of the tiles
     float m = -INFINITY, l = 0.f, o[kHeadDim];
 #pragma unroll
@@ -286,7 +315,7 @@ __device__ void row_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t 
           bool bad = false;
           const int pg = key0 / kPage + lane;
           if (lane < kKeys / kPage && pg * kPage < n_keys) {
-            const int id = p.kv.page_table[(int64_t)q.u.b * p.kv.max_pages + pg];
+            const int id = p.kv.page_table[(int64_t)q.b * p.kv.max_pages + pg];
             bad = id < 0 || id >= p.kv.n_pages;
           }
           gone = __ballot_sync(0xffffffffu, bad);
@@ -296,7 +325,7 @@ __device__ void row_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t 
         if (!wait(&ct->s_full[nt & 1], nt >> 1 & 1)) continue;
         tc_fence_after();
         const uint32_t s_at = tmem + kColS + (nt & 1) * kColS1 + lanes;
-        const int left = key0 + kKeys > q.u.pos0 ? lim - key0 : kKeys;  // keys of the tile that the row attends
+        const int left = key0 + kKeys > q.pos0 ? lim - key0 : kKeys;  // keys of the tile that the row attends
         // 32 scores at a time, those that are not the row's at -inf
         auto scores = [&](float *s, int c0) {
           tc_ld32(s, s_at + c0);
@@ -372,19 +401,19 @@ __device__ void row_role(const ChunkParams &p, Control *ct, Walk walk, uint32_t 
       if (wait(&ct->o_full, (nt - 1) & 1)) accumulate(corr_before);
     }
     // ---- the piece's rows: a whole unit goes out, a piece of one leaves its state
-    const bool whole = !q.cut(), keep = !wait.dead && r < n_rows;
-    const int c = blockIdx.x, c0 = whole ? c : walk.cta_of(p, q.u, 0), c1 = whole ? c : walk.cta_of(p, q.u, q.u.tiles - 1);
+    const bool whole = q.c0 < 0, keep = !wait.dead && r < n_rows;
+    const int c = blockIdx.x;
     if (keep) {
-      const int64_t row = (int64_t)(q.u.tok0 + r / p.G) * p.Hq + q.u.g * p.G + r % p.G;
+      const int64_t row = (int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G;
       const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      float *part = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + r) * kChunkStride;
+      float *part = p.part + ((int64_t)(2 * c + (c == q.c0 ? 1 : 0)) * p.part_rows + r) * kChunkStride;
       float *dst = (whole ? (float *)p.out + row * kHeadDim : part);
 #pragma unroll
       for (int e = 0; e < kHeadDim; e += 4) store_out(dst + e, make_float4(o[e] * f, o[e + 1] * f, o[e + 2] * f, o[e + 3] * f));
       if (!whole) *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(m, l);
       else if (p.lse) p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
-    if (!whole && c == c0) note = make_int4(q.u.tok0, q.u.g, n_rows, c1);
+    if (c == q.c0) note = make_int4(q.tok0, q.g, n_rows, q.c1);
   }
   if (tid == 0) leave_note(p, wait.dead ? make_int4(0, 0, 0, 0) : note);
   if (status) set_status(p.status, status);
@@ -424,15 +453,15 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
     mbar_init(smem_addr(&ct->s_free[1]), 4);
     mbar_init(smem_addr(&ct->p_full), 4);
     mbar_init(smem_addr(&ct->o_free), 4);
+    ct->pieces.init(13);  // warps 0-12
     ct->abort = 0;
     mbar_fence_init();
   }
   griddep_wait();  // from here on the previous kernel's writes are read
-  Walk walk;
   Plan &plan = *reinterpret_cast<Plan *>(kbuf);  // made where the K and V tiles go
   plan.build(p, kMinShare);
   if (plan.any_bad) chunk_bad_requests<float, Plan>(p);
-  const bool work = walk.start(p, plan);
+  const bool work = plan.has_work(p);
   tc_fence_before();
   block_sync();
   tc_fence_after();
@@ -444,13 +473,14 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   }
   if (warp < 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    row_role<PAGED>(p, ct, walk, tmem);
+    row_role<PAGED>(p, ct, tmem);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSplit));
-    split_role<PAGED>(p, qbuf, kbuf, vbuf, ct, walk);
+    split_role<PAGED>(p, qbuf, kbuf, vbuf, ct);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-    if (warp == 12) mma_role(p, smem_addr(qbuf), smem_addr(kbuf), smem_addr(vbuf), ct, walk, tmem);
+    if (warp == 12) mma_role(p, smem_addr(qbuf), smem_addr(kbuf), smem_addr(vbuf), ct, tmem);
+    else if (warp == 13) walk_role(p, ct, plan);
   }
   tc_fence_before();
   block_sync();
