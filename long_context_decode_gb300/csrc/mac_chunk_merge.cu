@@ -2,12 +2,15 @@
 //
 // Pieces of disjoint keys with states (o, m, l), o and l relative to 2^m:
 //   M = max m;  out = sum 2^(m - M) o / sum 2^(m - M) l;  lse = M ln 2 + ln sum.
-// One CTA per (CTA of the attention kernel, 16 rows): it looks at that CTA's
-// note and is done if no cut unit starts there.  A warp takes two rows, four
-// dims per lane; lane j holds piece j's weight, so that the outputs are read
-// eight pieces at a time.  Bound by reading the partials (from L2) and by
-// the launch.  (Merged by the CTA that finished a unit's last piece, 256
-// rows of 4 pieces took 5 us and 128 rows of 5 pieces 60.)
+// One CTA per (CTA of the attention kernel, 8 rows): it looks at that CTA's
+// note and is done if no cut unit starts there.  A warp takes a row, four
+// dims per lane: lane j reads piece j's state while the outputs of the first
+// eight pieces are on their way, so that up to eight pieces cost one trip to
+// L2.  Bound by these trips and the launch: 5 us of the 48 us of an fp32 call
+// (two requests of up to 4096 tokens, 8 query and 2 KV heads); four rows per
+// warp in turn took 11.
+// (Merged by the CTA that finished a unit's last piece, 128 rows of five
+// pieces took 60 us.)
 #include <math.h>
 
 #include "mac_chunk.cuh"
@@ -15,73 +18,62 @@
 namespace mac {
 namespace {
 
-constexpr int kThr = 256, kR = 2, kRowsPerCta = kThr / 32 * kR;
+constexpr int kThr = 256, kRowsPerCta = kThr / 32, kBatch = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kThr) merge_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kThr, 4) merge_kernel(const __grid_constant__ ChunkParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31, r0 = blockIdx.y * kRowsPerCta + (threadIdx.x >> 5) * kR;
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int4 note = __ldcg(p.notes + c0);  // first token, KV head, rows, last CTA
-  if (r0 >= note.z) return;
   const int n = note.w - c0 + 1;
   const int64_t slot = (int64_t)p.part_rows * kChunkStride;  // floats per partial
-  auto piece = [&](int j, int i) { return p.part + (2 * (c0 + j) + (j == 0)) * slot + (int64_t)min(r0 + i, note.z - 1) * kChunkStride; };
-  float m[kR], l[kR];
-  float4 o[kR];
+  const int r = blockIdx.y * kRowsPerCta + (threadIdx.x >> 5);
+  if (r >= note.z) return;
+  const float *row = p.part + 2 * c0 * slot + (int64_t)r * kChunkStride;
+  auto piece = [&](int j) { return row + (2 * j + (j == 0)) * slot; };
+  auto state = [&](int j) {
+    return j < n ? __ldcg(reinterpret_cast<const float2 *>(piece(j) + kHeadDim)) : make_float2(-INFINITY, 0.f);
+  };
+  float4 v[kBatch];
+  auto outputs = [&](int j0) {
 #pragma unroll
-  for (int i = 0; i < kR; ++i) {
-    m[i] = -INFINITY;
-    for (int j = lane; j < n; j += 32) m[i] = fmaxf(m[i], __ldcg(piece(j, i) + kHeadDim));
+    for (int e = 0; e < kBatch; ++e) {
+      v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j0 + e < n) v[e] = __ldcg(reinterpret_cast<const float4 *>(piece(j0 + e)) + lane);
+    }
+  };
+  float2 ml = state(lane);
+  outputs(0);
+  float m = ml.x;
+  for (int j = 32 + lane; j < n; j += 32) m = fmaxf(m, state(j).x);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-    if (m[i] == -INFINITY) m[i] = 0.f;
-    l[i] = 0.f;
-    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (m == -INFINITY) m = 0.f;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j0 = 0; j0 < n; j0 += 32) {
-    float w[kR];
+    if (j0) ml = state(j0 + lane);
+    const float w = ex2(ml.x - m);
+    l = fmaf(w, ml.y, l);
+    for (int j = 0; j < min(32, n - j0); j += kBatch) {
+      if (j0 + j) outputs(j0 + j);
 #pragma unroll
-    for (int i = 0; i < kR; ++i) {
-      w[i] = 0.f;
-      if (j0 + lane < n) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(piece(j0 + lane, i) + kHeadDim));
-        w[i] = ex2(ml.x - m[i]);
-        l[i] = fmaf(w[i], ml.y, l[i]);
+      for (int e = 0; e < kBatch; ++e) {
+        const float x = __shfl_sync(0xffffffffu, w, j + e);
+        o.x = fmaf(x, v[e].x, o.x);
+        o.y = fmaf(x, v[e].y, o.y);
+        o.z = fmaf(x, v[e].z, o.z);
+        o.w = fmaf(x, v[e].w, o.w);
       }
     }
-    const int k = min(32, n - j0);
-    for (int j = 0; j < k; j += 8) {
-      float4 v[kR][8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-          v[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j + e < k) v[i][e] = __ldcg(reinterpret_cast<const float4 *>(piece(j0 + j + e, i)) + lane);
-        }
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-          const float x = __shfl_sync(0xffffffffu, w[i], (j + e) & 31);
-          o[i].x = fmaf(x, v[i][e].x, o[i].x);
-          o[i].y = fmaf(x, v[i][e].y, o[i].y);
-          o[i].z = fmaf(x, v[i][e].z, o[i].z);
-          o[i].w = fmaf(x, v[i][e].w, o[i].w);
-        }
-    }
   }
 #pragma unroll
-  for (int i = 0; i < kR; ++i) {
-    for (int d = 16; d; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-    const int r = r0 + i;
-    if (r >= note.z) break;
-    const int64_t row = (int64_t)(note.x + r / p.G) * p.Hq + note.y * p.G + r % p.G;
-    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-    store_out((T *)p.out + row * kHeadDim + lane * 4, make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv));
-    if (p.lse && lane == 0) p.lse[row] = l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
-  }
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  const int64_t at = (int64_t)(note.x + r / p.G) * p.Hq + note.y * p.G + r % p.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store_out((T *)p.out + at * kHeadDim + lane * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 }  // namespace
