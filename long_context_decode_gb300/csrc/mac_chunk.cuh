@@ -8,9 +8,12 @@
 // two cut ones, so rows of very different lengths, one long row and many
 // short ones all spread evenly.  A cut unit's pieces leave (o, max, sum)
 // partials and the CTA of its first tile a note of them; a second kernel
-// merges them in CTA order, so results do not depend on timing.  When there is a CTA for every unit and
-// all are short (kChunkShort tiles), each CTA takes one whole unit instead: a
-// merge would cost more than the cut saves.
+// merges them in CTA order, so results do not depend on timing.  When there
+// is a CTA for every unit and all are short (kChunkShort tiles), each CTA
+// takes one whole unit instead: a merge would cost more than the cut saves.
+// With HALF, units of half the rows are taken there if there is a CTA for each
+// of those as well: four requests of up to 60 tokens at 1000, 8 / 2 heads, 20.3
+// -> 15.4 us; three prompts of up to 500, 15.9 -> 13.1.
 #pragma once
 
 #include "mac_batch.cuh"
@@ -43,16 +46,20 @@ struct ChunkPiece {
   __device__ bool cut() const { return t0 > 0 || t1 < u.tiles; }
 };
 
-template <int ROWS, int KT, int COST0, int W, int WS>
+template <int ROWS, int KT, int COST0, int W, int WS, bool HALF>
 struct ChunkPlan {
   static constexpr int kKt = log2i(KT);
 
-  long long prefix[2][kMaxUnits + 1];  // cost (and units) of all requests before b, all KV heads
+  // of all requests before b, all KV heads: cost; units, those of half the rows
+  // in the upper 32 bits (used where no request has more than kChunkShort tiles of
+  // new tokens: no overflow)
+  long long prefix[2][kMaxUnits + 1];
   long long warp_tot[2][32];
   long long share;
   int any_bad, whole;
+  int lt, shift;  // log2 of the tokens per unit, place of its count
 
-  __device__ static int log_tokens(const ChunkParams &p) { return log2i(ROWS) - (31 - __clz(p.G)); }  // tokens per unit
+  __device__ long long axis(int b) const { return whole ? (uint32_t)(prefix[1][b] >> shift) : prefix[0][b]; }
   __device__ static int units(int n, int lt) { return (n + (1 << lt) - 1) >> lt; }
   __device__ static int weight(int n_tok, int lt) { return 2 * n_tok > 1 << lt ? W : WS; }
 
@@ -80,7 +87,7 @@ struct ChunkPlan {
   // All threads of the block (a multiple of 32, at most 1024) call it.
   // min_share: least cost worth a CTA of its own.
   __device__ void build(const ChunkParams &p, int min_share) {
-    const int lt = log_tokens(p), n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lt0 = log2i(ROWS) - (31 - __clz(p.G)), n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long sum[2] = {0, 0};  // cost, units
     int bad = 0, is_long = 0;
     if (threadIdx.x == 0) prefix[0][0] = prefix[1][0] = 0;
@@ -91,8 +98,8 @@ struct ChunkPlan {
         int a, n;
         bad |= request(p, b, &a, &n) != 0;
         is_long |= n > 0 && (((long long)a + n + KT - 1) >> kKt) > kChunkShort;
-        v[0] = cost(a, n, lt, false) * p.Hkv;
-        v[1] = cost(a, n, lt, true) * p.Hkv;
+        v[0] = cost(a, n, lt0, false) * p.Hkv;
+        v[1] = (units(n, lt0) + (HALF ? (long long)units(n, lt0 - 1) << 32 : 0)) * p.Hkv;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -116,9 +123,12 @@ struct ChunkPlan {
       if (b0 + n_thr < p.B) __syncthreads();
     }
     any_bad = __syncthreads_or(bad);  // (every thread writes the same; the barrier is the last one's too)
-    const bool each = !__syncthreads_or(is_long) && sum[1] <= gridDim.x;
+    const bool each = !__syncthreads_or(is_long) && (uint32_t)sum[1] <= gridDim.x;
     if (threadIdx.x == 0) {
+      const bool half = HALF && each && sum[1] >> 32 <= gridDim.x;
       whole = each;
+      lt = half ? lt0 - 1 : lt0;
+      shift = half ? 32 : 0;
       long long ctas = (int)min(sum[0], 1LL << 30) / min_share;
       if (ctas > gridDim.x) ctas = gridDim.x;
       if (ctas < 1) ctas = 1;
@@ -127,7 +137,7 @@ struct ChunkPlan {
     __syncthreads();
   }
 
-  __device__ bool has_work(const ChunkParams &p) const { return blockIdx.x * share < prefix[whole][p.B]; }
+  __device__ bool has_work(const ChunkParams &p) const { return blockIdx.x * share < axis(p.B); }
 
   // Lengths of request b: tokens before the new ones, new tokens (0: nothing
   // to attend).  Returns the status bits of a bad request; *rows, where
@@ -168,14 +178,12 @@ struct ChunkPlan {
   // The unit that holds position x of the axis in use.
   __device__ ChunkUnit find(const ChunkParams &p, long long x) const {
     ChunkUnit u;
-    const int lt = log_tokens(p);
     const bool by_units = whole;
-    const long long *pre = prefix[by_units];
-    u.b = last_not_above(p.B, x, [&](int b) { return pre[b]; });
+    u.b = last_not_above(p.B, x, [&](int b) { return axis(b); });
     request(p, u.b, &u.a, &u.n, &u.row0);
     const int a = u.a;
     const long long per = cost(a, u.n, lt, by_units);
-    long long rem = x - pre[u.b];
+    long long rem = x - axis(u.b);
     u.g = last_not_above(p.Hkv, rem, [&](int g) { return g * per; });
     rem -= u.g * per;
     const int i = last_not_above(units(u.n, lt), rem, [&](int k) { return before(a, lt, k, by_units); });
@@ -198,29 +206,29 @@ template <typename PLAN, int COST0, int W, int WS>
 struct ChunkWalk {
   long long x, end, share;
   ChunkUnit u;
+  int lt;
   bool first, whole;
 
   // A whole warp calls it, of a CTA with work.
   __device__ void start(const ChunkParams &p, const PLAN &plan) {
     share = plan.share;
     whole = plan.whole;
+    lt = plan.lt;
     x = blockIdx.x * share;
-    end = min(plan.prefix[whole][p.B], x + share);
+    end = min(plan.axis(p.B), x + share);
     first = true;
     u = plan.find(p, x);
   }
-  __device__ int weight(int lt) const { return PLAN::weight(u.n_tok, lt); }
   // Next piece with a tile; false when the CTA's work is done.
   __device__ bool next(const ChunkParams &p, ChunkPiece &q) {
-    const int lt = PLAN::log_tokens(p);
     while (x < end) {
-      if (!first) advance(p, lt);
+      if (!first) advance(p);
       first = false;
       int t0 = 0, t1 = u.tiles;
       if (whole) {
         x = u.at + 1;
       } else {
-        const int w = weight(lt);
+        const int w = PLAN::weight(u.n_tok, lt);
         auto first_tile = [&](long long y) { return (int)(w == W ? (y + W - 1) / W : (y + WS - 1) / WS); };
         if (x > u.at) t0 = first_tile(x - u.at);
         if (end < u.at + (long long)u.tiles * w) t1 = end > u.at ? first_tile(end - u.at) : 0;
@@ -235,14 +243,14 @@ struct ChunkWalk {
     return false;
   }
   // CTAs that hold the pieces of a cut unit: the one of its first tile, and of its last.
-  __device__ int cta_of(const ChunkParams &p, const ChunkUnit &v, int tile) const {
-    return (int)((v.at + (long long)tile * PLAN::weight(v.n_tok, PLAN::log_tokens(p))) / share);
+  __device__ int cta_of(const ChunkUnit &v, int tile) const {
+    return (int)((v.at + (long long)tile * PLAN::weight(v.n_tok, lt)) / share);
   }
 
  private:
   // The unit after u (there is one).
-  __device__ void advance(const ChunkParams &p, int lt) {
-    const long long at = u.at + (whole ? 1 : (long long)u.tiles * weight(lt) + COST0);
+  __device__ void advance(const ChunkParams &p) {
+    const long long at = u.at + (whole ? 1 : (long long)u.tiles * PLAN::weight(u.n_tok, lt) + COST0);
     int i = u.i + 1;
     if (i << lt >= u.n) {
       i = 0;

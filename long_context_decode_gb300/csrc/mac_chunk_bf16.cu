@@ -41,7 +41,7 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThr * 168, "the split co
 constexpr int kStK = 2, kStV = 3, kNSt = kStK + kStV;  // stages of the K ring and of the V ring
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr float kLazy = 8.f;                  // growth of the maximum (base 2) that moves the reference
-using Plan = ChunkPlan<kChunkRowsBf16, kTile, kCost0, kW, kWs>;
+using Plan = ChunkPlan<kChunkRowsBf16, kTile, kCost0, kW, kWs, true>;
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -358,8 +358,8 @@ __device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, co
       q.end0 = min(x.t1, (u.pos0 + kTile / p.G - 1 + kTile - 1) / kTile);
       q.pair = u.n_tok * p.G <= kTile;
       q.clear = x.t1 == u.tiles ? min(kTile, u.a + u.n - (x.t1 - 1) * kTile) : kTile;
-      q.c0 = cut ? walk.cta_of(p, u, 0) : -1;
-      q.c1 = cut ? walk.cta_of(p, u, u.tiles - 1) : -1;
+      q.c0 = cut ? walk.cta_of(u, 0) : -1;
+      q.c1 = cut ? walk.cta_of(u, u.tiles - 1) : -1;
     }
     ct->pieces.post(wait, i, q);
     if (clear < kTile && wait(&ct->tail, nt & 1)) {

@@ -45,7 +45,7 @@ constexpr int kRegsLaunch = 128, kRegsSoft = 232, kRegsSplit = 104, kRegsMma = 7
 static_assert(kRegsSoft + 2 * kRegsSplit + kRegsMma <= 4 * kRegsLaunch && kThr * kRegsLaunch <= 65536, "the split comes out of the launch's registers");
 constexpr int kQPart = kRows * kHeadDim * 2, kKvPart = kKeys * kHeadDim * 2;  // bytes of one bf16 part of a tile
 constexpr uint32_t kColS = 0, kColS1 = 64, kColP = 128, kColO = 256;  // TMEM columns: S twice, P, P V
-using Plan = ChunkPlan<kRows, kKeys, kCost0, 1, 1>;
+using Plan = ChunkPlan<kRows, kKeys, kCost0, 1, 1, false>;
 
 // A piece of a unit, as the roles see it.
 struct Piece {
@@ -261,7 +261,7 @@ __device__ void walk_role(const ChunkParams &p, Control *ct, const Plan &plan) {
     if (more) {
       const ChunkUnit &u = x.u;
       const bool cut = x.cut();
-      q = {u.b, u.g, u.tok0, u.n_tok, u.pos0, x.t0, x.t1, cut ? walk.cta_of(p, u, 0) : -1, cut ? walk.cta_of(p, u, u.tiles - 1) : -1};
+      q = {u.b, u.g, u.tok0, u.n_tok, u.pos0, x.t0, x.t1, cut ? walk.cta_of(u, 0) : -1, cut ? walk.cta_of(u, u.tiles - 1) : -1};
     }
     ct->pieces.post(wait, i, q);
     if (!more || wait.dead) return;

@@ -455,6 +455,18 @@ def test_chunk_drawn(seed):
     b.check()
 
 
+# 129 to 256 rows per request and head: one unit or two of half the rows, by the number of SMs
+@pytest.mark.parametrize("Hq,Hkv,new", [
+    (4, 1, [33] * (torch.cuda.get_device_properties(0).multi_processor_count // 2 if torch.cuda.is_available() else 1)),
+    (4, 1, [33] * (torch.cuda.get_device_properties(0).multi_processor_count // 2 + 1 if torch.cuda.is_available() else 1)),
+    (8, 2, [64, 32, 65, 0, 33, 63]), (2, 2, [129, 256, 257, 1]), (16, 2, [17, 32, 33])])
+def test_chunk_units_of_half_the_rows(Hq, Hkv, new):
+    b = Batch([(i * 97) % 500 for i in range(len(new))], new, Hq, Hkv, BF16, True, seed=6, pad=2)
+    b.run()
+    assert b.status() == 0
+    b.check()
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_chunk_many_requests(dt):
     rng = random.Random(1)
