@@ -211,6 +211,10 @@ __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stage
 // products ahead, so whatever this warp does between the last product of one
 // group and the first of the other must be short: waits come where products
 // are still running, and one whose phase has already come costs one test.
+// A branch between two products costs more than code: both groups' products
+// from one rolled copy took 711 us for 2048 tokens at 32768 (32 / 8 heads)
+// where this takes 656.  The code that a short prompt fetches for a few tiles
+// is what that would have saved (six prompts of up to 900 tokens: 77 -> 71 us).
 struct RingPos {
   uint32_t st, phase;  // stage, parity of its next completion
   __device__ void step(uint32_t first, uint32_t n) {
@@ -428,15 +432,16 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
       tc_wait_ld();
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) tc_loaded32(s + c);
-      if (key0 + kTile > q.pos0) {  // some row of the unit does not attend the whole tile
+      if (key0 + kTile > q.pos0 || (PAGED && gone)) {  // some row of the unit does not attend the whole tile (one mask for
+        // both reasons: with two the loop's code took 668 us for 2048 tokens at 32768, now 656)
+        if (PAGED && gone) status |= MAC_DEV_BAD_PAGE;
         const int left = lim - key0;
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) s[c] = c < left ? s[c] : -INFINITY;
-      }
-      if (PAGED && gone) {
-        status |= MAC_DEV_BAD_PAGE;
+        for (int pg = 0; pg < kTile / kPage; ++pg) {
+          const int of_page = PAGED && (gone >> pg & 1) ? 0 : left;  // keys attended end here
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) s[c] = (gone >> (c / kPage)) & 1 ? -INFINITY : s[c];
+          for (int c = pg * kPage; c < (pg + 1) * kPage; ++c) s[c] = c < of_page ? s[c] : -INFINITY;
+        }
       }
       float mx[4] = {fmaxf(s[0], s[4]), fmaxf(s[1], s[5]), fmaxf(s[2], s[6]), fmaxf(s[3], s[7])};
 #pragma unroll
