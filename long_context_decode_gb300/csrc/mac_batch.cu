@@ -384,9 +384,10 @@ cudaError_t launch_write(const WriteParams &p, int dtype, cudaStream_t s) {
   // 8679 rows of 32 + 2 x 8 bf16 heads: 34.8 us (6.1 TB/s); with four rows of
   // 256 threads 36.4, two rows of 256 threads 39.5, one row of 256 threads 53.
   // 2160 rows of 32 + 2 x 4 fp32 heads: 15.9 us; two rows per CTA 17.0.
-  // Few rows leave SMs idle either way and take one CTA each.
+  // Fewer bf16 rows take a CTA each: 608 rows 4.1 us (two per CTA: 6.0), 1216
+  // 5.7 (6.3), 2400 8.6 (8.5).
   if (dtype == MAC_F32) return launch_write_t<float, 1>(p, s);
-  return p.T <= 608 ? launch_write_t<uint16_t, 1>(p, s) : launch_write_t<uint16_t, 2>(p, s);
+  return p.T <= 2048 ? launch_write_t<uint16_t, 1>(p, s) : launch_write_t<uint16_t, 2>(p, s);
 }
 
 }  // namespace mac

@@ -59,10 +59,25 @@ struct ChunkParams {
 };
 
 constexpr int kChunkGrid = 256;   // most CTAs of a launch (one per SM)
-constexpr int kChunkRowsBf16 = 256, kChunkRowsF32 = 128;  // rows per unit
+// What the plan of a chunk attention launch counts with, per kernel: rows of
+// a unit, keys of a tile, and costs: a unit's start and end, a key tile of
+// a unit and of one of at most half the rows, the least worth a CTA of its
+// own, and what cutting units costs a launch (partials, notes, the merge).
+// bf16, in quarters of a full unit's tile (2900 cycles): half the rows compute
+// half as much per tile but copy as much; a start and end cost as three tiles.
+// fp32: in tiles (7200 cycles).
+struct ChunkBf16 {
+  static constexpr int kRows = 256, kKeys = 128;
+  static constexpr int kStart = 12, kTile = 4, kTileHalf = 3, kMinShare = 16, kCut = 35;
+  static constexpr bool kHalves = true;  // units of half the rows, where there are CTAs for all of them
+};
+struct ChunkF32 {
+  static constexpr int kRows = 128, kKeys = 64;
+  static constexpr int kStart = 3, kTile = 1, kTileHalf = 1, kMinShare = 4, kCut = 4;
+  static constexpr bool kHalves = false;
+};
 constexpr int kChunkStride = kHeadDim + 8;  // floats per row of a partial: o[d], m, l, and to a multiple of 32 bytes
 constexpr int kMaxTokens = 1 << 24;
-constexpr int kChunkShort = 8;    // key tiles of a short unit
 
 // Launch with programmatic stream serialization: the kernel may start while
 // the previous one on the stream finishes, and waits (griddep_wait) before it

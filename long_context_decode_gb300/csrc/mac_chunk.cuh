@@ -2,18 +2,18 @@
 // over the CTAs, shared by the bf16 (tensor core) and fp32 kernels.
 //
 // Units are laid end to end in order (request, KV head, row tile) on a cost
-// axis: a unit costs COST0 plus W per tile of KT keys that its last row
-// attends (WS for a unit of at most half the rows).  CTA c works on
-// positions [c share, (c+1) share): any number of whole units and at most
-// two cut ones, so rows of very different lengths, one long row and many
-// short ones all spread evenly.  A cut unit's pieces leave (o, max, sum)
-// partials and the CTA of its first tile a note of them; a second kernel
-// merges them in CTA order, so results do not depend on timing.  When there
-// is a CTA for every unit and all are short (kChunkShort tiles), each CTA
-// takes one whole unit instead: a merge would cost more than the cut saves.
-// With HALF, units of half the rows are taken there if there is a CTA for each
-// of those as well: four requests of up to 60 tokens at 1000, 8 / 2 heads, 20.3
-// -> 15.4 us; three prompts of up to 500, 15.9 -> 13.1.
+// axis (ChunkBf16, ChunkF32: a unit's start plus its key tiles, as many as its
+// last row attends).  CTA c works on positions [c share, (c+1) share): any
+// number of whole units and at most two cut ones, so rows of very different
+// lengths, one long row and many short ones all spread evenly.  A cut unit's
+// pieces leave (o, max, sum) partials and the CTA of its first tile a note of
+// them; a second kernel merges them in CTA order, so results do not depend on
+// timing.  When there is a CTA for every unit and the longest is done before
+// an equal share and what cutting costs, each CTA takes one whole unit
+// instead, of half the rows if there are CTAs for those as well (us, cut and
+// whole): 4 chunks of 60 tokens at 1000, 8 / 2 heads, 22.4 and 16.7; 12 at 1200,
+// 32 / 8 heads, 36.6 and 29.8; 16 single tokens at 1100, 21.7 and 17.3; but two
+// single tokens at 1900, few and long, 16.4 and 21.1.
 #pragma once
 
 #include "mac_batch.cuh"
@@ -46,13 +46,15 @@ struct ChunkPiece {
   __device__ bool cut() const { return t0 > 0 || t1 < u.tiles; }
 };
 
-template <int ROWS, int KT, int COST0, int W, int WS, bool HALF>
+template <typename C>
 struct ChunkPlan {
+  static constexpr int ROWS = C::kRows, KT = C::kKeys, COST0 = C::kStart, W = C::kTile, WS = C::kTileHalf;
   static constexpr int kKt = log2i(KT);
 
   // of all requests before b, all KV heads: cost; units, those of half the rows
-  // in the upper 32 bits (used where no request has more than kChunkShort tiles of
-  // new tokens: no overflow)
+  // in the upper 32 bits (counted up to kMany per request and head: used only
+  // where all requests together have fewer)
+  static constexpr int kMany = 2 * kChunkGrid;
   long long prefix[2][kMaxUnits + 1];
   long long warp_tot[2][32];
   long long share;
@@ -85,11 +87,10 @@ struct ChunkPlan {
   }
 
   // All threads of the block (a multiple of 32, at most 1024) call it.
-  // min_share: least cost worth a CTA of its own.
-  __device__ void build(const ChunkParams &p, int min_share) {
+  __device__ void build(const ChunkParams &p) {
     const int lt0 = log2i(ROWS) - (31 - __clz(p.G)), n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long sum[2] = {0, 0};  // cost, units
-    int bad = 0, is_long = 0;
+    int bad = 0, top = 0, top_half = 0;  // highest cost of a unit
     if (threadIdx.x == 0) prefix[0][0] = prefix[1][0] = 0;
     for (int b0 = 0; b0 < p.B; b0 += n_thr) {
       const int b = b0 + threadIdx.x;
@@ -97,9 +98,13 @@ struct ChunkPlan {
       if (b < p.B) {
         int a, n;
         bad |= request(p, b, &a, &n) != 0;
-        is_long |= n > 0 && (((long long)a + n + KT - 1) >> kKt) > kChunkShort;
+        if (n > 0) {
+          const int tiles = (int)(((long long)a + n + KT - 1) >> kKt);
+          top = max(top, COST0 + tiles * weight(n, lt0));
+          top_half = max(top_half, COST0 + tiles * WS);
+        }
         v[0] = cost(a, n, lt0, false) * p.Hkv;
-        v[1] = (units(n, lt0) + (HALF ? (long long)units(n, lt0 - 1) << 32 : 0)) * p.Hkv;
+        v[1] = (min(units(n, lt0), kMany) + (C::kHalves ? (long long)min(units(n, lt0 - 1), kMany) << 32 : 0)) * p.Hkv;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -123,16 +128,17 @@ struct ChunkPlan {
       if (b0 + n_thr < p.B) __syncthreads();
     }
     any_bad = __syncthreads_or(bad);  // (every thread writes the same; the barrier is the last one's too)
-    const bool each = !__syncthreads_or(is_long) && (uint32_t)sum[1] <= gridDim.x;
+    long long ctas = (int)min(sum[0], 1LL << 30) / C::kMinShare;
+    if (ctas > gridDim.x) ctas = gridDim.x;
+    if (ctas < 1) ctas = 1;
+    const long long even = max(1LL, (sum[0] + ctas - 1) / ctas);
+    const bool half = C::kHalves && !__syncthreads_or(top_half > even + C::kCut) && sum[1] >> 32 <= gridDim.x;
+    const bool each = half || (!__syncthreads_or(top > even + C::kCut) && (uint32_t)sum[1] <= gridDim.x);
     if (threadIdx.x == 0) {
-      const bool half = HALF && each && sum[1] >> 32 <= gridDim.x;
       whole = each;
       lt = half ? lt0 - 1 : lt0;
       shift = half ? 32 : 0;
-      long long ctas = (int)min(sum[0], 1LL << 30) / min_share;
-      if (ctas > gridDim.x) ctas = gridDim.x;
-      if (ctas < 1) ctas = 1;
-      share = each ? 1 : max(1LL, (sum[0] + ctas - 1) / ctas);
+      share = each ? 1 : even;
     }
     __syncthreads();
   }
@@ -202,8 +208,10 @@ struct ChunkPlan {
 };
 
 // A CTA's walk through its pieces.
-template <typename PLAN, int COST0, int W, int WS>
+template <typename C>
 struct ChunkWalk {
+  using PLAN = ChunkPlan<C>;
+  static constexpr int COST0 = C::kStart, W = C::kTile, WS = C::kTileHalf;
   long long x, end, share;
   ChunkUnit u;
   int lt;

@@ -31,17 +31,14 @@ namespace mac {
 namespace {
 
 constexpr int kTile = 128;                    // rows of a row tile, keys of a key tile
-// Costs in quarters of a full unit's key tile.  A unit of at most 128 rows
-// computes half as much per tile, but copies as much; a unit's start and end
-// cost as much as three tiles.
-constexpr int kCost0 = 12, kW = 4, kWs = 3, kMinShare = 16;
 constexpr int kThr = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;  // registers per thread once the roles have split
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThr * 168, "the split comes out of the launch's registers");
 constexpr int kStK = 2, kStV = 3, kNSt = kStK + kStV;  // stages of the K ring and of the V ring
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr float kLazy = 8.f;                  // growth of the maximum (base 2) that moves the reference
-using Plan = ChunkPlan<kChunkRowsBf16, kTile, kCost0, kW, kWs, true>;
+static_assert(ChunkBf16::kRows == 2 * kTile && ChunkBf16::kKeys == kTile, "tiles");
+using Plan = ChunkPlan<ChunkBf16>;
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -340,7 +337,7 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
 __device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, const Plan &plan) {
   const int lane = threadIdx.x & 31;
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
-  ChunkWalk<Plan, kCost0, kW, kWs> walk;
+  ChunkWalk<ChunkBf16> walk;
   walk.start(p, plan);
   fence_proxy_async();  // the plan has been read: its place is the stages'
   uint32_t nt = 0, last_v = 0;  // tiles cleared; V uses before the next piece
@@ -627,7 +624,7 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   griddep_wait();  // from here on the previous kernel's writes are read
   // this CTA's part of the work, the plan made where the stages go
   Plan &plan = *reinterpret_cast<Plan *>(smem);
-  plan.build(p, kMinShare);
+  plan.build(p);
   if (plan.any_bad) chunk_bad_requests<uint16_t, Plan>(p);
   const bool work = plan.has_work(p);
   fence_proxy_async();  // copies into the stages come after this

@@ -38,14 +38,13 @@
 namespace mac {
 namespace {
 
-constexpr int kRows = kChunkRowsF32, kKeys = 64;
-constexpr int kCost0 = 3, kMinShare = 4;            // costs in key tiles
+constexpr int kRows = ChunkF32::kRows, kKeys = ChunkF32::kKeys;
 constexpr int kThr = 512, kConv = kKeys / kPage;    // threads; warps that split K (V): one for each page of a tile
 constexpr int kRegsLaunch = 128, kRegsSoft = 232, kRegsSplit = 104, kRegsMma = 72;  // registers per thread
 static_assert(kRegsSoft + 2 * kRegsSplit + kRegsMma <= 4 * kRegsLaunch && kThr * kRegsLaunch <= 65536, "the split comes out of the launch's registers");
 constexpr int kQPart = kRows * kHeadDim * 2, kKvPart = kKeys * kHeadDim * 2;  // bytes of one bf16 part of a tile
 constexpr uint32_t kColS = 0, kColS1 = 64, kColP = 128, kColO = 256;  // TMEM columns: S twice, P, P V
-using Plan = ChunkPlan<kRows, kKeys, kCost0, 1, 1, false>;
+using Plan = ChunkPlan<ChunkF32>;
 
 // A piece of a unit, as the roles see it.
 struct Piece {
@@ -252,7 +251,7 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
 // ---- the walk (warp 13) -----------------------------------------------------------
 __device__ void walk_role(const ChunkParams &p, Control *ct, const Plan &plan) {
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
-  ChunkWalk<Plan, kCost0, 1, 1> walk;
+  ChunkWalk<ChunkF32> walk;
   walk.start(p, plan);
   for (uint32_t i = 0;; ++i) {
     ChunkPiece x = {};
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   }
   griddep_wait();  // from here on the previous kernel's writes are read
   Plan &plan = *reinterpret_cast<Plan *>(kbuf);  // made where the K and V tiles go
-  plan.build(p, kMinShare);
+  plan.build(p);
   if (plan.any_bad) chunk_bad_requests<float, Plan>(p);
   const bool work = plan.has_work(p);
   tc_fence_before();

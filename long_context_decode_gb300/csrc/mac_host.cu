@@ -251,7 +251,7 @@ struct ChunkLayout {
 ChunkLayout chunk_layout(const mac_config *c, int32_t n_tokens) {
   const bool f32 = c->dtype == MAC_F32;
   const int64_t rows = (int64_t)n_tokens * (c->n_q_heads / c->n_kv_heads);
-  const int unit = f32 ? kChunkRowsF32 : kChunkRowsBf16;
+  const int unit = f32 ? ChunkF32::kRows : ChunkBf16::kRows;
   ChunkLayout L;
   L.part_rows = (int)(rows < unit ? rows : unit);
   size_t off = 0;
@@ -730,11 +730,16 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
   const bool f32 = cfg->dtype == MAC_F32;
   const int grid = sms < kChunkGrid ? sms : kChunkGrid;
   if ((f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s)) != cudaSuccess) return MAC_ERR_CUDA;
-  // No unit can be cut when a CTA is there for each and none is long,
-  // whatever the lengths on the device: then nothing needs merging.
-  const int64_t unit_tokens = (f32 ? kChunkRowsF32 : kChunkRowsBf16) / p.G, tile = f32 ? 64 : 128;
-  const int64_t units = (n_tokens / unit_tokens + p.B) * p.Hkv;
-  if (units <= grid && p.max_len <= kChunkShort * tile) return MAC_OK;
+  // No unit is cut when a CTA is there for each and none is long, whatever
+  // the lengths on the device: then nothing needs merging.
+  auto each = [&](auto c, int rows, int tile_cost) {
+    using C = decltype(c);
+    const int64_t tiles = (C::kMinShare + C::kCut - C::kStart) / tile_cost;  // an equal share is at least kMinShare
+    return (n_tokens / (rows / p.G) + (int64_t)p.B) * p.Hkv <= grid && p.max_len <= tiles * C::kKeys;
+  };
+  if (f32 ? each(ChunkF32{}, ChunkF32::kRows, ChunkF32::kTile)
+          : each(ChunkBf16{}, ChunkBf16::kRows, ChunkBf16::kTile) || each(ChunkBf16{}, ChunkBf16::kRows / 2, ChunkBf16::kTileHalf))
+    return MAC_OK;
   return launch_chunk_merge(p, grid, f32, s) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
 }
 
