@@ -467,6 +467,17 @@ def test_chunk_units_of_half_the_rows(Hq, Hkv, new):
     b.check()
 
 
+# a CTA for every unit; units of many tiles, alike (taken whole) and very unlike (cut)
+@pytest.mark.parametrize("dt,Hq,Hkv,ctx,new", [
+    (BF16, 32, 8, [1200] * 12, [60] * 12), (BF16, 32, 8, [3000, 10, 0, 700], [60, 64, 1, 65]), (BF16, 8, 8, [2500] * 16, [1] * 16),
+    (F32, 4, 2, [700] * 16, [60] * 16), (F32, 8, 2, [2000, 5, 64, 300], [20, 32, 1, 33])])
+def test_chunk_a_cta_for_each_unit(dt, Hq, Hkv, ctx, new):
+    b = Batch(ctx, new, Hq, Hkv, dt, True, seed=8, pad=1)
+    b.run()
+    assert b.status() == 0
+    b.check()
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_chunk_many_requests(dt):
     rng = random.Random(1)
