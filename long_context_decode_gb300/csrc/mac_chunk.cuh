@@ -58,7 +58,8 @@ struct ChunkPlan {
   long long prefix[2][kMaxUnits + 1];
   long long warp_tot[2][32];
   long long share;
-  int any_bad, whole;
+  int whole;
+  int flags;  // 1: a bad request; 2, 4: a unit, one of half the rows, too long to be taken whole
   int lt, shift;  // log2 of the tokens per unit, place of its count
 
   __device__ long long axis(int b) const { return whole ? (uint32_t)(prefix[1][b] >> shift) : prefix[0][b]; }
@@ -91,7 +92,7 @@ struct ChunkPlan {
     const int lt0 = log2i(ROWS) - (31 - __clz(p.G)), n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long sum[2] = {0, 0};  // cost, units
     int bad = 0, top = 0, top_half = 0;  // highest cost of a unit
-    if (threadIdx.x == 0) prefix[0][0] = prefix[1][0] = 0;
+    if (threadIdx.x == 0) prefix[0][0] = prefix[1][0] = flags = 0;
     for (int b0 = 0; b0 < p.B; b0 += n_thr) {
       const int b = b0 + threadIdx.x;
       long long v[2] = {0, 0};
@@ -127,22 +128,26 @@ struct ChunkPlan {
       }
       if (b0 + n_thr < p.B) __syncthreads();
     }
-    any_bad = __syncthreads_or(bad);  // (every thread writes the same; the barrier is the last one's too)
     long long ctas = (int)min(sum[0], 1LL << 30) / C::kMinShare;
     if (ctas > gridDim.x) ctas = gridDim.x;
     if (ctas < 1) ctas = 1;
-    const long long even = max(1LL, (sum[0] + ctas - 1) / ctas);
-    const bool half = C::kHalves && !__syncthreads_or(top_half > even + C::kCut) && sum[1] >> 32 <= gridDim.x;
-    const bool each = half || (!__syncthreads_or(top > even + C::kCut) && (uint32_t)sum[1] <= gridDim.x);
+    auto too_long = [&](int cost) { return (cost - C::kCut - 1) * ctas >= sum[0]; };  // cost > ceil(sum / ctas) + kCut
+    const int mine = (bad ? 1 : 0) | (too_long(top) ? 2 : 0) | (too_long(top_half) ? 4 : 0);
+    const int of_warp = __reduce_or_sync(0xffffffffu, mine);
+    if (lane == 0 && of_warp) atomicOr(&flags, of_warp);
+    __syncthreads();
+    const bool half = C::kHalves && !(flags & 4) && sum[1] >> 32 <= gridDim.x;
+    const bool each = half || (!(flags & 2) && (uint32_t)sum[1] <= gridDim.x);
     if (threadIdx.x == 0) {
       whole = each;
       lt = half ? lt0 - 1 : lt0;
       shift = half ? 32 : 0;
-      share = each ? 1 : even;
+      share = each ? 1 : max(1LL, (sum[0] + ctas - 1) / ctas);
     }
     __syncthreads();
   }
 
+  __device__ bool any_bad() const { return flags & 1; }
   __device__ bool has_work(const ChunkParams &p) const { return blockIdx.x * share < axis(p.B); }
 
   // Lengths of request b: tokens before the new ones, new tokens (0: nothing

@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   // this CTA's part of the work, the plan made where the stages go
   Plan &plan = *reinterpret_cast<Plan *>(smem);
   plan.build(p);
-  if (plan.any_bad) chunk_bad_requests<uint16_t, Plan>(p);
+  if (plan.any_bad()) chunk_bad_requests<uint16_t, Plan>(p);
   const bool work = plan.has_work(p);
   fence_proxy_async();  // copies into the stages come after this
   tc_fence_before();

@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   griddep_wait();  // from here on the previous kernel's writes are read
   Plan &plan = *reinterpret_cast<Plan *>(kbuf);  // made where the K and V tiles go
   plan.build(p);
-  if (plan.any_bad) chunk_bad_requests<float, Plan>(p);
+  if (plan.any_bad()) chunk_bad_requests<float, Plan>(p);
   const bool work = plan.has_work(p);
   tc_fence_before();
   block_sync();
