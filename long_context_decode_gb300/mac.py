@@ -244,7 +244,7 @@ def _row_stride(t, heads, head_dim) -> int:
     st = t.stride()
     if (st[1] != head_dim and t.shape[1] != 1) or st[2] != 1:
         raise MacError("mac_write_kv: a row's heads must lie end to end")
-    return st[0]
+    return st[0] if t.shape[0] != 1 else heads * head_dim  # (one row's stride may be anything)
 
 
 def mac_write_kv(cfg, chunk_ws, q, k, v, pos, slot, n_tokens, kv: mac_kv, q_out, stream=None):

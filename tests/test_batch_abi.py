@@ -91,6 +91,16 @@ def test_write_kv_refuses_rows_whose_heads_are_apart(mac):
         mac.mac_write_kv(cfg, 256, x[..., :128], k, k, 256, 256, 4, kv, 512)
 
 
+def test_row_stride_of_views(mac):
+    torch = pytest.importorskip("torch")
+    fused = torch.zeros(5, 12, 128, dtype=torch.bfloat16)
+    assert mac._row_stride(fused[:, 8:10], 2, 128) == 12 * 128
+    assert mac._row_stride(torch.zeros(5, 2, 128), 2, 128) == 256
+    # one row of a cache-like [heads, T, d] tensor: its row stride says nothing
+    assert mac._row_stride(torch.zeros(2, 1, 128).transpose(0, 1), 2, 128) == 256
+    assert mac._row_stride(4096, 2, 128) == 256
+
+
 def test_chunk_attention_refusals(mac):
     INV, UNS = mac.MAC_ERR_INVALID_ARG, mac.MAC_ERR_UNSUPPORTED
     cfg = mac.config(2, 8, 2, max_context=4096)
