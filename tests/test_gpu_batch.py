@@ -267,6 +267,14 @@ def test_write(T, Hq, Hkv, paged, fused, with_q, dt, mode):
     assert (q_out[~live] == 7).all() and (with_q or (q_out == 7).all())
 
 
+# bf16 rows past 2048 go two to a CTA; the last CTA of an odd number has one
+@pytest.mark.parametrize("mode", [mac.MAC_ROPE_HALF, mac.MAC_ROPE_INTERLEAVED, mac.MAC_ROPE_NONE])
+@pytest.mark.parametrize("T,Hq,Hkv,paged,fused,with_q", [
+    (2048, 8, 2, True, True, True), (2049, 8, 2, True, False, True), (2501, 12, 3, False, True, True), (4000, 1, 1, True, False, False)])
+def test_write_many_rows(T, Hq, Hkv, paged, fused, with_q, mode):
+    test_write(T, Hq, Hkv, paged, fused, with_q, BF16, mode)
+
+
 def test_write_in_place_and_rows_refused_on_the_device():
     cfg = mac.config(1, 8, 2, page_size=PAGE, max_context=4096)
     T = 6
