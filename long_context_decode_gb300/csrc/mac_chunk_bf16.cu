@@ -200,14 +200,12 @@ __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stage
       }
     }
   }
-  // After a wait ran out, copies may still be in flight: let them land
-  // before the CTA gives its shared memory up.
-  if (*(volatile int *)&ct->abort) {
-    const int dummy = 0;
-    for (int u = use > NST ? use - NST : 0; u < use; ++u)
-      mbar_wait_bounded(smem_addr(&ct->full[ST0 + u % NST]), (u / NST) & 1, (volatile int *)&dummy, p.wait_limit);
-    if (nq) mbar_wait_bounded(smem_addr(&ct->q_full), (nq - 1) & 1, (volatile int *)&dummy, p.wait_limit);
-  }
+  // The last copies of every stage land before the CTA gives its shared memory
+  // up.  Where all is well they have; another role may give up (and end the CTA)
+  // after this warp is through, so this does not go by ct->abort.
+  for (int u = use > NST ? use - NST : 0; u < use; ++u)
+    if (!IS_K || u != p.withhold) drained(&ct->full[ST0 + u % NST], (u / NST) & 1);
+  if (nq) drained(&ct->q_full, (nq - 1) & 1);
 }
 
 // ---- products (warp 9) -----------------------------------------------------------
@@ -328,9 +326,8 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
     }
   }
   // every product has ended before the CTA gives its memory up
-  const int dummy = 0;
   tc_commit(smem_addr(&ct->drain));
-  if (!mbar_wait_bounded(smem_addr(&ct->drain), 0, (volatile int *)&dummy, p.wait_limit)) {
+  if (!drained(&ct->drain, 0)) {
     *(volatile int *)&ct->abort = 1;
     set_status(p.status, MAC_DEV_WAIT_TIMEOUT);
   }

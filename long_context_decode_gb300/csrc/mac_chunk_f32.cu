@@ -144,9 +144,8 @@ __device__ void mma_role(const ChunkParams &p, uint32_t qbuf, uint32_t kbuf, uin
     }
   }
   // every product has ended before the CTA gives its memory up
-  const int dummy = 0;
   tc_commit(smem_addr(&ct->drain));
-  if (!mbar_wait_bounded(smem_addr(&ct->drain), 0, (volatile int *)&dummy, p.wait_limit)) {
+  if (!drained(&ct->drain, 0)) {
     *(volatile int *)&ct->abort = 1;
     set_status(p.status, MAC_DEV_WAIT_TIMEOUT);
   }

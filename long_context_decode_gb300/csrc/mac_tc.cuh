@@ -137,6 +137,16 @@ struct Waiter {
   }
 };
 
+// Before a CTA gives its shared memory and TMEM up, everything that writes or
+// reads them has ended: the phase of `parity` of `bar`, waited for even after
+// a wait has run out, and for about half a second whatever limit the other
+// waits were given (a copy or product that was issued ends within microseconds).
+constexpr long long kDrainLimit = 1LL << 30;
+__device__ __forceinline__ bool drained(unsigned long long *bar, uint32_t parity) {
+  const int never = 0;
+  return mbar_wait_bounded(smem_addr(bar), parity, (volatile int *)&never, kDrainLimit);
+}
+
 // The pieces of a CTA, from the one warp that works them out to the warps of
 // the other roles (`readers` of them): a short ring in shared memory.  The
 // walk's code runs in one place only, ahead of its use; in every role it was

@@ -602,6 +602,31 @@ def test_chunk_wait_runs_out(dt, use, paged, new):
     b.check()
 
 
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("use", [-1, 0, 2])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_chunk_gives_up_at_once_with_work_in_flight(dt, use, paged):
+    # a budget of one cycle: every wait that is not over already gives up while copies and products that were
+    # issued are in flight.  The launch returns when those have ended, so the launches right behind it, on
+    # workspaces of their own, find shared memory and TMEM free and are right.
+    b = Batch([3000, 700, 90], [200, 1, 64], 8, 2, dt, paged, seed=10)
+    b.run()
+    assert b.status() == 0
+    b.check()
+    ref, bad = b.out.clone(), workspace(b.cfg, b.T)
+    good = b.ws
+    for _ in range(10):
+        b.ws = bad
+        bad.zero_()
+        mac.mac_test_wait_budget(1, use)
+        b.run()
+        b.ws = good
+        b.run()
+        assert torch.equal(b.out, ref) and b.status() == 0
+        if use >= 0:
+            assert mac.mac_last_status(b.cfg, bad) & mac.MAC_DEV_WAIT_TIMEOUT
+
+
 def test_chunk_output_on_any_16_byte_boundary():
     b = Batch([50], [70], 8, 2, BF16, True, seed=6)
     b.run()
