@@ -367,6 +367,7 @@ __device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, co
       q.c1 = cut ? walk.cta_of(u, u.tiles - 1) : -1;
     }
     ct->pieces.post(wait, i, q);
+    wait.limit += (long long)(q.t1 - q.t0) << kTileLimitLog;
     if (clear < kTile && wait(&ct->tail, nt & 1)) {
       ++nt;
       uint8_t *v = stages + (kStK + (last_v + kStV - 1) % kStV) * kTileBytes;

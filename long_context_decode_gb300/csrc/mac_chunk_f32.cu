@@ -262,6 +262,7 @@ __device__ void walk_role(const ChunkParams &p, Control *ct, const Plan &plan) {
       q = {u.b, u.g, u.tok0, u.n_tok, u.pos0, x.t0, x.t1, cut ? walk.cta_of(u, 0) : -1, cut ? walk.cta_of(u, u.tiles - 1) : -1};
     }
     ct->pieces.post(wait, i, q);
+    wait.limit += (long long)(q.t1 - q.t0) << kTileLimitLog;
     if (!more || wait.dead) return;
   }
 }

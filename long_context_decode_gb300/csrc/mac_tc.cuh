@@ -147,6 +147,12 @@ __device__ __forceinline__ bool drained(unsigned long long *bar, uint32_t parity
   return mbar_wait_bounded(smem_addr(bar), parity, (volatile int *)&never, kDrainLimit);
 }
 
+// The warp that works out the pieces waits for whole pieces (room for the next
+// ones, a piece's last tile), not for one copy or product, so its limit grows
+// by 2^14 cycles with every key tile that it has posted (a tile takes 2900
+// to 7200).  A role that is stuck gives up by its own limit and sets *abort.
+constexpr int kTileLimitLog = 14;
+
 // The pieces of a CTA, from the one warp that works them out to the warps of
 // the other roles (`readers` of them): a short ring in shared memory.  The
 // walk's code runs in one place only, ahead of its use; in every role it was

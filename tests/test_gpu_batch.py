@@ -602,6 +602,18 @@ def test_chunk_wait_runs_out(dt, use, paged, new):
     b.check()
 
 
+@pytest.mark.parametrize("dt,Hq,Hkv,ctx,new", [
+    (BF16, 8, 2, [80001] * 8, [30] * 8),     # one warp waits for a piece's last value tile, to clear its end
+    (F32, 4, 4, [1500] * 250, [2] * 250)])   # and for room for the next pieces, several ahead
+def test_chunk_pieces_longer_than_any_wait(dt, Hq, Hkv, ctx, new):
+    # no copy or product takes 2^16 cycles, but a piece of 60 tiles (bf16) or 24 (fp32) does: nothing has run out
+    b = Batch(ctx, new, Hq, Hkv, dt, False, seed=11)
+    mac.mac_test_wait_budget(1 << 16, -1)
+    b.run()
+    assert b.status() == 0
+    b.check()
+
+
 @pytest.mark.parametrize("paged", [True, False])
 @pytest.mark.parametrize("use", [-1, 0, 2])
 @pytest.mark.parametrize("dt", [BF16, F32])
