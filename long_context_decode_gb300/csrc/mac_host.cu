@@ -112,7 +112,8 @@ int check_kv(const mac_config *c, const mac_kv *kv) {
   if (c->page_size == 0) {
     if (kv->capacity < 1) return MAC_ERR_INVALID_ARG;
   } else {
-    if (!kv->page_table || kv->max_pages < 1 || kv->n_pages < 1) return MAC_ERR_INVALID_ARG;
+    if (!kv->page_table || ((uintptr_t)kv->page_table & 3u) != 0 || kv->max_pages < 1 || kv->n_pages < 1)
+      return MAC_ERR_INVALID_ARG;
   }
   return MAC_OK;
 }

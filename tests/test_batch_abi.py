@@ -114,3 +114,16 @@ def test_chunk_attention_refusals(mac):
     paged = [R(mac.config(2, 8, 2, page_size=16))] + good[1:]
     refused(mac, "mac_chunk_attention", paged, [(6, R(mac.mac_kv(256, 256, None, 0, 8, 8)), INV),
                                                 (6, R(mac.mac_kv(256, 256, 256, 0, 8, 0)), INV)])
+
+
+def test_a_misaligned_page_table_is_refused(mac):
+    # the kernels read it in 4-byte words
+    INV = mac.MAC_ERR_INVALID_ARG
+    cfg = mac.config(2, 8, 2, page_size=16, max_context=4096)
+    kv = R(mac.mac_kv(256, 256, 258, 0, 8, 8))
+    L = mac.load()
+    assert L.mac_chunk_attention(R(cfg), 256, 256, 256, 256, 4, kv, 512, 256, None) == INV
+    assert L.mac_full_attention(R(cfg), 256, 256, 256, kv, 512, None, None) == INV
+    assert L.mac_full_attention_noalloc(R(cfg), 256, 256, kv, 512, None, None) == INV
+    assert L.mac_decode_step(R(cfg), 256, 256, 256, 256, kv, 512, None, None, None) == INV
+    assert L.mac_init_rings(R(cfg), 256, 256, 256, 256, 1, kv, None) == INV
