@@ -297,8 +297,9 @@ int mac_write_kv(const mac_config *cfg, void *chunk_ws, const void *q, int64_t q
  * [0, n_pages) are left out (MAC_DEV_BAD_PAGE); a row that so has nothing
  * to attend gets out 0 and lse -inf, and so does every row of a request
  * whose seq_len is below n or beyond the cache (MAC_DEV_BAD_SEQ_LEN);
- * a request whose rows q_start puts outside [0, n_tokens] is passed over
- * (MAC_DEV_BAD_SEQ_LEN).  Cache rows beyond seq_len may hold anything.  V of
+ * a request whose rows q_start puts outside [0, n_tokens], or ends before
+ * they start, is passed over (MAC_DEV_BAD_SEQ_LEN); of rows that q_start so
+ * gives to several requests out and lse are unspecified.  Cache rows beyond seq_len may hold anything.  V of
  * positions up to seq_len must be finite even where a row of the same call
  * does not attend them yet: they meet its zero weights (K may be anything).  dtype bf16:
  * products of bf16, sums and statistics in fp32, the probabilities rounded

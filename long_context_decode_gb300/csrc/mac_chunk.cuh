@@ -52,18 +52,17 @@ struct ChunkPlan {
   static constexpr int kKt = log2i(KT);
 
   // of all requests before b, all KV heads: cost; units, those of half the rows
-  // in the upper 32 bits (counted up to kMany per request and head: used only
-  // where all requests together have fewer)
-  static constexpr int kMany = 2 * kChunkGrid;
+  // in the upper 32 bits
+  static_assert(8LL * kMaxTokens / (C::kHalves ? ROWS / 2 : ROWS) * kMaxUnits < 1LL << 31, "units, each request with every row of the batch");
   long long prefix[2][kMaxUnits + 1];
   long long warp_tot[2][32];
   long long share;
   int whole;
-  int flags;  // 1: a bad request; 2, 4: a unit, one of half the rows, too long to be taken whole
+  int flags;  // 1: a bad request; 2, 4: a unit, one of half the rows, too long to be taken whole; 8: q_start goes back
   int lt, shift;  // log2 of the tokens per unit, place of its count
 
   __device__ long long axis(int b) const { return whole ? (uint32_t)(prefix[1][b] >> shift) : prefix[0][b]; }
-  __device__ static int units(int n, int lt) { return (n + (1 << lt) - 1) >> lt; }
+  __device__ static int units(int n, int lt) { return (n + (1 << lt) - 1) >> lt; }  // n <= kMaxTokens
   __device__ static int weight(int n_tok, int lt) { return 2 * n_tok > 1 << lt ? W : WS; }
 
   // tiles attended by the first k units, all of them full, of a request
@@ -91,21 +90,24 @@ struct ChunkPlan {
   __device__ void build(const ChunkParams &p) {
     const int lt0 = log2i(ROWS) - (31 - __clz(p.G)), n_thr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long sum[2] = {0, 0};  // cost, units
-    int bad = 0, top = 0, top_half = 0;  // highest cost of a unit
+    int bad = 0, back = 0, top = 0, top_half = 0;  // highest cost of a unit
     if (threadIdx.x == 0) prefix[0][0] = prefix[1][0] = flags = 0;
     for (int b0 = 0; b0 < p.B; b0 += n_thr) {
       const int b = b0 + threadIdx.x;
       long long v[2] = {0, 0};
       if (b < p.B) {
         int a, n;
-        bad |= request(p, b, &a, &n) != 0;
+        if (request(p, b, &a, &n) != 0) {
+          bad = 1;
+          back |= p.q_start[b + 1] < p.q_start[b];
+        }
         if (n > 0) {
           const int tiles = (int)(((long long)a + n + KT - 1) >> kKt);
           top = max(top, COST0 + tiles * weight(n, lt0));
           top_half = max(top_half, COST0 + tiles * WS);
         }
         v[0] = cost(a, n, lt0, false) * p.Hkv;
-        v[1] = (min(units(n, lt0), kMany) + (C::kHalves ? (long long)min(units(n, lt0 - 1), kMany) << 32 : 0)) * p.Hkv;
+        v[1] = (units(n, lt0) + (C::kHalves ? (long long)units(n, lt0 - 1) << 32 : 0)) * p.Hkv;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -132,17 +134,20 @@ struct ChunkPlan {
     if (ctas > gridDim.x) ctas = gridDim.x;
     if (ctas < 1) ctas = 1;
     auto too_long = [&](int cost) { return (cost - C::kCut - 1) * ctas >= sum[0]; };  // cost > ceil(sum / ctas) + kCut
-    const int mine = (bad ? 1 : 0) | (too_long(top) ? 2 : 0) | (too_long(top_half) ? 4 : 0);
+    const int mine = bad | (too_long(top) ? 2 : 0) | (too_long(top_half) ? 4 : 0) | (back ? 8 : 0);
     const int of_warp = __reduce_or_sync(0xffffffffu, mine);
     if (lane == 0 && of_warp) atomicOr(&flags, of_warp);
     __syncthreads();
     const bool half = C::kHalves && !(flags & 4) && sum[1] >> 32 <= gridDim.x;
     const bool each = half || (!(flags & 2) && (uint32_t)sum[1] <= gridDim.x);
+    // Rows that several requests claim (only where q_start goes back) make more
+    // units than the host counts on when it leaves the merge out: none is cut.
+    const bool uncut = !each && (flags & 8);
     if (threadIdx.x == 0) {
-      whole = each;
+      whole = each || uncut;
       lt = half ? lt0 - 1 : lt0;
       shift = half ? 32 : 0;
-      share = each ? 1 : max(1LL, (sum[0] + ctas - 1) / ctas);
+      share = each ? 1 : uncut ? ((uint32_t)sum[1] + gridDim.x - 1) / gridDim.x : max(1LL, (sum[0] + ctas - 1) / ctas);
     }
     __syncthreads();
   }

@@ -543,6 +543,28 @@ def test_chunk_bad_lengths(dt):
     assert (b.out[33:] == 7).all() and (b.lse[:33] > -math.inf).all()
 
 
+@pytest.mark.parametrize("dt,ctx,T,B", [(BF16, 1128, 1024, 12), (F32, 280, 280, 16)])
+def test_chunk_requests_that_claim_the_same_rows(dt, ctx, T, B):
+    # a q_start that goes back is reported; a request whose rows nobody else claims is right all the same,
+    # also where the lengths need more units than n_tokens rows in order could
+    b = Batch([ctx] + [0] * (B - 1), [24] + [0] * (B - 1), 8, 8, dt, False, seed=13, pad=T)
+    b.cfg.max_context = ctx + 24
+    b.run()
+    assert b.status() == 0
+    b.check()
+    b.q_start.copy_(ints([0] + [24, 24 + T] * (B // 2)))
+    b.seq_len.copy_(ints([ctx + 24] + [T] * (B - 1)))
+    for x in (b.k, b.v):  # the other requests' tokens
+        x[1:] = 0
+    b.out.fill_(7)
+    b.lse.fill_(7)
+    b.run()
+    assert b.status() == mac.MAC_DEV_BAD_SEQ_LEN
+    b.out[24:] = 7
+    b.lse[24:] = 7
+    b.check()
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_chunk_infinite_and_nan_rows_stay_in_their_row(dt):
     b = Batch([100], [70], 8, 2, dt, True, seed=6)
