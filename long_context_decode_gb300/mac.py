@@ -236,33 +236,51 @@ def mac_build_tables(cfg, chunk_ws, pages: mac_pages, reset_flags, len_in, new_l
                                    _ptr(q_start), _ptr(pos), _ptr(slot), _stream(stream)), "mac_build_tables")
 
 
-def _row_stride(t, heads, head_dim) -> int:
-    """Elements between rows of [T, heads, d] whose rows are whole (a raw
-    pointer's rows lie end to end)."""
+def _row_stride(t, heads, head_dim, rows=0) -> int:
+    """Elements between rows of [T, heads, d] whose rows are whole, T >= rows
+    (a raw pointer's rows lie end to end)."""
     if t is None or isinstance(t, int):
         return heads * head_dim
-    st = t.stride()
-    if (st[1] != head_dim and t.shape[1] != 1) or st[2] != 1:
+    try:
+        (n, h, d), (row, head, one) = t.shape, t.stride()
+    except ValueError:
+        n = h = d = row = head = one = 0
+    if n < rows or h < heads or d != head_dim:
+        raise MacError(f"mac_write_kv: {rows} rows of {heads} heads of {head_dim} are needed, not {tuple(t.shape)}")
+    if (head != d and h != 1) or one != 1:
         raise MacError("mac_write_kv: a row's heads must lie end to end")
-    return st[0] if t.shape[0] != 1 else heads * head_dim  # (one row's stride may be anything)
+    return row if n != 1 else heads * head_dim  # (one row's stride may be anything)
+
+
+def _whole(t, n, what) -> int | None:
+    """Pointer of a tensor that the library takes as n elements end to end."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_contiguous() or t.numel() < n:
+        raise MacError(f"{what} must be {n} elements end to end")
+    return t.data_ptr()
 
 
 def mac_write_kv(cfg, chunk_ws, q, k, v, pos, slot, n_tokens, kv: mac_kv, q_out, stream=None):
     """Rotate and store the rows of a batch.  q, k, v: [T, heads, d] tensors,
     strided views of a fused projection included, or pointers to contiguous
-    rows; q and q_out None for keys and values only."""
-    d = cfg.head_dim
-    _check(load().mac_write_kv(ctypes.byref(cfg), _ptr(chunk_ws), _ptr(q), _row_stride(q, cfg.n_q_heads, d), _ptr(k),
-                               _row_stride(k, cfg.n_kv_heads, d), _ptr(v), _row_stride(v, cfg.n_kv_heads, d), _ptr(pos),
-                               _ptr(slot), int(n_tokens), ctypes.byref(kv) if kv is not None else None, _ptr(q_out),
+    rows; q_out contiguous; q and q_out None for keys and values only."""
+    d, hq, hkv, n = cfg.head_dim, cfg.n_q_heads, cfg.n_kv_heads, int(n_tokens)
+    _check(load().mac_write_kv(ctypes.byref(cfg), _ptr(chunk_ws), _ptr(q), _row_stride(q, hq, d, n), _ptr(k),
+                               _row_stride(k, hkv, d, n), _ptr(v), _row_stride(v, hkv, d, n), _ptr(pos), _ptr(slot), n,
+                               ctypes.byref(kv) if kv is not None else None, _whole(q_out, n * hq * d, "mac_write_kv: q_out"),
                                _stream(stream)), "mac_write_kv")
 
 
 def mac_chunk_attention(cfg, chunk_ws, q, q_start, seq_len, n_tokens, kv: mac_kv, out, lse=None, stream=None):
-    """Exact causal attention of a batch's rotated rows over the cache."""
-    _check(load().mac_chunk_attention(ctypes.byref(cfg), _ptr(chunk_ws), _ptr(q), _ptr(q_start), _ptr(seq_len),
-                                      int(n_tokens), ctypes.byref(kv) if kv is not None else None, _ptr(out), _ptr(lse),
-                                      _stream(stream)), "mac_chunk_attention")
+    """Exact causal attention of a batch's rotated rows over the cache; q, out
+    and lse contiguous."""
+    n = int(n_tokens)
+    rows = n * cfg.n_q_heads
+    _check(load().mac_chunk_attention(ctypes.byref(cfg), _ptr(chunk_ws), _whole(q, rows * cfg.head_dim, "mac_chunk_attention: q"),
+                                      _ptr(q_start), _ptr(seq_len), n, ctypes.byref(kv) if kv is not None else None,
+                                      _whole(out, rows * cfg.head_dim, "mac_chunk_attention: out"),
+                                      _whole(lse, rows, "mac_chunk_attention: lse"), _stream(stream)), "mac_chunk_attention")
 
 
 def mac_status_string(code: int) -> str:

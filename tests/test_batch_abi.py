@@ -127,3 +127,24 @@ def test_a_misaligned_page_table_is_refused(mac):
     assert L.mac_full_attention_noalloc(R(cfg), 256, 256, kv, 512, None, None) == INV
     assert L.mac_decode_step(R(cfg), 256, 256, 256, 256, kv, 512, None, None, None) == INV
     assert L.mac_init_rings(R(cfg), 256, 256, 256, 256, 1, kv, None) == INV
+
+
+def test_binding_refuses_tensors_that_the_calls_cannot_take(mac):
+    # the library sees addresses only: rows apart, or fewer than n_tokens, would be read and written at the wrong places
+    torch = pytest.importorskip("torch")
+    cfg = mac.config(2, 8, 2, max_context=4096)
+    kv = mac.mac_kv(256, 256, None, 4096, 0, 0)
+    fused = torch.zeros(4, 12, 128, dtype=torch.bfloat16)
+    q, k, v = fused[:, :8], fused[:, 8:10], fused[:, 10:]
+    whole = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
+    for out in (q, whole[:3], whole.transpose(0, 1)):  # q_out: a row's heads and the rows end to end, n_tokens of them
+        with pytest.raises(mac.MacError, match="q_out"):
+            mac.mac_write_kv(cfg, 256, whole, k, v, 256, 256, 4, kv, out)
+    for args in ((whole[:3], k, v), (whole, k[:3], v), (whole, k, v[:3]), (whole, k[:, :1], v), (whole[0], k, v)):
+        with pytest.raises(mac.MacError):
+            mac.mac_write_kv(cfg, 256, *args, 256, 256, 4, kv, 512)
+    for args in ((q, whole), (whole, q), (whole[:3], whole), (whole, whole[:3]), (whole, whole[:, :4])):
+        with pytest.raises(mac.MacError, match="mac_chunk_attention"):
+            mac.mac_chunk_attention(cfg, 256, args[0], 256, 256, 4, kv, args[1])
+    with pytest.raises(mac.MacError, match="lse"):
+        mac.mac_chunk_attention(cfg, 256, whole, 256, 256, 4, kv, whole.clone(), torch.zeros(8, 4).t())
