@@ -299,12 +299,14 @@ int mac_write_kv(const mac_config *cfg, void *chunk_ws, const void *q, int64_t q
  * whose seq_len is below n or beyond the cache (MAC_DEV_BAD_SEQ_LEN);
  * a request whose rows q_start puts outside [0, n_tokens], or ends before
  * they start, is passed over (MAC_DEV_BAD_SEQ_LEN); of rows that q_start so
- * gives to several requests out and lse are unspecified.  Cache rows beyond seq_len may hold anything.  V of
- * positions up to seq_len must be finite even where a row of the same call
- * does not attend them yet: they meet its zero weights (K may be anything).  dtype bf16:
- * products of bf16, sums and statistics in fp32, the probabilities rounded
- * to bf16 before they meet V.  dtype f32: products and sums to fp32; a row
- * that attends an infinite element is NaN. */
+ * gives to several requests out and lse are unspecified.  Cache rows beyond
+ * seq_len may hold anything.  V of positions up to seq_len must be finite
+ * even where a row of the same call does not attend them yet: they meet its
+ * zero weights (K may be anything).  dtype bf16: products of bf16, sums and
+ * statistics in fp32, the probabilities rounded to bf16 before they meet V.
+ * dtype f32: weights, sums and statistics in fp32, each product to 2^-21 of
+ * its size (2^-24 on average); a row that attends an infinite element is
+ * NaN. */
 int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
                         const int32_t *q_start, const int32_t *seq_len, int32_t n_tokens,
                         const mac_kv *kv, void *out, float *lse, void *stream);

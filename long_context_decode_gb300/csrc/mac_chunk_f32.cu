@@ -6,9 +6,11 @@
 //   out = o / l;  lse = m ln 2 + ln l.
 // An fp32 number is the exact sum of three bf16 ones, a = a0 + a1 + a2, eight
 // bits of its significand each (cut off, not rounded), so a product is
-//   a b = a0 b0 + (a0 b1 + a1 b0) + (a1 b1 + a0 b2 + a2 b0) + terms below 2^-23 |a b|:
+//   a b = a0 b0 + (a0 b1 + a1 b0) + (a1 b1 + a0 b2 + a2 b0) + what is left out:
 // six bf16 products for one in fp32, each exact in the tensor cores' fp32
-// sums.  The small ones are summed first, so that what the sums cut off is
+// sums.  With a1 up to 2^-7 |a| and a2 up to 2^-15 |a|, a1 b2 + a2 b1 is up to
+// 2^-21 |a b| (2^-24 on average) and always has the product's sign: leaving it
+// out shrinks |a b|.  The small ones are summed first, so that what the sums cut off is
 // small against the result, and a tile's P V is added to o in registers
 // (rounded to nearest): errors do not pile up over a long context.
 //
