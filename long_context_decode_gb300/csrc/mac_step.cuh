@@ -1887,15 +1887,16 @@ struct Step {
         }
       }
     }
-    // band: the cached summary (a state of sum 1 at its ln-LSE) with the
-    // band state
-    const float cm = hit ? c_lse * kLog2e : -INFINITY;
+    // band: the cached summary (a state of sum 1 at its ln-LSE; empty, at
+    // -inf, where its position is within the band) with the band state
+    const bool cached = hit && c_lse != -INFINITY;
+    const float cm = cached ? c_lse * kLog2e : -INFINITY;
     const float M = fmaxf(cm, Lb > 0.f ? Mb : -INFINITY);
-    const float wc = mweight(cm, hit ? 1.f : 0.f, M), wbb = mweight(Mb, Lb, M);
-    const float La = (hit ? wc : 0.f) + wbb * Lb;
+    const float wc = mweight(cm, cached ? 1.f : 0.f, M), wbb = mweight(Mb, Lb, M);
+    const float La = (cached ? wc : 0.f) + wbb * Lb;
     float Oa[kDL];
 #pragma unroll
-    for (int i = 0; i < kDL; ++i) Oa[i] = (hit ? wc * c_o[i] : 0.f) + wbb * Ob[i];
+    for (int i = 0; i < kDL; ++i) Oa[i] = (cached ? wc * c_o[i] : 0.f) + wbb * Ob[i];
     if (!fin) {
       // the group's partial: the raw state, in a piece partial's layout
       float *dst = p.part_g + ((size_t)(u + group) * G + hh) * kPartStride;
