@@ -780,3 +780,165 @@ def test_prompts_in_chunks_then_decode(dt, paged):
         held = sum(pages_of(n) for n in length.tolist())
         assert n_free.tolist() == [n_pages - held]
     layer.release()
+
+
+@pytest.mark.parametrize("how", ["eager", "graph"])
+@pytest.mark.parametrize("dt,Hq,Hkv,paged", [(BF16, 8, 2, True), (BF16, 8, 2, False), (BF16, 16, 2, True), (F32, 4, 4, True)])
+def test_keys_and_values_then_decode_steps_of_several_layers(dt, Hq, Hkv, paged, how):
+    """A decode step of a model: pages and slots once, then per layer the new token's key and value (no query: the
+    step rotates its own) and the step, one behind the other with nothing in between.  It has to leave what the same
+    calls leave with the device idle before each."""
+    B, layers, steps, room = 5, 4, 14, 512
+    g = torch.Generator(device=DEV)
+    g.manual_seed(12)
+    n_pages = B * room // PAGE
+    cfg = mac.config(B, Hq, Hkv, ring_k=32, band_r=16, dtype=mac.MAC_BF16 if dt == BF16 else mac.MAC_F32,
+                     page_size=PAGE if paged else 0, max_context=room)
+    shape = (n_pages, Hkv, PAGE, D) if paged else (B, Hkv, room, D)
+    start = [300, 17, 0, 255, 495]
+    cache = [torch.randn(shape, generator=g, device=DEV).to(dt) for _ in range(2 * layers)]
+    base = torch.randn(layers, B, Hq, D, generator=g, device=DEV)
+    ids = torch.randperm(n_pages, generator=g, device=DEV).int()
+
+    class Model:
+        def __init__(self):
+            self.cache = [x.clone() for x in cache]
+            self.table = torch.full((B, room // PAGE), -1, dtype=torch.int32, device=DEV)
+            self.n_free, self.free, at = ints([0]), ids.clone(), n_pages
+            for b, n in enumerate(start):
+                at -= pages_of(n)
+                self.table[b, :pages_of(n)] = ids[at:at + pages_of(n)]
+            self.n_free.fill_(at)
+            self.pages = mac.pages_view(self.table, self.free, self.n_free) if paged else mac.pages_view(capacity=room)
+            self.length, self.new = ints(start), ints([1] * B)
+            self.q_start, self.pos, self.slot = ints([0] * (B + 1)), ints([0] * B), ints([0] * B, torch.int64)
+            self.ws = workspace(cfg, B)
+            self.layers = [mac.MacLayer(cfg, device=DEV) for _ in range(layers)]
+            self.q = [torch.zeros(B, Hq, D, device=DEV, dtype=dt) for _ in range(layers)]
+            self.kv = [torch.zeros(B, 2 * Hkv, D, device=DEV, dtype=dt) for _ in range(layers)]
+            self.out = [torch.zeros(B, Hq, D, device=DEV) for _ in range(layers)]
+            self.match = [ints([[0] * Hq] * B) for _ in range(layers)]
+            for x in self.layers:
+                mac.mac_init_rings(cfg, x.ring, x.scratch, None, None, 0, None)
+
+        def inputs(self, step):
+            g = torch.Generator(device=DEV)
+            g.manual_seed(1000 + step)
+            for i in range(layers):
+                noise = torch.randn(B, Hq, D, generator=g, device=DEV)
+                self.q[i].copy_(base[i] + (0.02 if step % 3 else 1.0) * noise)
+                self.kv[i].copy_(torch.randn(B, 2 * Hkv, D, generator=g, device=DEV))
+
+        def step(self, stream, wait=lambda: None):
+            mac.mac_build_tables(cfg, self.ws, self.pages, None, self.length, self.new, B, self.length, self.q_start, self.pos,
+                                 self.slot, stream)
+            for i, x in enumerate(self.layers):
+                view = mac.kv_view(*self.cache[2 * i:2 * i + 2], self.table if paged else None)
+                wait()
+                mac.mac_write_kv(cfg, self.ws, None, self.kv[i][:, :Hkv], self.kv[i][:, Hkv:], self.pos, self.slot, B, view, None,
+                                 stream)
+                wait()
+                mac.mac_decode_step(cfg, x.ring, x.scratch, self.q[i], self.length, view, self.out[i], self.match[i], stream)
+                wait()
+
+    apart, close = Model(), Model()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if how == "graph":
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            close.step(torch.cuda.current_stream())
+    hits = 0
+    for step in range(steps):
+        apart.inputs(step)
+        close.inputs(step)
+        torch.cuda.synchronize()
+        apart.step(s, torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay() if how == "graph" else close.step(s)
+        torch.cuda.synchronize()
+        assert close.length.tolist() == [n + step + 1 for n in start] and torch.equal(close.slot, apart.slot)
+        for i in range(layers):
+            assert torch.equal(close.match[i], apart.match[i])
+            assert torch.equal(close.out[i], apart.out[i])
+            hits += int((close.match[i] >= 0).sum())
+    assert hits > 0
+    for a, c in zip(apart.cache, close.cache):
+        assert torch.equal(a, c)
+    for m in (apart, close):
+        assert mac.mac_last_status(cfg, m.ws) == 0
+        for x in m.layers:
+            assert mac.mac_last_status(cfg, x.scratch) == 0
+            x.release()
+
+
+# ---------------------------------------------------------------------------
+# many requests: more than a CTA has threads, and as many as a table call takes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B", [385, 513, 1024])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("G", [1, 4])
+def test_chunk_more_requests_than_threads(dt, B, G):
+    # the plan's last trip holds the long requests, or the only ones; empty ones and single tokens before them
+    for sparse in (False, True):
+        ctx, new = [0 if sparse else b % 7 for b in range(B)], [0 if sparse else int(b % 3 == 0) for b in range(B)]
+        ctx[B - 1], new[B - 1] = 900, 70
+        if B > 513:
+            ctx[520:523], new[520:523] = [400, 0, 5], [1, 130, 0]
+        b = Batch(ctx, new, G, 1, dt, True, seed=B, pad=1)
+        b.run()
+        assert b.status() == 0
+        b.check()
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("B,rows", [(1023, 1000), (1024, 1024), (1023, 1025), (1024, 3000)])
+def test_tables_of_as_many_requests_as_there_may_be(B, rows, paged):
+    rng = random.Random(B + rows)
+    length = [rng.randint(0, 70) for _ in range(B)]
+    new = [rng.choice([0, 1, rows // B * 2]) for _ in range(B)]
+    while sum(new) > rows - 3:
+        new[rng.randrange(B)] = 0
+    new[B - 1] = rows - 3 - sum(new[:-1]) if paged else new[B - 1]  # the last request takes what is left, but three rows
+    flags = [int(rng.randrange(4) == 0) for _ in range(B)]
+    width = pages_of(70 + max(new)) + 1
+    assert check_tables(length, new, flags, rows, width, 6000, paged, limit=width * PAGE, seed=B)[5] == 0
+
+
+def test_write_leaves_skipped_rows_and_other_slots_alone():
+    # every third row is skipped: by a negative slot, one beyond the cache or a position below 1, in CTAs of one and
+    # of two rows.  What they would have written, and every slot that no row names, keeps what it held.
+    for T in (50, 2100):
+        cfg = mac.config(1, 4, 2, page_size=PAGE, max_context=4096)
+        n_pages = pages_of(T) + 2
+        q, k, v = (torch.randn(T, h, D, device=DEV).to(BF16) for h in (4, 2, 2))
+        kc, vc = (torch.randn(n_pages, 2, PAGE, D, device=DEV).to(BF16) for _ in range(2))
+        k0, v0, t = kc.clone(), vc.clone(), torch.arange(T, device=DEV)
+        slot, pos = torch.randperm(n_pages * PAGE, device=DEV)[:T], (t % 900 + 1).int()
+        named = slot.clone()
+        slot[t % 9 == 2], slot[t % 9 == 5] = -1, n_pages * PAGE
+        pos[t % 9 == 8] = 0
+        live = t % 3 != 2
+        out, ws = torch.full_like(q, 7.0), workspace(cfg, T)
+        mac.mac_write_kv(cfg, ws, q, k, v, pos, slot, T, mac.kv_view(kc, vc, ints([[0]])), out)
+        assert mac.mac_last_status(cfg, ws) == mac.MAC_DEV_BAD_PAGE | mac.MAC_DEV_BAD_SEQ_LEN
+        assert (out[~live] == 7).all() and (out[live] != 7).any(-1).all()
+        kept = torch.ones(n_pages * PAGE, dtype=torch.bool, device=DEV)
+        kept[named[live]] = False
+        rows = lambda x: x.transpose(1, 2).flatten(0, 1)  # noqa: E731
+        assert torch.equal(rows(kc)[kept], rows(k0)[kept]) and torch.equal(rows(vc)[kept], rows(v0)[kept])
+        assert torch.equal(rows(vc)[named[live]], v[live])
+
+
+def test_chunk_fp32_rows_that_attend_an_infinite_key_are_nan_and_no_others():
+    # an infinity has no sum of three finite parts: whatever the score, the row says so
+    for bad in (float("inf"), -float("inf")):
+        b = Batch([100], [70], 8, 2, F32, True, seed=6)
+        b.run()
+        ref = b.out.clone()
+        b.k[b.table[0, 140 // PAGE].long(), 1, 140 % PAGE, 5] = bad  # position 141 of KV head 1: rows 40 and on of heads 4 to 7
+        b.run()
+        assert b.out[40:, 4:].isnan().all()
+        assert torch.equal(b.out[:40], ref[:40]) and torch.equal(b.out[:, :4], ref[:, :4])
