@@ -942,3 +942,155 @@ def test_chunk_fp32_rows_that_attend_an_infinite_key_are_nan_and_no_others():
         b.run()
         assert b.out[40:, 4:].isnan().all()
         assert torch.equal(b.out[:40], ref[:40]) and torch.equal(b.out[:, :4], ref[:, :4])
+
+
+# ---------------------------------------------------------------------------
+# large offsets, calls at once
+# ---------------------------------------------------------------------------
+
+def attend(q, k, v, first):
+    """Rows q [n, H, D] at positions first, first + 1, .. (0-based) over k, v [Hkv, seen, D], in 64 bits: out, A = sum P |v|."""
+    G = q.shape[1] // k.shape[0]
+    q, k, v = q.double().transpose(0, 1), k.double().repeat_interleave(G, 0), v.double().repeat_interleave(G, 0)
+    late = torch.arange(k.shape[1], device=DEV)[None] > torch.arange(first, first + q.shape[1], device=DEV)[:, None]
+    w = torch.softmax((q @ k.transpose(1, 2) / math.sqrt(D)).masked_fill(late, -math.inf), -1)
+    return (w @ v).transpose(0, 1), (w @ v.abs()).transpose(0, 1)
+
+
+def attention_tol(want, A, dt):
+    # up to 4200 normal keys: sum |q k| <= 120, e = (D + 4) 2^-24 120 / sqrt(D) = 2^-13.5 (four times that in bf16), and
+    # (n + 64) 2^-24 = 2^-12: 2 e + that is below 2^-10 and 2^-11
+    return (2.0 ** -10 * A + 2.0 ** -8 * (A + want.abs())) if dt == BF16 else 2.0 ** -11 * A
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_caches_beyond_32_bit_offsets(dt, paged):
+    # keys and values of the last request and of page ids at the pool's end lie past element 2^32
+    Hq, Hkv, B, n, ctx = 8, 4, 2, 40, 300
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    total, held = ctx + n, pages_of(ctx + n)
+    cap = (1 << 32) // (B * Hkv * D) // PAGE * PAGE + 40000 * PAGE
+    n_pages = (1 << 32) // (Hkv * PAGE * D) + 3 * held
+    shape = (n_pages, Hkv, PAGE, D) if paged else (B, Hkv, cap, D)
+    kc, vc = (torch.empty(shape, device=DEV, dtype=dt) for _ in range(2))
+    cfg = mac.config(B, Hq, Hkv, dtype=mac.MAC_BF16 if dt == BF16 else mac.MAC_F32, page_size=PAGE if paged else 0,
+                     rope_mode=mac.MAC_ROPE_NONE, max_context=cap if not paged else 4096)
+    table = ints([list(range(held)), list(range(n_pages - 1, n_pages - 1 - held, -1))]) if paged else None
+    pos = torch.arange(total, device=DEV)
+    slot = torch.cat([(table[b, pos // PAGE].long() * PAGE + pos % PAGE) if paged else b * cap + pos for b in range(B)])
+    assert kc.numel() > 1 << 32
+    T = B * total
+    q, k, v = (torch.randn(T, h, D, generator=g, device=DEV).to(dt) for h in (Hq, Hkv, Hkv))
+    ws = workspace(cfg, T)
+    kv = mac.kv_view(kc, vc, table) if paged else mac.kv_view(kc, vc)
+    mac.mac_write_kv(cfg, ws, None, k, v, pos.repeat(B).int() + 1, slot, T, kv, None)
+    for b in range(B):
+        for x, new in ((kc, k), (vc, v)):
+            rows = x[table[b, pos // PAGE].long(), :, pos % PAGE] if paged else x[b, :, :total].transpose(0, 1)
+            assert torch.equal(rows, new[b * total:(b + 1) * total])
+    qn = torch.cat([q[(b + 1) * total - n:(b + 1) * total] for b in range(B)])
+    out, lse = torch.zeros_like(qn), torch.zeros(B * n, Hq, device=DEV)
+    mac.mac_chunk_attention(cfg, ws, qn, ints([0, n, 2 * n]), ints([total] * B), B * n, kv, out, lse)
+    assert mac.mac_last_status(cfg, ws) == 0
+    for b in range(B):
+        want, A = attend(qn[b * n:(b + 1) * n], *(x[b * total:(b + 1) * total].transpose(0, 1) for x in (k, v)), ctx)
+        near(out[b * n:(b + 1) * n], want, attention_tol(want, A, dt))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_rows_beyond_32_bit_offsets(dt):
+    # queries, outputs and a fused projection's rows past element 2^31
+    B, Hq, Hkv, n = 64, 64, 16, 4200
+    T = B * n
+    assert T * Hq * D > 1 << 31
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    cfg = mac.config(B, Hq, Hkv, dtype=mac.MAC_BF16 if dt == BF16 else mac.MAC_F32, page_size=PAGE, rope_mode=mac.MAC_ROPE_NONE,
+                     max_context=n + PAGE)
+    fused = torch.empty(T, Hq + 2 * Hkv, D, device=DEV, dtype=dt).normal_(generator=g)
+    q, k, v = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+    n_pages = B * pages_of(n)
+    kc, vc = (torch.empty(n_pages, Hkv, PAGE, D, device=DEV, dtype=dt) for _ in range(2))
+    table = torch.zeros(B, pages_of(n) + 1, dtype=torch.int32, device=DEV)
+    free, n_free = torch.randperm(n_pages, generator=g, device=DEV).int(), ints([n_pages])
+    length, q_start, pos, slot = ints([0] * B), ints([0] * (B + 1)), ints([0] * T), ints([0] * T, torch.int64)
+    ws, kv = workspace(cfg, T), mac.kv_view(kc, vc, table)
+    rows, out = (torch.empty(T, Hq, D, device=DEV, dtype=dt) for _ in range(2))
+    lse = torch.zeros(T, Hq, device=DEV)
+    mac.mac_build_tables(cfg, ws, mac.pages_view(table, free, n_free), None, length, ints([n] * B), T, length, q_start, pos, slot)
+    mac.mac_write_kv(cfg, ws, q, k, v, pos, slot, T, kv, rows)
+    mac.mac_chunk_attention(cfg, ws, rows, q_start, length, T, kv, out, lse)
+    assert mac.mac_last_status(cfg, ws) == 0 and n_free.tolist() == [0]
+    for lo in range(0, T, 1 << 15):
+        assert torch.equal(rows[lo:lo + (1 << 15)], q[lo:lo + (1 << 15)])
+    for b, at in ((0, 0), (31, 17), (B - 2, 4100), (B - 1, n - 40)):
+        r = slice(b * n + at, b * n + at + 40)
+        want, A = attend(q[r], *(x[b * n:b * n + at + 40].transpose(0, 1) for x in (k, v)), at)
+        near(out[r], want, attention_tol(want, A, dt))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_two_captured_batches_at_once(dt):
+    """Two programs, each its own stream, workspace, cache and graph of the three calls (rows past those of a single
+    CTA of tables), replayed side by side: each leaves what it leaves alone."""
+    Hq, Hkv, B, T, room = 8, 2, 6, 1300, 1024
+    cfg = mac.config(B, Hq, Hkv, dtype=mac.MAC_BF16 if dt == BF16 else mac.MAC_F32, page_size=PAGE, max_context=room)
+    rng = random.Random(7)
+
+    class Program:
+        def __init__(self, seed):
+            g = torch.Generator(device=DEV)
+            g.manual_seed(seed)
+            n_pages = B * room // PAGE
+            self.cache = [torch.zeros(n_pages, Hkv, PAGE, D, device=DEV, dtype=dt) for _ in range(2)]
+            self.table = torch.full((B, room // PAGE), -1, dtype=torch.int32, device=DEV)
+            self.free, self.n_free = torch.randperm(n_pages, generator=g, device=DEV).int(), ints([n_pages])
+            self.first = self.free.clone()
+            self.length, self.new, self.q_start = ints([0] * B), ints([0] * B), ints([0] * (B + 1))
+            self.pos, self.slot = ints([0] * T), ints([0] * T, torch.int64)
+            self.q, self.k, self.v = (torch.randn(T, h, D, generator=g, device=DEV).to(dt) for h in (Hq, Hkv, Hkv))
+            self.rows, self.out, self.lse = torch.zeros_like(self.q), torch.zeros_like(self.q), torch.zeros(T, Hq, device=DEV)
+            self.ws, self.stream = workspace(cfg, T), torch.cuda.Stream()
+            self.pages, self.kv = mac.pages_view(self.table, self.free, self.n_free), mac.kv_view(*self.cache, self.table)
+            torch.cuda.synchronize()
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph, stream=self.stream):
+                s = torch.cuda.current_stream()
+                mac.mac_build_tables(cfg, self.ws, self.pages, None, self.length, self.new, T, self.length, self.q_start, self.pos,
+                                     self.slot, s)
+                mac.mac_write_kv(cfg, self.ws, self.q, self.k, self.v, self.pos, self.slot, T, self.kv, self.rows, s)
+                mac.mac_chunk_attention(cfg, self.ws, self.rows, self.q_start, self.length, T, self.kv, self.out, self.lse, s)
+
+        def start(self, new):
+            self.new.copy_(ints(new))
+            self.length.zero_()
+            self.free.copy_(self.first)
+            self.n_free.fill_(self.free.numel())
+            self.out.zero_()
+            torch.cuda.synchronize()
+
+        def replay(self):
+            with torch.cuda.stream(self.stream):
+                self.graph.replay()  # the batch's tokens
+                self.graph.replay()  # and as many more behind them
+
+    both = Program(1), Program(2)
+    for _ in range(5):
+        lengths = [[rng.choice([0, 1, rng.randint(2, 210)]) for _ in range(B)] for _ in both]
+        alone = []
+        for p, new in zip(both, lengths):
+            p.start(new)
+            p.replay()
+            torch.cuda.synchronize()
+            alone.append([x.clone() for x in (p.out, p.lse, p.slot, p.length, *p.cache)])
+        for p, new in zip(both, lengths):
+            p.start(new)
+        for p in both:
+            p.replay()
+        torch.cuda.synchronize()
+        for p, new, ref in zip(both, lengths, alone):
+            assert p.length.tolist() == [2 * n for n in new]
+            assert all(torch.equal(x, y) for x, y in zip((p.out, p.lse, p.slot, p.length, *p.cache), ref))
+            assert mac.mac_last_status(cfg, p.ws) == 0
