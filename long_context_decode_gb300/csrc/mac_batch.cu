@@ -29,8 +29,8 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Inclusive scans of three values over the block's threads (all call it;
-// blockDim.x a multiple of 32); `tot` holds one entry per warp.
+// Inclusive scans of three values over the block's threads (all call it; whole
+// warps, two at least); `tot` holds one entry per warp.
 __device__ __forceinline__ void block_scan3(long long v[3], long long (*tot)[3]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
 #pragma unroll
@@ -39,7 +39,6 @@ __device__ __forceinline__ void block_scan3(long long v[3], long long (*tot)[3])
       const long long o = __shfl_up_sync(0xffffffffu, v[i], d);
       if (lane >= d) v[i] += o;
     }
-  if (n_warps == 1) return;
   __syncthreads();  // the last scan's totals have been read
   if (lane == 31)
 #pragma unroll
