@@ -17,11 +17,15 @@ namespace mac {
 // the stack: inputs are read before any output is written, and pages given
 // back are on the stack before any page is taken.
 // Rows: in a single CTA (up to kOneCta rows) a thread finds each row's page
-// for itself (16 requests of one token: 3.2 us).  In the cluster they go a
+// for itself (16 requests of one token: 3.3 us).  In the cluster they go a
 // page's worth at a time: a lane finds its page (the search, the load of the
 // id), then the warp writes the rows of its 32 pages, two pages at once.  A
 // search per row, 100 instructions, made 104K rows of 128 requests take 18.3
-// us on the cluster's eight SMs; this way the call takes 12 (and the 16 requests 4.4).
+// us on the cluster's eight SMs; this way the call takes 10 to 12 (and the 16 requests 4.4).
+// Pages given back are dealt like pages taken, so with few rows it is a single
+// CTA's threads that search, load and store them: 7 of 16 requests of up to
+// 131072 tokens reset (33K pages) take 52 us, 31 of 128 of up to 65536 (62K
+// pages) 121 us, where the calls without resets take 3.3 and 3.9.
 constexpr int kTablesCluster = 8, kOneCta = 1024;
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -383,8 +387,13 @@ cudaError_t launch_write(const WriteParams &p, int dtype, cudaStream_t s) {
   // 8679 rows of 32 + 2 x 8 bf16 heads: 34.8 us (6.1 TB/s); with four rows of
   // 256 threads 36.4, two rows of 256 threads 39.5, one row of 256 threads 53.
   // 2160 rows of 32 + 2 x 4 fp32 heads: 15.9 us; two rows per CTA 17.0.
-  // Fewer bf16 rows take a CTA each: 608 rows 4.1 us (two per CTA: 6.0), 1216
-  // 5.7 (6.3), 2400 8.6 (8.5).
+  // Fewer bf16 rows take a CTA each, whatever their heads, as the number of
+  // CTAs in flight decides (us, one and two rows per CTA): 32 + 2 x 8 heads, 600
+  // rows 4.1 and 5.7, 1200 5.7 and 6.4, 1800 6.8 and 6.5; 8 + 2 x 2 heads, 600
+  // rows 2.9 and 3.4, 1200 3.9 and 3.8, 1800 4.4 and 3.8; 1 + 2 heads, 600 rows
+  // 2.4 and 2.7, 1800 3.9 and 2.9.  Many rows of few heads are bound by the CTAs
+  // too: 8000 rows of 8 + 2 x 2 bf16 heads take 10.1 us (four rows per CTA 8.1;
+  // 32 + 2 x 8 heads 31.8 and 32.1), of fp32 heads 16.8 (13.1 and 12.8; 59, 60.6 and 62.5).
   if (dtype == MAC_F32) return launch_write_t<float, 1>(p, s);
   return p.T <= 2048 ? launch_write_t<uint16_t, 1>(p, s) : launch_write_t<uint16_t, 2>(p, s);
 }

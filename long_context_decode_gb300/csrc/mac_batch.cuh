@@ -54,11 +54,14 @@ struct ChunkParams {
   int4 *notes;                    // [kChunkGrid] the cut unit whose first tile a CTA holds
   float *part;                    // [2 * grid][part_rows][kChunkStride]
   int part_rows;
-  long long wait_limit;           // bf16 kernel: cycles a wait may take
+  long long wait_limit;           // cycles that a wait on a copy, a product or another role may take
   int withhold;                   // run-out test only: the stage use (>= 0) whose copy is never issued
 };
 
-constexpr int kChunkGrid = 256;   // most CTAs of a launch (one per SM)
+// Most CTAs of a launch (one per SM).  The workspace is laid out for as many,
+// so that its size (71 MB of bf16 pieces at most, of which 152 SMs use 42) can
+// be asked where there is no device.
+constexpr int kChunkGrid = 256;
 // What the plan of a chunk attention launch counts with, per kernel: rows of
 // a unit, keys of a tile, and costs: a unit's start and end, a key tile of
 // a unit and of one of at most half the rows, the least worth a CTA of its

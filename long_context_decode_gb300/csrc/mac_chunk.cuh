@@ -1,5 +1,5 @@
 // mac_chunk.cuh -- the work of a chunk-attention launch and how it is cut
-// over the CTAs, shared by the bf16 (tensor core) and fp32 kernels.
+// over the CTAs, shared by the bf16 and fp32 kernels.
 //
 // Units are laid end to end in order (request, KV head, row tile) on a cost
 // axis (ChunkBf16, ChunkF32: a unit's start plus its key tiles, as many as its
@@ -11,9 +11,9 @@
 // timing.  When there is a CTA for every unit and the longest is done before
 // an equal share and what cutting costs, each CTA takes one whole unit
 // instead, of half the rows if there are CTAs for those as well (us, cut and
-// whole): 4 chunks of 60 tokens at 1000, 8 / 2 heads, 22.4 and 16.7; 12 at 1200,
-// 32 / 8 heads, 36.6 and 29.8; 16 single tokens at 1100, 21.7 and 17.3; but two
-// single tokens at 1900, few and long, 16.4 and 21.1.
+// whole): 4 chunks of 60 tokens at 1000, 8 / 2 heads, 19.5 and 16.5; 12 at 1200,
+// 32 / 8 heads, 36.1 and 26.9; 16 single tokens at 1100, 23.2 and 17.0; but two
+// single tokens at 1900, few and long, 17.2 and 20.9.
 #pragma once
 
 #include "mac_batch.cuh"

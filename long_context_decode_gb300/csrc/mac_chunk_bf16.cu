@@ -5,6 +5,13 @@
 //   P_j = 2^(x_j - m) with m a running reference of the row's maximum;
 //   l = sum P_j (fp32);  O = sum P_j V_j (P rounded to bf16, sums in fp32);
 //   out = O / l;  lse = m ln 2 + ln l.
+// P is the one number between the inputs and the output that is held in fewer
+// than 32 bits: the product with V takes both factors in bf16, a second part of
+// P would make it twice as long (half as much again per tile).  Each weight is
+// off by up to 2^-8 of itself, independently, so where the weights are flat the
+// output is off by about as much as by its own rounding to bf16: against 64 bits
+// 2.1e-3 where the output's rounding alone makes 1.6e-3 (7 tokens at 100), 1.8e-3
+// (16384 tokens) and 1.7e-3 (2048 at 32768).  l sums the weights unrounded.
 // The reference m moves only when the maximum has grown by more than 8 in
 // base 2 (P stays below 2^8, and bf16 keeps the same relative precision
 // there), so O is rarely rescaled; any m gives the same quotient.
@@ -23,8 +30,8 @@
 //
 // TMEM (512 columns): S0, S1, O0, O1, 128 columns each; P overwrites S.
 //
-// 2048 tokens at 32768, 32 / 8 heads, paged: 656 us with the merge, 1.62 PFLOP/s
-// (up to 725 us in a loop of a second, at the card's power limit).  A pair of
+// 2048 tokens at 32768, 32 / 8 heads, paged: 640 to 660 us with the merge, 1.65 PFLOP/s
+// (up to 743 us in a loop of a second, at the card's power limit).  A pair of
 // row tiles and a key tile take 2900 cycles: the products 2048, 2620 with the
 // softmax taken out (both operands of S come from shared memory beside the
 // copies), the rest is the softmax in the way.  Four single tokens over 131072
@@ -483,7 +490,7 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
           x.x = ex2(x.x);
           x.y = ex2(x.y);
           acc[j & 1] = add2(acc[j & 1], x);
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x.y), "f"(x.x));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x.y), "f"(x.x));  // to bf16: see above
         }
         tc_st16(s_at + c / 2, pk);
       }

@@ -28,8 +28,10 @@
 // S of the next tile is made while the softmax runs; K is stored while the
 // products of the last weights run, V while the scores do.
 //
-// 4096 tokens, 8 heads of 2 KV heads: 217 us, 158 TFLOP/s of fp32 products
-// (multiply-adds on the CUDA cores: 945 us).  A tile takes 7200 cycles: its 72
+// 4096 tokens, 8 heads of 2 KV heads: 193 to 217 us, 158 to 178 TFLOP/s of fp32
+// products (multiply-adds on the CUDA cores: 945 us).  A tile takes 7200 cycles
+// whatever its rows, so single tokens are bound by splitting and products, not
+// by HBM: four of 32 / 8 heads at 8192 take 95 us (2.8 TB/s).  Of a tile, its 72
 // products 4100 (S 48 of 55, reading Q from shared memory, P V 24 of 60), the
 // rest waits for K and V to be split, which is 45 instructions per row and
 // warp.  Error against 64 bits 3.2e-7 where fp32 matrix products have 5.6e-7.
