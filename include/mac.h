@@ -261,7 +261,9 @@ int mac_chunk_workspace_size(const mac_config *cfg, int32_t n_tokens, size_t *ch
  * Outputs: len_out [B] (may be len_in); q_start int32 [B+1]; pos int32
  * [n_tokens], 1-based; slot int64 [n_tokens]: page * 16 + row (paged) or
  * b * capacity + pos - 1 (contiguous); rows that belong to nobody get pos 0
- * and slot -1.  n_tokens >= 1. */
+ * and slot -1.  n_tokens >= 1.  (mac_decode_step takes a query of every
+ * request: one that brings no token, or is not admitted, decodes the position
+ * of its last token again, and its row of out is to be dropped.) */
 int mac_build_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pages,
                      const int32_t *reset_flags, const int32_t *len_in, const int32_t *new_len,
                      int32_t n_tokens, int32_t *len_out, int32_t *q_start, int32_t *pos,

@@ -31,7 +31,7 @@
 // TMEM (512 columns): S0, S1, O0, O1, 128 columns each; P overwrites S.
 //
 // 2048 tokens at 32768, 32 / 8 heads, paged: 640 to 660 us with the merge, 1.65 PFLOP/s
-// (up to 743 us in a loop of a second, at the card's power limit).  A pair of
+// (up to 752 us in a loop of a second, at the card's power limit).  A pair of
 // row tiles and a key tile take 2900 cycles: the products 2048, 2620 with the
 // softmax taken out (both operands of S come from shared memory beside the
 // copies), the rest is the softmax in the way.  Four single tokens over 131072
