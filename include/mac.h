@@ -313,6 +313,24 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
                         const int32_t *q_start, const int32_t *seq_len, int32_t n_tokens,
                         const mac_kv *kv, void *out, float *lse, void *stream);
 
+/* Attention over another sequence's states ([ACSP] MHA with repeat_kv, its
+ * keys and values those of an encoder; the pages do not describe the call):
+ * every row of the batch attends the whole memory of its source, [1,
+ * mem_len[b]], with no causal mask.  cfg->batch counts the sources, kv is
+ * their cache (mac_write_kv fills it, with MAC_ROPE_NONE where the keys keep
+ * no position), mem_len: int32 [B].  The rows of source b are those of its
+ * `group` >= 1 slots, which lie next to one another (its beams, say): rows
+ * q_start[b group] .. q_start[(b+1) group] - 1, q_start int32 [B group + 1]
+ * as mac_build_tables writes it for the slots (the entries between are not
+ * looked at).  q, out, lse, chunk_ws, n_tokens as in mac_chunk_attention, of
+ * this cfg; the query is taken as it is.  A source without states (mem_len
+ * 0) gives its rows out 0 and lse -inf.  Bad lengths, pages and rows are
+ * reported and left out as there.  Cache rows beyond mem_len may hold
+ * anything.  The numerics are mac_chunk_attention's. */
+int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, const int32_t *q_start,
+                        int32_t group, const int32_t *mem_len, int32_t n_tokens, const mac_kv *kv,
+                        void *out, float *lse, void *stream);
+
 /* Make stream_main wait for the last append enqueued on ring_ws (no-op if
  * none is pending).  Needed before ending a stream capture that used a
  * separate aux stream. */

@@ -47,7 +47,8 @@ struct ChunkParams {
   int64_t max_len;
   KvView kv;
   const void *q;
-  const int32_t *q_start, *seq_len;
+  const int32_t *q_start, *seq_len;  // cross attention: seq_len is the memories' lengths
+  int group;                      // slots of q_start per request (1 but for cross attention)
   void *out;
   float *lse;                     // or null
   uint32_t *status;
@@ -73,11 +74,20 @@ struct ChunkBf16 {
   static constexpr int kRows = 256, kKeys = 128;
   static constexpr int kStart = 12, kTile = 4, kTileHalf = 3, kMinShare = 16, kCut = 35;
   static constexpr bool kHalves = true;  // units of half the rows, where there are CTAs for all of them
+  static constexpr bool kCross = false;
 };
 struct ChunkF32 {
   static constexpr int kRows = 128, kKeys = 64;
   static constexpr int kStart = 3, kTile = 1, kTileHalf = 1, kMinShare = 4, kCut = 4;
   static constexpr bool kHalves = false;
+  static constexpr bool kCross = false;
+};
+// Cross attention: every row of a request attends all of its memory.
+struct CrossBf16 : ChunkBf16 {
+  static constexpr bool kCross = true;
+};
+struct CrossF32 : ChunkF32 {
+  static constexpr bool kCross = true;
 };
 constexpr int kChunkStride = kHeadDim + 8;  // floats per row of a partial: o[d], m, l, and to a multiple of 32 bytes
 constexpr int kMaxTokens = 1 << 24;
@@ -122,6 +132,9 @@ cudaError_t prepare_chunk(K *kernel, DeviceFlags &done, int smem, int regs) {
 // The attention kernels, `grid` CTAs (one per SM).
 cudaError_t launch_chunk_f32(const ChunkParams &p, int grid, cudaStream_t s);
 cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s);
+// The same with every row attending all of its request's keys.
+cudaError_t launch_cross_f32(const ChunkParams &p, int grid, cudaStream_t s);
+cudaError_t launch_cross_bf16(const ChunkParams &p, int grid, cudaStream_t s);
 // The cut units of an attention launch of `grid` CTAs.
 cudaError_t launch_chunk_merge(const ChunkParams &p, int grid, bool f32, cudaStream_t s);
 

@@ -14,6 +14,10 @@
 // whole): 4 chunks of 60 tokens at 1000, 8 / 2 heads, 19.5 and 16.5; 12 at 1200,
 // 32 / 8 heads, 36.1 and 26.9; 16 single tokens at 1100, 23.2 and 17.0; but two
 // single tokens at 1900, few and long, 17.2 and 20.9.
+//
+// Cross attention (C::kCross) is cut the same way: a request's rows are those
+// of its `group` slots, its keys those of its memory, and every unit attends
+// all of them.
 #pragma once
 
 #include "mac_batch.cuh"
@@ -32,9 +36,9 @@ __host__ __device__ constexpr int log2i(int x) { return x <= 1 ? 0 : 1 + log2i(x
 
 struct ChunkUnit {
   int b, g, i;         // request, KV head, row tile of the request's new tokens
-  int a, n, row0;      // the request's tokens before the new ones, new tokens, first row
+  int a, n, row0;      // the request's tokens before the new ones (cross attention: its keys), new tokens, first row
   int tok0, n_tok;     // first row (token) of the unit in the batch, tokens in it
-  int pos0;            // tokens attended by its first token (its 1-based position)
+  int pos0;            // tokens attended by its first token (its 1-based position; cross attention: by all of them)
   int tiles;           // key tiles its last token attends
   long long at;        // cost position of its first tile
 };
@@ -50,6 +54,8 @@ template <typename C>
 struct ChunkPlan {
   static constexpr int ROWS = C::kRows, KT = C::kKeys, COST0 = C::kStart, W = C::kTile, WS = C::kTileHalf;
   static constexpr int kKt = log2i(KT);
+  static constexpr bool CROSS = C::kCross;
+  static constexpr int kNoKeys = 1 << 30;  // request(): rows without a key to attend, no error
 
   // of all requests before b, all KV heads: cost; units, those of half the rows
   // in the upper 32 bits
@@ -69,6 +75,7 @@ struct ChunkPlan {
   // with `a` tokens before its new ones; exact because one of KT and the
   // tokens per unit divides the other
   __device__ static long long tiles_before(int a, int lt, int k) {
+    if (CROSS) return (long long)k * (((long long)a + KT - 1) >> kKt);
     if (lt <= kKt) {
       const long long e = (a + (1LL << lt) - 1) >> lt;
       return ceil_sum(e + k, kKt - lt) - ceil_sum(e, kKt - lt);
@@ -83,7 +90,7 @@ struct ChunkPlan {
     if (n <= 0) return 0;
     const int u = units(n, lt);
     if (whole) return u;
-    return before(a, lt, u - 1, false) + COST0 + (((long long)a + n + KT - 1) >> kKt) * weight(n - ((u - 1) << lt), lt);
+    return before(a, lt, u - 1, false) + COST0 + (((long long)a + (CROSS ? 0 : n) + KT - 1) >> kKt) * weight(n - ((u - 1) << lt), lt);
   }
 
   // All threads of the block (a multiple of 32, at most 1024) call it.
@@ -99,10 +106,10 @@ struct ChunkPlan {
         int a, n;
         if (request(p, b, &a, &n) != 0) {
           bad = 1;
-          back |= p.q_start[b + 1] < p.q_start[b];
+          back |= CROSS ? p.q_start[(b + 1) * p.group] < p.q_start[b * p.group] : p.q_start[b + 1] < p.q_start[b];
         }
         if (n > 0) {
-          const int tiles = (int)(((long long)a + n + KT - 1) >> kKt);
+          const int tiles = (int)(((long long)a + (CROSS ? 0 : n) + KT - 1) >> kKt);
           top = max(top, COST0 + tiles * weight(n, lt0));
           top_half = max(top_half, COST0 + tiles * WS);
         }
@@ -159,18 +166,18 @@ struct ChunkPlan {
   // to attend).  Returns the status bits of a bad request; *rows, where
   // given, is the number of its rows that lie in the batch.
   __device__ static int request(const ChunkParams &p, int b, int *a, int *n, int *row0 = nullptr, int *rows = nullptr) {
-    const int r0 = p.q_start[b], r1 = p.q_start[b + 1], m = p.seq_len[b];
+    const int r0 = p.q_start[CROSS ? b * p.group : b], r1 = p.q_start[CROSS ? (b + 1) * p.group : b + 1], m = p.seq_len[b];
     const bool in = r0 >= 0 && r1 >= r0 && r1 <= p.T;
     const int k = in ? r1 - r0 : 0;
     if (row0) *row0 = r0;
     if (rows) *rows = k;
     *n = k;
-    *a = m - k;
+    *a = CROSS ? m : m - k;
     if (!in) return MAC_DEV_BAD_SEQ_LEN;
     if (k == 0) return 0;
-    if (m < k || m > p.max_len) {
+    if (m < (CROSS ? 1 : k) || m > p.max_len) {
       *a = *n = 0;
-      return MAC_DEV_BAD_SEQ_LEN;
+      return CROSS && m == 0 ? kNoKeys : MAC_DEV_BAD_SEQ_LEN;
     }
     return 0;
   }
@@ -212,8 +219,8 @@ struct ChunkPlan {
     u.i = i;
     u.tok0 = u.row0 + (i << lt);
     u.n_tok = min(1 << lt, u.n - (i << lt));
-    u.pos0 = u.a + (i << lt) + 1;
-    u.tiles = (int)(((long long)u.a + (i << lt) + u.n_tok + KT - 1) >> kKt);
+    u.pos0 = CROSS ? u.a : u.a + (i << lt) + 1;
+    u.tiles = (int)(((long long)u.a + (CROSS ? 0 : (i << lt) + u.n_tok) + KT - 1) >> kKt);
   }
 };
 
@@ -286,14 +293,14 @@ struct ChunkWalk {
 };
 
 // Rows of requests that cannot be attended (a length below its new tokens or
-// beyond the cache): out 0, lse -inf.  All threads of the grid take part.
+// beyond the cache, a memory without keys): out 0, lse -inf.  All threads of the grid take part.
 template <typename T, typename PLAN>
 __device__ void chunk_bad_requests(const ChunkParams &p) {
   for (int b = 0; b < p.B; ++b) {
     int a, n, row0, rows;
     const int st = PLAN::request(p, b, &a, &n, &row0, &rows);
     if (!st) continue;
-    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, st);
+    if (st != PLAN::kNoKeys && blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, st);
     T *out = (T *)p.out + (int64_t)row0 * p.Hq * kHeadDim;
     const int64_t step = (int64_t)gridDim.x * blockDim.x, i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     for (int64_t i = i0; i < (int64_t)rows * p.Hq * kHeadDim; i += step) out[i] = (T)0;

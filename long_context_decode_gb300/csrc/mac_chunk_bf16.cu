@@ -52,7 +52,7 @@ constexpr int kStK = 2, kStV = 3, kNSt = kStK + kStV;  // stages of the K ring a
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr float kLazy = 8.f;                  // growth of the maximum (base 2) that moves the reference
 static_assert(ChunkBf16::kRows == 2 * kTile && ChunkBf16::kKeys == kTile, "tiles");
-using Plan = ChunkPlan<ChunkBf16>;
+static_assert(sizeof(ChunkPlan<ChunkBf16>) == sizeof(ChunkPlan<CrossBf16>), "plans");
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -62,13 +62,15 @@ struct Maps {
 struct Piece {
   int b, g;           // request, KV head
   int tok0, n_tok;    // first token (row of the batch), tokens
-  int pos0;           // keys that the first token attends
+  int pos0;           // keys that the first token attends (cross attention: that all do)
   int t0, t1;         // key tiles
   int end0;           // normal: key tiles of row tile 0 end here (those of row tile 1 at t1)
   int pair;           // both groups on row tile 0, key tiles in turn
   int clear;          // keys of the last tile that exist, if V is to be cleared after them; else kTile
   int c0, c1;         // a cut unit's first and last CTA; else -1
   __device__ int n() const { return t1 - t0; }
+  template <bool CROSS>
+  __device__ int keys() const { return CROSS ? pos0 : pos0 + n_tok - 1; }  // of the unit
   __device__ bool cut() const { return c0 >= 0; }
   // key tiles of group w
   __device__ int count(int w) const { return pair ? (n() - w + 1) >> 1 : w ? t1 - t0 : max(0, end0 - t0); }
@@ -84,7 +86,7 @@ struct Control {
 };
 constexpr int kSmemBytes = (kNSt + 2) * kTileBytes + (int)sizeof(Control);
 static_assert(kSmemBytes <= (int)kMaxSmem, "shared memory of a CTA");
-static_assert(sizeof(Plan) <= kNSt * kTileBytes, "the plan is made where the stages go");
+static_assert(sizeof(ChunkPlan<ChunkBf16>) <= kNSt * kTileBytes, "the plan is made where the stages go");
 
 // ---- products ----------------------------------------------------------------
 // The products of a tile, D[128 x 128] (+)= A B in eight steps of depth 16;
@@ -160,7 +162,7 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *v) {
 // ---- copies (warps 8 and 11) ---------------------------------------------------
 // One ring's copies: key or value tiles into stages st0 .. st0 + NST - 1, and
 // (K) the Q tiles.  A paged tile is 8 pages of two 64-column halves, one copy each.
-template <bool PAGED, bool IS_K>
+template <bool PAGED, bool CROSS, bool IS_K>
 __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stages, uint32_t qbuf, Control *ct) {
   constexpr int NST = IS_K ? kStK : kStV, ST0 = IS_K ? 0 : kStK;
   const CUtensorMap *map = IS_K ? &maps.k : &maps.v;
@@ -170,7 +172,7 @@ __device__ void load_role(const ChunkParams &p, const Maps &maps, uint32_t stage
   uint32_t nq = 0, np = 0;  // Q tiles, pieces so far
   Piece q = {};
   while (ct->pieces.take(wait, np, q)) {
-    const int n_pages = (q.pos0 + q.n_tok - 1 + kPage - 1) / kPage;  // of the unit's keys
+    const int n_pages = (q.keys<CROSS>() + kPage - 1) / kPage;  // of the unit's keys
     auto page = [&](int t) {  // page of this lane's copy; out of range where there is none: the copy fills with zeros
       const int k = t * (kTile / kPage) + pg;
       int id = k < n_pages ? p.kv.page_table[(int64_t)q.b * p.kv.max_pages + k] : -1;
@@ -345,10 +347,11 @@ __device__ void mma_role(const ChunkParams &p, uint32_t stages, uint32_t qbuf, C
 // may be anything, so those rows are cleared in shared memory before the
 // product reads them.  That waits for the products, so it comes one piece
 // behind the walk.
-__device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, const Plan &plan) {
+template <typename C>
+__device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, const ChunkPlan<C> &plan) {
   const int lane = threadIdx.x & 31;
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
-  ChunkWalk<ChunkBf16> walk;
+  ChunkWalk<C> walk;
   walk.start(p, plan);
   fence_proxy_async();  // the plan has been read: its place is the stages'
   uint32_t nt = 0, last_v = 0;  // tiles cleared; V uses before the next piece
@@ -367,9 +370,9 @@ __device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, co
       q.pos0 = u.pos0;
       q.t0 = x.t0;
       q.t1 = x.t1;
-      q.end0 = min(x.t1, (u.pos0 + kTile / p.G - 1 + kTile - 1) / kTile);
+      q.end0 = C::kCross ? x.t1 : min(x.t1, (u.pos0 + kTile / p.G - 1 + kTile - 1) / kTile);
       q.pair = u.n_tok * p.G <= kTile;
-      q.clear = x.t1 == u.tiles ? min(kTile, u.a + u.n - (x.t1 - 1) * kTile) : kTile;
+      q.clear = x.t1 == u.tiles ? min(kTile, u.a + (C::kCross ? 0 : u.n) - (x.t1 - 1) * kTile) : kTile;
       q.c0 = cut ? walk.cta_of(u, 0) : -1;
       q.c1 = cut ? walk.cta_of(u, u.tiles - 1) : -1;
     }
@@ -393,7 +396,7 @@ __device__ void walk_role(const ChunkParams &p, uint8_t *stages, Control *ct, co
 }
 
 // ---- softmax, output (warps 0-7) --------------------------------------------------
-template <bool PAGED>
+template <bool PAGED, bool CROSS>
 __device__ void softmax_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   const int tid = threadIdx.x, w = tid >> 7, r = tid & 127, lane = tid & 31;
   const uint32_t lanes = (uint32_t)((tid >> 5) & 3) << 21;  // this warp's 32 TMEM lanes
@@ -407,9 +410,9 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   Piece q = {};
   while (ct->pieces.take(wait, np, q)) {
     const int tok = ((q.pair ? 0 : w * kTile) + r) / p.G;   // token of this row
-    const int lim = q.pos0 + tok;                         // it attends keys [0, lim)
+    const int lim = CROSS ? q.pos0 : q.pos0 + tok;        // it attends keys [0, lim)
     const int mine = q.count(w), step = q.pair ? 2 : 1, first = q.t0 + (q.pair ? w : 0);
-    const int n_keys = q.pos0 + q.n_tok - 1;
+    const int n_keys = q.keys<CROSS>();
     const int n_rows = q.n_tok * p.G;
     // a warp without a row of the unit only keeps the order of the tiles:
     // its weights are whatever TMEM holds, and so are its rows of O
@@ -588,8 +591,9 @@ __device__ void softmax_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   if (status) set_status(p.status, status);
 }
 
-template <bool PAGED>
+template <bool PAGED, typename C>
 __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps) {
+  using Plan = ChunkPlan<C>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   griddep_launch_dependents();
@@ -651,14 +655,14 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   }
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_role<PAGED>(p, ct, tmem);
+    softmax_role<PAGED, C::kCross>(p, ct, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) load_role<PAGED, true>(p, maps, smem_addr(smem), smem_addr(qbuf), ct);
-    else if (warp == 11) load_role<PAGED, false>(p, maps, smem_addr(smem), smem_addr(qbuf), ct);
+    if (warp == 8) load_role<PAGED, C::kCross, true>(p, maps, smem_addr(smem), smem_addr(qbuf), ct);
+    else if (warp == 11) load_role<PAGED, C::kCross, false>(p, maps, smem_addr(smem), smem_addr(qbuf), ct);
     else if (warp == 9) {
       mma_role(p, smem_addr(smem), smem_addr(qbuf), ct, tmem);
-    } else walk_role(p, smem, ct, plan);
+    } else walk_role<C>(p, smem, ct, plan);
   }
   tc_fence_before();
   block_sync();
@@ -691,18 +695,17 @@ bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool PAGED>
+template <bool PAGED, typename C>
 cudaError_t launch(const ChunkParams &p, const Maps &maps, int grid, cudaStream_t s) {
   // with fewer registers at launch the split between the roles would wait forever
   static DeviceFlags done;
-  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED>, done, kSmemBytes, (256 * kRegsSoftmax + 128 * kRegsOther) / kThr);
+  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED, C>, done, kSmemBytes, (256 * kRegsSoftmax + 128 * kRegsOther) / kThr);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_kernel<PAGED>, grid, kThr, kSmemBytes, s, p, maps);
+  return launch_dependent(chunk_kernel<PAGED, C>, grid, kThr, kSmemBytes, s, p, maps);
 }
 
-}  // namespace
-
-cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s) {
+template <typename C>
+cudaError_t launch(const ChunkParams &p, int grid, cudaStream_t s) {
   Maps maps;
   const cuuint64_t row = kHeadDim * 2;
   const cuuint32_t G = p.G;
@@ -726,7 +729,12 @@ cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s) {
       if (!encode(m, base, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
   }
-  return p.kv.paged ? launch<true>(p, maps, grid, s) : launch<false>(p, maps, grid, s);
+  return p.kv.paged ? launch<true, C>(p, maps, grid, s) : launch<false, C>(p, maps, grid, s);
 }
+
+}  // namespace
+
+cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s) { return launch<ChunkBf16>(p, grid, s); }
+cudaError_t launch_cross_bf16(const ChunkParams &p, int grid, cudaStream_t s) { return launch<CrossBf16>(p, grid, s); }
 
 }  // namespace mac

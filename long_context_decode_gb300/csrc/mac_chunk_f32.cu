@@ -48,15 +48,16 @@ constexpr int kRegsLaunch = 128, kRegsSoft = 232, kRegsSplit = 104, kRegsMma = 7
 static_assert(kRegsSoft + 2 * kRegsSplit + kRegsMma <= 4 * kRegsLaunch && kThr * kRegsLaunch <= 65536, "the split comes out of the launch's registers");
 constexpr int kQPart = kRows * kHeadDim * 2, kKvPart = kKeys * kHeadDim * 2;  // bytes of one bf16 part of a tile
 constexpr uint32_t kColS = 0, kColS1 = 64, kColP = 128, kColO = 256;  // TMEM columns: S twice, P, P V
-using Plan = ChunkPlan<ChunkF32>;
 
 // A piece of a unit, as the roles see it.
 struct Piece {
   int b, g;           // request, KV head
   int tok0, n_tok;    // first token (row of the batch), tokens
-  int pos0;           // keys that the first token attends
+  int pos0;           // keys that the first token attends (cross attention: that all do)
   int t0, t1;         // key tiles
   int c0, c1;         // a cut unit's first and last CTA; else -1
+  template <bool CROSS>
+  __device__ int keys() const { return CROSS ? pos0 : pos0 + n_tok - 1; }  // of the unit
 };
 
 struct Control {
@@ -67,7 +68,7 @@ struct Control {
   PieceRing<Piece> pieces;
 };
 constexpr int kSmemBytes = 3 * kQPart + 6 * kKvPart + (int)sizeof(Control);
-static_assert(kSmemBytes <= (int)kMaxSmem && sizeof(Plan) <= 6 * kKvPart, "shared memory of a CTA");
+static_assert(kSmemBytes <= (int)kMaxSmem && sizeof(ChunkPlan<ChunkF32>) <= 6 * kKvPart, "shared memory of a CTA");
 
 // ---- products ----------------------------------------------------------------
 // 128 x 64 (+)= 128 x 128 . 128 x 64 of one part of Q and one of K; 128 x 128
@@ -188,7 +189,7 @@ __device__ __forceinline__ float4 load_if(const float *src, bool ok) {
   return f;
 }
 
-template <bool PAGED>
+template <bool PAGED, bool CROSS>
 __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, uint8_t *vbuf, Control *ct) {
   const int lane = threadIdx.x & 31, me_q = (threadIdx.x >> 5) - 4, me = me_q & (kConv - 1);
   const bool is_k = me_q < kConv;  // one copy of the code for both: see above
@@ -204,7 +205,7 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
     if (lane == 0) mbar_arrive(smem_addr(bar));
   };
   while (ct->pieces.take(wait, np, q)) {
-    const int n_rows = q.n_tok * p.G, n_keys = q.pos0 + q.n_tok - 1;
+    const int n_rows = q.n_tok * p.G, n_keys = q.keys<CROSS>();
     // this warp's 16 rows of tile t: the element of their first one (-1: no
     // page), and how many of them are keys of the unit
     auto at = [&](int t) -> int64_t {
@@ -252,9 +253,10 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
 }
 
 // ---- the walk (warp 13) -----------------------------------------------------------
-__device__ void walk_role(const ChunkParams &p, Control *ct, const Plan &plan) {
+template <typename C>
+__device__ void walk_role(const ChunkParams &p, Control *ct, const ChunkPlan<C> &plan) {
   Waiter wait{&ct->abort, p.status, p.wait_limit, false};
-  ChunkWalk<ChunkF32> walk;
+  ChunkWalk<C> walk;
   walk.start(p, plan);
   for (uint32_t i = 0;; ++i) {
     ChunkPiece x = {};
@@ -272,7 +274,7 @@ __device__ void walk_role(const ChunkParams &p, Control *ct, const Plan &plan) {
 }
 
 // ---- softmax and output (warps 0-3) -----------------------------------------------
-template <bool PAGED>
+template <bool PAGED, bool CROSS>
 __device__ void row_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   const int tid = threadIdx.x, r = tid, lane = tid & 31;
   const uint32_t lanes = (uint32_t)(tid >> 5) << 21;  // this warp's 32 TMEM lanes
@@ -287,8 +289,8 @@ __device__ void row_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
     if (lane == 0) mbar_arrive(smem_addr(bar));
   };
   while (ct->pieces.take(wait, np, q)) {
-    const int lim = q.pos0 + r / p.G;  // keys [0, lim) are the row's
-    const int n = q.t1 - q.t0, n_rows = q.n_tok * p.G, n_keys = q.pos0 + q.n_tok - 1;
+    const int lim = CROSS ? q.pos0 : q.pos0 + r / p.G;  // keys [0, lim) are the row's
+    const int n = q.t1 - q.t0, n_rows = q.n_tok * p.G, n_keys = q.keys<CROSS>();
     const bool idle = (r & ~31) >= n_rows;  // no row of this warp: it only keeps the order of the tiles
     float m = -INFINITY, l = 0.f, o[kHeadDim];
 #pragma unroll
@@ -422,8 +424,9 @@ __device__ void row_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   if (status) set_status(p.status, status);
 }
 
-template <bool PAGED>
+template <bool PAGED, typename C>
 __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+  using Plan = ChunkPlan<C>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   griddep_launch_dependents();
@@ -476,33 +479,36 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   }
   if (warp < 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    row_role<PAGED>(p, ct, tmem);
+    row_role<PAGED, C::kCross>(p, ct, tmem);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSplit));
-    split_role<PAGED>(p, qbuf, kbuf, vbuf, ct);
+    split_role<PAGED, C::kCross>(p, qbuf, kbuf, vbuf, ct);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == 12) mma_role(p, smem_addr(qbuf), smem_addr(kbuf), smem_addr(vbuf), ct, tmem);
-    else if (warp == 13) walk_role(p, ct, plan);
+    else if (warp == 13) walk_role<C>(p, ct, plan);
   }
   tc_fence_before();
   block_sync();
   if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <bool PAGED>
+template <bool PAGED, typename C>
 cudaError_t launch(const ChunkParams &p, int grid, cudaStream_t s) {
   // with fewer registers at launch the split between the roles would wait forever
   static DeviceFlags done;
-  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED>, done, kSmemBytes, kRegsLaunch);
+  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED, C>, done, kSmemBytes, kRegsLaunch);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_kernel<PAGED>, grid, kThr, kSmemBytes, s, p);
+  return launch_dependent(chunk_kernel<PAGED, C>, grid, kThr, kSmemBytes, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_f32(const ChunkParams &p, int grid, cudaStream_t s) {
-  return p.kv.paged ? launch<true>(p, grid, s) : launch<false>(p, grid, s);
+  return p.kv.paged ? launch<true, ChunkF32>(p, grid, s) : launch<false, ChunkF32>(p, grid, s);
+}
+cudaError_t launch_cross_f32(const ChunkParams &p, int grid, cudaStream_t s) {
+  return p.kv.paged ? launch<true, CrossF32>(p, grid, s) : launch<false, CrossF32>(p, grid, s);
 }
 
 }  // namespace mac

@@ -371,6 +371,66 @@ cudaError_t launch_step(StepParams p, const mac_config *c, cudaStream_t s) {
   return f32 ? launch_step_f32(p, grid, s) : launch_step_bf16(p, grid, s);
 }
 
+// Chunk attention (group 0) and cross attention (slots per memory).
+int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int32_t *q_start, int32_t group,
+                const int32_t *seq_len, int32_t n_tokens, const mac_kv *kv, void *out, float *lse, cudaStream_t s) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_tokens(n_tokens)) != MAC_OK) return v;
+  if (!chunk_ws || !q || !q_start || !seq_len || !out || q == out || !aligned16(chunk_ws) || !aligned16(q) ||
+      !aligned16(out) || !aligned(q_start, 4) || !aligned(seq_len, 4) || !aligned(lse, 4))
+    return MAC_ERR_INVALID_ARG;
+  if ((v = check_kv(cfg, kv)) != MAC_OK) return v;
+  const bool cross = group > 0;
+  if ((int64_t)cfg->batch * group > kMaxTokens) return MAC_ERR_UNSUPPORTED;
+  const ChunkLayout L = chunk_layout(cfg, n_tokens);
+  uint8_t *ws = (uint8_t *)chunk_ws;
+  ChunkParams p;
+  memset(&p, 0, sizeof p);
+  p.B = cfg->batch;
+  p.Hq = cfg->n_q_heads;
+  p.Hkv = cfg->n_kv_heads;
+  p.G = cfg->n_q_heads / cfg->n_kv_heads;
+  p.T = n_tokens;
+  p.q_scale = q_scale(cfg);
+  p.kv = kv_view(cfg, kv);
+  p.max_len = max_len(cfg, p.kv);
+  if (p.max_len > 0x7ffffe00) p.max_len = 0x7ffffe00;  // key numbers, rounded up to a tile, in 32 bits
+  p.q = q;
+  p.q_start = q_start;
+  p.seq_len = seq_len;
+  p.group = cross ? group : 1;
+  p.out = out;
+  p.lse = lse;
+  p.status = (uint32_t *)(ws + L.ctl);
+  p.notes = (int4 *)(ws + L.notes);
+  p.part = (float *)(ws + L.part);
+  p.part_rows = L.part_rows;
+  p.wait_limit = t_wait_limit > 0 ? t_wait_limit : kWaitLimit;
+  p.withhold = t_withhold;
+  t_wait_limit = 0;
+  t_withhold = -1;
+  const int sms = num_sms();
+  if (sms < 1) return MAC_ERR_CUDA;
+  note_launch(s, nullptr, nullptr);
+  const bool f32 = cfg->dtype == MAC_F32;
+  const int grid = sms < kChunkGrid ? sms : kChunkGrid;
+  if ((cross ? (f32 ? launch_cross_f32(p, grid, s) : launch_cross_bf16(p, grid, s))
+             : (f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s))) != cudaSuccess)
+    return MAC_ERR_CUDA;
+  // No unit is cut when a CTA is there for each and none is long, whatever
+  // the lengths on the device: then nothing needs merging.
+  auto each = [&](auto c, int rows, int tile_cost) {
+    using C = decltype(c);
+    const int64_t tiles = (C::kMinShare + C::kCut - C::kStart) / tile_cost;  // an equal share is at least kMinShare
+    return (n_tokens / (rows / p.G) + (int64_t)p.B) * p.Hkv <= grid && p.max_len <= tiles * C::kKeys;
+  };
+  if (f32 ? each(ChunkF32{}, ChunkF32::kRows, ChunkF32::kTile)
+          : each(ChunkBf16{}, ChunkBf16::kRows, ChunkBf16::kTile) || each(ChunkBf16{}, ChunkBf16::kRows / 2, ChunkBf16::kTileHalf))
+    return MAC_OK;
+  return launch_chunk_merge(p, grid, f32, s) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+}
+
 // Inside a stream capture the record becomes an event-record node of the
 // graph (timestamped at replay), not a capture-time dependency marker.
 cudaError_t record_phase(int i, cudaStream_t s) {
@@ -691,57 +751,14 @@ int mac_write_kv(const mac_config *cfg, void *chunk_ws, const void *q, int64_t q
 int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
                         const int32_t *q_start, const int32_t *seq_len, int32_t n_tokens,
                         const mac_kv *kv, void *out, float *lse, void *stream) {
-  int v = validate(cfg);
-  if (v != MAC_OK) return v;
-  if ((v = check_tokens(n_tokens)) != MAC_OK) return v;
-  if (!chunk_ws || !q || !q_start || !seq_len || !out || q == out || !aligned16(chunk_ws) || !aligned16(q) ||
-      !aligned16(out) || !aligned(q_start, 4) || !aligned(seq_len, 4) || !aligned(lse, 4))
-    return MAC_ERR_INVALID_ARG;
-  if ((v = check_kv(cfg, kv)) != MAC_OK) return v;
-  const ChunkLayout L = chunk_layout(cfg, n_tokens);
-  uint8_t *ws = (uint8_t *)chunk_ws;
-  ChunkParams p;
-  memset(&p, 0, sizeof p);
-  p.B = cfg->batch;
-  p.Hq = cfg->n_q_heads;
-  p.Hkv = cfg->n_kv_heads;
-  p.G = cfg->n_q_heads / cfg->n_kv_heads;
-  p.T = n_tokens;
-  p.q_scale = q_scale(cfg);
-  p.kv = kv_view(cfg, kv);
-  p.max_len = max_len(cfg, p.kv);
-  if (p.max_len > 0x7ffffe00) p.max_len = 0x7ffffe00;  // key numbers, rounded up to a tile, in 32 bits
-  p.q = q;
-  p.q_start = q_start;
-  p.seq_len = seq_len;
-  p.out = out;
-  p.lse = lse;
-  p.status = (uint32_t *)(ws + L.ctl);
-  p.notes = (int4 *)(ws + L.notes);
-  p.part = (float *)(ws + L.part);
-  p.part_rows = L.part_rows;
-  p.wait_limit = t_wait_limit > 0 ? t_wait_limit : kWaitLimit;
-  p.withhold = t_withhold;
-  t_wait_limit = 0;
-  t_withhold = -1;
-  cudaStream_t s = (cudaStream_t)stream;
-  const int sms = num_sms();
-  if (sms < 1) return MAC_ERR_CUDA;
-  note_launch(s, nullptr, nullptr);
-  const bool f32 = cfg->dtype == MAC_F32;
-  const int grid = sms < kChunkGrid ? sms : kChunkGrid;
-  if ((f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s)) != cudaSuccess) return MAC_ERR_CUDA;
-  // No unit is cut when a CTA is there for each and none is long, whatever
-  // the lengths on the device: then nothing needs merging.
-  auto each = [&](auto c, int rows, int tile_cost) {
-    using C = decltype(c);
-    const int64_t tiles = (C::kMinShare + C::kCut - C::kStart) / tile_cost;  // an equal share is at least kMinShare
-    return (n_tokens / (rows / p.G) + (int64_t)p.B) * p.Hkv <= grid && p.max_len <= tiles * C::kKeys;
-  };
-  if (f32 ? each(ChunkF32{}, ChunkF32::kRows, ChunkF32::kTile)
-          : each(ChunkBf16{}, ChunkBf16::kRows, ChunkBf16::kTile) || each(ChunkBf16{}, ChunkBf16::kRows / 2, ChunkBf16::kTileHalf))
-    return MAC_OK;
-  return launch_chunk_merge(p, grid, f32, s) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+  return attend_rows(cfg, chunk_ws, q, q_start, 0, seq_len, n_tokens, kv, out, lse, (cudaStream_t)stream);
+}
+
+int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, const int32_t *q_start,
+                        int32_t group, const int32_t *mem_len, int32_t n_tokens, const mac_kv *kv,
+                        void *out, float *lse, void *stream) {
+  if (group < 1) return MAC_ERR_INVALID_ARG;
+  return attend_rows(cfg, chunk_ws, q, q_start, group, mem_len, n_tokens, kv, out, lse, (cudaStream_t)stream);
 }
 
 int mac_join_aux(void *ring_ws, void *stream_main) {

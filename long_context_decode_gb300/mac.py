@@ -25,7 +25,8 @@ EXPORTS = ("mac_workspace_size", "mac_ring_layout_of", "mac_init_rings", "mac_de
            "mac_full_attention", "mac_full_attention_noalloc", "mac_join_aux", "mac_release_ring",
            "mac_last_status", "mac_set_phase_events", "mac_set_trace", "mac_status_string",
            "mac_threshold_sq", "mac_reset_requests", "mac_test_wait_budget",
-           "mac_chunk_workspace_size", "mac_build_tables", "mac_write_kv", "mac_chunk_attention")
+           "mac_chunk_workspace_size", "mac_build_tables", "mac_write_kv", "mac_chunk_attention",
+           "mac_cross_attention")
 MAC_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -99,6 +100,7 @@ def load() -> ctypes.CDLL:
     L.mac_build_tables.argtypes = [P(mac_config), vp, P(mac_pages), vp, vp, vp, i32, vp, vp, vp, vp, vp]
     L.mac_write_kv.argtypes = [P(mac_config), vp, vp, i64, vp, i64, vp, i64, vp, vp, i32, P(mac_kv), vp, vp]
     L.mac_chunk_attention.argtypes = [P(mac_config), vp, vp, vp, vp, i32, P(mac_kv), vp, vp, vp]
+    L.mac_cross_attention.argtypes = [P(mac_config), vp, vp, vp, i32, vp, i32, P(mac_kv), vp, vp, vp]
     L.mac_status_string.argtypes = [ctypes.c_int]
     L.mac_status_string.restype = ctypes.c_char_p
     L.mac_threshold_sq.argtypes = [P(mac_config)]
@@ -281,6 +283,17 @@ def mac_chunk_attention(cfg, chunk_ws, q, q_start, seq_len, n_tokens, kv: mac_kv
                                       _ptr(q_start), _ptr(seq_len), n, ctypes.byref(kv) if kv is not None else None,
                                       _whole(out, rows * cfg.head_dim, "mac_chunk_attention: out"),
                                       _whole(lse, rows, "mac_chunk_attention: lse"), _stream(stream)), "mac_chunk_attention")
+
+
+def mac_cross_attention(cfg, chunk_ws, q, q_start, group, mem_len, n_tokens, kv: mac_kv, out, lse=None, stream=None):
+    """Attention of the rows of each source's ``group`` slots over the whole of
+    that source's memory; q, out and lse contiguous."""
+    n = int(n_tokens)
+    rows = n * cfg.n_q_heads
+    _check(load().mac_cross_attention(ctypes.byref(cfg), _ptr(chunk_ws), _whole(q, rows * cfg.head_dim, "mac_cross_attention: q"),
+                                      _ptr(q_start), int(group), _ptr(mem_len), n, ctypes.byref(kv) if kv is not None else None,
+                                      _whole(out, rows * cfg.head_dim, "mac_cross_attention: out"),
+                                      _whole(lse, rows, "mac_cross_attention: lse"), _stream(stream)), "mac_cross_attention")
 
 
 def mac_status_string(code: int) -> str:
