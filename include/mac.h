@@ -50,6 +50,8 @@ extern "C" {
 #define MAC_DEV_NONFINITE_Q 0x8    /* non-finite query: treated as a miss */
 #define MAC_DEV_BAD_COPY 0x10      /* a copy outside its tile was refused (internal check) */
 #define MAC_DEV_NO_ROOM 0x20       /* free pages or token rows ran out: request not admitted */
+#define MAC_DEV_BAD_PARENT 0x40    /* a slot's parent outside its group: the slot keeps what it has */
+#define MAC_DEV_NONFINITE_LOGIT 0x80 /* NaN or +inf among a beam's logits, or in its score: no candidates of it */
 
 /* ---- configuration ------------------------------------------------------ */
 enum { MAC_BF16 = 0, MAC_F32 = 1 };
@@ -330,6 +332,98 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
 int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, const int32_t *q_start,
                         int32_t group, const int32_t *mem_len, int32_t n_tokens, const mac_kv *kv,
                         void *out, float *lse, void *stream);
+
+/* ---- beam search --------------------------------------------------------
+ * The batch's slots form groups of n_beams slots next to one another: group g
+ * is slots g n_beams .. (g+1) n_beams - 1, a sequence's beams (cfg->batch is
+ * a multiple of n_beams).  A step decodes one token per slot, then:
+ * mac_beam_select chooses the next beams from the logits, mac_reorder_tables
+ * gives every slot its parent's history (pages, length), mac_reorder_state
+ * moves what each layer keeps per slot.  (The pages describe none of the
+ * three: the interfaces are this library's own.) */
+#define MAC_MAX_BEAMS 16
+#define MAC_MAX_CANDIDATES 32
+
+/* Bytes of beam_ws for mac_beam_select: zero-filled before its first use, for
+ * one stream at a time; its device status word is read by
+ * mac_last_status(cfg, beam_ws, ..). */
+int mac_beam_workspace_size(const mac_config *cfg, int32_t n_beams, int32_t vocab, int32_t n_out,
+                            size_t *beam_bytes);
+
+/* The n_out <= MAC_MAX_CANDIDATES best next tokens of every group's beams.
+ * logits: logits_dtype (MAC_BF16 | MAC_F32) rows of vocab <= 2^20 of every
+ * slot, row_stride >= vocab elements apart, on any element boundary.  scores:
+ * f32 [batch], the beams' sums of log probabilities; -inf: the beam has no
+ * candidates (all but one slot of a group before its first token), and its
+ * logits are not read.  A candidate is (beam j, token v) with score s =
+ * scores[j] + x_jv - ln sum_v exp x_jv; logits of -inf are no candidates.
+ * The order is that of the exact scores (by s, rounded no coarser than 2^-36),
+ * ties to the lowest (j, v), whatever the card's sums in fp32 make of it.
+ * done (int32 [batch] or NULL): a beam whose flag is set is finished and is
+ * one candidate, end_token with the beam's score; its logits are not read.
+ * end_token: a token, or any other number if there is none (then done must be
+ * NULL).
+ * Outputs, [batch / n_beams][n_out], best first: scores_out f32; parent int32,
+ * the beam's place in its group; token int32; done_out int32 or NULL: whether
+ * the token is end_token.  Where a group has fewer candidates: score -inf,
+ * parent -1, token -1, done 1.  placed != 0 (n_out = n_beams): instead of
+ * best first, the best child of each parent in the parent's slot and the
+ * others, best first, in the slots that are left, so that mac_reorder_state
+ * has the least to move.  A beam with a NaN or +inf logit (or score) has no
+ * candidates (MAC_DEV_NONFINITE_LOGIT).  scores_out and done_out may be scores
+ * and done themselves. */
+int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const void *logits,
+                    int32_t logits_dtype, int64_t row_stride, int32_t vocab, const float *scores,
+                    const int32_t *done, int32_t end_token, int32_t n_out, int32_t placed,
+                    float *scores_out, int32_t *parent, int32_t *token, int32_t *done_out,
+                    void *stream);
+
+/* Slots take over the histories of their parents.  parent: int32 [batch], the
+ * place in its group of the slot whose history a slot goes on from (as
+ * mac_beam_select gives it with n_out = n_beams), or -1: the slot is given
+ * up and is empty afterwards.  len_in, len_out: int32 [batch] tokens of every
+ * slot; a child has its parent's.  shared_in, shared_out: int32
+ * [batch][n_beams], for each slot of a group how many leading positions a
+ * slot has in common with it; the caller keeps the array, zero-filled at
+ * first, and only these calls write it.
+ *   Pages (pages == NULL for a contiguous cache): children share their
+ *     parent's pages.  A history whose last page is not full is parted: its
+ *     slot keeps that page if it goes on as its own child, else the child of
+ *     the lowest slot does, and every other child gets a free page, the k-th
+ *     from the top for the k-th such child of the batch.  Pages that no slot
+ *     of the group holds any more are put on the stack first, in order of
+ *     group, place in the table and slot, each once.  Table entries past a
+ *     slot's pages stay as they are.  Pages are shared within a group only,
+ *     and slots that share pages are given back here, with parent -1, not
+ *     with mac_build_tables' reset_flags.
+ *   A child whose free page is missing (MAC_DEV_NO_ROOM) is empty afterwards.
+ *     A parent outside [-1, n_beams) (MAC_DEV_BAD_PARENT) is taken for the
+ *     slot itself.  A group with a length outside [0, limit]
+ *     (MAC_DEV_BAD_SEQ_LEN) is passed over.  A held page id outside
+ *     [0, n_pages) is not put on the stack (MAC_DEV_BAD_PAGE), a page
+ *     parted from or to one is not copied.
+ * moves: int32 [batch][8] (16-byte aligned), what mac_reorder_state has to
+ * move into every slot: the slot copied from (-1: nothing to do), the first and
+ * last position whose ring entries may differ, the new length, the page
+ * parted from, the page that its rows are copied to (-1: none), those rows, 0.
+ * len_out may be len_in, shared_out shared_in.  The workspace is that of
+ * the batch calls, of any number of rows. */
+int mac_reorder_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pages, int32_t n_beams,
+                       const int32_t *parent, const int32_t *len_in, int32_t *len_out,
+                       const int32_t *shared_in, int32_t *shared_out, int32_t *moves, void *stream);
+
+/* One layer's part of the moves that mac_reorder_tables has left, in place,
+ * each slot from what its parent held before the call (slots may change
+ * places).  ring_ws (or NULL): the layer's rings, where the entries of the
+ * positions that parent and child do not share are moved.  Their mac_reset_requests
+ * goes with parent -1.  kv (or NULL): the layer's cache; contiguous, the
+ * keys and values of those positions; paged, the rows of parted pages
+ * (kv->page_table is not read).  Moves outside a group, the cache or its pages are
+ * reported (MAC_DEV_BAD_PARENT, _BAD_SEQ_LEN, _BAD_PAGE in chunk_ws) and
+ * left out.  Runs after an append still pending on an auxiliary stream for
+ * ring_ws, as mac_reset_requests does. */
+int mac_reorder_state(const mac_config *cfg, void *chunk_ws, void *ring_ws, int32_t n_beams,
+                      const int32_t *moves, const mac_kv *kv, void *stream);
 
 /* Make stream_main wait for the last append enqueued on ring_ws (no-op if
  * none is pending).  Needed before ending a stream capture that used a

@@ -8,6 +8,7 @@
 #include <unordered_map>
 
 #include "mac_batch.cuh"
+#include "mac_beam.cuh"
 #include "mac_common.cuh"
 
 using namespace mac;
@@ -270,6 +271,50 @@ int check_tokens(int32_t n_tokens) {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// The pool of a paged cache.
+int check_pages(const mac_pages *p) {
+  if (!p || !p->page_table || !p->free_pages || !p->n_free_in || !p->n_free_out || p->max_pages < 1 || p->n_pages < 1 ||
+      !aligned(p->page_table, 4) || !aligned(p->free_pages, 4) || !aligned(p->n_free_in, 4) || !aligned(p->n_free_out, 4))
+    return MAC_ERR_INVALID_ARG;
+  return MAC_OK;
+}
+
+// Beams per group, and that the slots are whole groups.
+int check_beams(const mac_config *c, int32_t n_beams) {
+  if (n_beams < 1) return MAC_ERR_INVALID_ARG;
+  if (n_beams > kMaxBeams) return MAC_ERR_UNSUPPORTED;
+  return c->batch % n_beams ? MAC_ERR_INVALID_ARG : MAC_OK;
+}
+
+int check_select(const mac_config *c, int32_t n_beams, int32_t vocab, int32_t n_out) {
+  const int v = check_beams(c, n_beams);
+  if (v != MAC_OK) return v;
+  if (vocab < 1 || n_out < 1) return MAC_ERR_INVALID_ARG;
+  return vocab > kMaxVocab || n_out > kMaxPicks ? MAC_ERR_UNSUPPORTED : MAC_OK;
+}
+
+// CTAs of a row with `per` logits per thread, rows starting up to `shift`
+// elements behind a 16-byte boundary.
+int select_segs(int vocab, int per, int shift) {
+  return (vocab + shift + kScanThreads * per - 1) / (kScanThreads * per);
+}
+
+// Selection workspace: the status word, then every piece's maximum and sum,
+// and its best logits.  Laid out for the smallest pieces.
+struct SelectLayout {
+  size_t ctl, ml, keys, total;
+};
+SelectLayout select_layout(const mac_config *c, int32_t vocab, int32_t n_out) {
+  const size_t pieces = (size_t)c->batch * select_segs(vocab, kScanLeast, 7);
+  SelectLayout L;
+  size_t off = 0;
+  L.ctl = off;   off = align_up(off + 64 * 4, 256);
+  L.ml = off;    off = align_up(off + pieces * sizeof(float2), 256);
+  L.keys = off;  off = align_up(off + pieces * n_out * 8, 256);
+  L.total = off;
+  return L;
+}
+
 // ---- per-ring events: the append of step n on stream_aux must finish before
 // step n+1 on the same ring reads or rewrites the rings ([MAC] K3 runs on an
 // auxiliary stream with a single event dependency).
@@ -309,6 +354,15 @@ unsigned long long capture_id_of(cudaStream_t s) {
   unsigned long long id = 0;
   if (cudaStreamGetCaptureInfo(s, &st, &id) != cudaSuccess) return 0;
   return st == cudaStreamCaptureStatusActive ? id : 0;
+}
+
+// Makes s wait for an append still pending on an auxiliary stream for these rings.
+bool wait_for_append(void *ring_ws, cudaStream_t s) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto it = g_rings.find(ring_ws);
+  if (it != g_rings.end() && it->second.pending && it->second.capture_id == capture_id_of(s))
+    return cudaStreamWaitEvent(s, it->second.aux_done, 0) == cudaSuccess;
+  return true;
 }
 
 // Scratch of mac_full_attention_noalloc: a fixed array inside the library,
@@ -677,10 +731,7 @@ int mac_build_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pag
   memset(&p, 0, sizeof p);
   p.paged = cfg->page_size != 0;
   if (p.paged) {
-    if (!pages->page_table || !pages->free_pages || !pages->n_free_in || !pages->n_free_out || pages->max_pages < 1 ||
-        pages->n_pages < 1 || !aligned(pages->page_table, 4) || !aligned(pages->free_pages, 4) ||
-        !aligned(pages->n_free_in, 4) || !aligned(pages->n_free_out, 4))
-      return MAC_ERR_INVALID_ARG;
+    if ((v = check_pages(pages)) != MAC_OK) return v;
   } else if (pages->capacity < 1) {
     return MAC_ERR_INVALID_ARG;
   }
@@ -761,6 +812,146 @@ int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, co
   return attend_rows(cfg, chunk_ws, q, q_start, group, mem_len, n_tokens, kv, out, lse, (cudaStream_t)stream);
 }
 
+int mac_beam_workspace_size(const mac_config *cfg, int32_t n_beams, int32_t vocab, int32_t n_out,
+                            size_t *beam_bytes) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_select(cfg, n_beams, vocab, n_out)) != MAC_OK) return v;
+  if (!beam_bytes) return MAC_ERR_INVALID_ARG;
+  *beam_bytes = select_layout(cfg, vocab, n_out).total;
+  return MAC_OK;
+}
+
+int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const void *logits,
+                    int32_t logits_dtype, int64_t row_stride, int32_t vocab, const float *scores,
+                    const int32_t *done, int32_t end_token, int32_t n_out, int32_t placed,
+                    float *scores_out, int32_t *parent, int32_t *token, int32_t *done_out,
+                    void *stream) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_select(cfg, n_beams, vocab, n_out)) != MAC_OK) return v;
+  if (logits_dtype != MAC_BF16 && logits_dtype != MAC_F32) return MAC_ERR_INVALID_ARG;
+  const int es = logits_dtype == MAC_F32 ? 4 : 2;
+  if (!beam_ws || !logits || !scores || !scores_out || !parent || !token || !aligned16(beam_ws) || !aligned(logits, es) ||
+      !aligned(scores, 4) || !aligned(done, 4) || !aligned(scores_out, 4) || !aligned(parent, 4) || !aligned(token, 4) ||
+      !aligned(done_out, 4) || row_stride < vocab || (placed && n_out != n_beams) ||
+      (done && (end_token < 0 || end_token >= vocab)) ||
+      // in place only where the outputs lie as the inputs do
+      (((const void *)scores == scores_out || (done && done == done_out)) && n_out != n_beams))
+    return MAC_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms < 1) return MAC_ERR_CUDA;
+  SelectParams p;
+  memset(&p, 0, sizeof p);
+  p.S = cfg->batch;
+  p.n = n_beams;
+  p.V = vocab;
+  p.n_out = n_out;
+  p.placed = placed != 0;
+  p.end = end_token;
+  p.stride = row_stride;
+  p.logits = logits;
+  p.scores = scores;
+  p.done = done;
+  p.scores_out = scores_out;
+  p.parent = parent;
+  p.token = token;
+  p.done_out = done_out;
+  const int shift = aligned16(logits) && row_stride * es % 16 == 0 ? 0 : 16 / es - 1;
+  p.per = 32;
+  while (p.per > kScanLeast && (int64_t)p.S * select_segs(vocab, p.per, shift) < 2 * sms) p.per /= 2;
+  p.segs = select_segs(vocab, p.per, shift);
+  const SelectLayout L = select_layout(cfg, vocab, n_out);
+  uint8_t *ws = (uint8_t *)beam_ws;
+  p.status = (uint32_t *)(ws + L.ctl);
+  p.ml = (float2 *)(ws + L.ml);
+  p.keys = (unsigned long long *)(ws + L.keys);
+  note_launch((cudaStream_t)stream, nullptr, nullptr);
+  return launch_select(p, logits_dtype, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+}
+
+int mac_reorder_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pages, int32_t n_beams,
+                       const int32_t *parent, const int32_t *len_in, int32_t *len_out,
+                       const int32_t *shared_in, int32_t *shared_out, int32_t *moves, void *stream) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_beams(cfg, n_beams)) != MAC_OK) return v;
+  if (!chunk_ws || !parent || !len_in || !len_out || !shared_in || !shared_out || !moves || !aligned16(chunk_ws) ||
+      !aligned(parent, 4) || !aligned(len_in, 4) || !aligned(len_out, 4) || !aligned(shared_in, 4) ||
+      !aligned(shared_out, 4) || !aligned16(moves))
+    return MAC_ERR_INVALID_ARG;
+  ReorderParams p;
+  memset(&p, 0, sizeof p);
+  p.paged = cfg->page_size != 0;
+  p.limit = cfg->max_context;
+  if (p.paged) {
+    if ((v = check_pages(pages)) != MAC_OK) return v;
+    const int64_t room = (int64_t)pages->max_pages * cfg->page_size;
+    if (room < p.limit) p.limit = room;
+    p.max_pages = pages->max_pages;
+    p.n_pages = pages->n_pages;
+    p.table = pages->page_table;
+    p.free_pages = pages->free_pages;
+    p.n_free_in = pages->n_free_in;
+    p.n_free_out = pages->n_free_out;
+  } else if (pages) {
+    if (pages->capacity < 1) return MAC_ERR_INVALID_ARG;
+    if (pages->capacity < p.limit) p.limit = pages->capacity;
+  }
+  p.S = cfg->batch;
+  p.n = n_beams;
+  p.parent = parent;
+  p.len_in = len_in;
+  p.len_out = len_out;
+  p.shared_in = shared_in;
+  p.shared_out = shared_out;
+  p.moves = (Move *)moves;
+  p.status = (uint32_t *)chunk_ws;
+  note_launch((cudaStream_t)stream, nullptr, nullptr);
+  return launch_reorder(p, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+}
+
+int mac_reorder_state(const mac_config *cfg, void *chunk_ws, void *ring_ws, int32_t n_beams,
+                      const int32_t *moves, const mac_kv *kv, void *stream) {
+  int v = validate(cfg);
+  if (v != MAC_OK) return v;
+  if ((v = check_beams(cfg, n_beams)) != MAC_OK) return v;
+  if (!chunk_ws || !moves || (!ring_ws && !kv) || !aligned16(chunk_ws) || !aligned16(ring_ws) || !aligned16(moves))
+    return MAC_ERR_INVALID_ARG;
+  if (kv && (!kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v) || (cfg->page_size ? kv->n_pages < 1 : kv->capacity < 1)))
+    return MAC_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int sms = num_sms();
+  if (sms < 1 || (ring_ws && !wait_for_append(ring_ws, s))) return MAC_ERR_CUDA;
+  StateParams p;
+  memset(&p, 0, sizeof p);
+  p.S = cfg->batch;
+  p.n = n_beams;
+  p.Hq = cfg->n_q_heads;
+  p.Hkv = cfg->n_kv_heads;
+  p.K = cfg->ring_k;
+  p.es = elem_size(cfg);
+  p.paged = cfg->page_size != 0;
+  p.moves = (const Move *)moves;
+  if (ring_ws) {
+    const mac_ring_layout R = ring_layout(cfg);
+    uint8_t *ring = (uint8_t *)ring_ws;
+    p.pos = (int32_t *)(ring + R.pos);
+    p.q = ring + R.q;
+    p.o = (float *)(ring + R.o);
+    p.lse = (float *)(ring + R.lse);
+  }
+  if (kv) {
+    p.k = (uint8_t *)const_cast<void *>(kv->k);
+    p.v = (uint8_t *)const_cast<void *>(kv->v);
+    p.capacity = kv->capacity;
+    p.n_pages = kv->n_pages;
+  }
+  p.status = (uint32_t *)chunk_ws;
+  note_launch(s, nullptr, nullptr);  // the next step reads these rings: it waits
+  return launch_state(p, sms, s) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+}
+
 int mac_join_aux(void *ring_ws, void *stream_main) {
   if (!ring_ws) return MAC_ERR_INVALID_ARG;
   cudaStream_t sm = (cudaStream_t)stream_main;
@@ -798,14 +989,7 @@ int mac_reset_requests(const mac_config *cfg, void *ring_ws, int32_t *reset_flag
   if (v != MAC_OK) return v;
   if (!ring_ws || !reset_flags || ((uintptr_t)reset_flags & 3u) != 0) return MAC_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
-  {
-    // after an append still pending on an auxiliary stream for these rings
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto it = g_rings.find(ring_ws);
-    if (it != g_rings.end() && it->second.pending && it->second.capture_id == capture_id_of(s)) {
-      if (cudaStreamWaitEvent(s, it->second.aux_done, 0) != cudaSuccess) return MAC_ERR_CUDA;
-    }
-  }
+  if (!wait_for_append(ring_ws, s)) return MAC_ERR_CUDA;
   const mac_ring_layout R = ring_layout(cfg);
   int32_t *pos = (int32_t *)((uint8_t *)ring_ws + R.pos);
   note_launch(s, nullptr, nullptr);

@@ -14,7 +14,8 @@ from . import build as _build
 
 MAC_OK, MAC_ERR_INVALID_ARG, MAC_ERR_UNSUPPORTED, MAC_ERR_CUDA = 0, -1, -2, -3
 MAC_DEV_BAD_SEQ_LEN, MAC_DEV_BAD_PAGE, MAC_DEV_WAIT_TIMEOUT, MAC_DEV_NONFINITE_Q, MAC_DEV_BAD_COPY = 1, 2, 4, 8, 16
-MAC_DEV_NO_ROOM = 32
+MAC_DEV_NO_ROOM, MAC_DEV_BAD_PARENT, MAC_DEV_NONFINITE_LOGIT = 32, 64, 128
+MAC_MAX_BEAMS, MAC_MAX_CANDIDATES = 16, 32
 MAC_TRACE_POINTS = 32
 MAC_BF16, MAC_F32 = 0, 1
 MAC_THR_ONE_MINUS_TAU, MAC_THR_TAU = 0, 1
@@ -26,7 +27,8 @@ EXPORTS = ("mac_workspace_size", "mac_ring_layout_of", "mac_init_rings", "mac_de
            "mac_last_status", "mac_set_phase_events", "mac_set_trace", "mac_status_string",
            "mac_threshold_sq", "mac_reset_requests", "mac_test_wait_budget",
            "mac_chunk_workspace_size", "mac_build_tables", "mac_write_kv", "mac_chunk_attention",
-           "mac_cross_attention")
+           "mac_cross_attention", "mac_beam_workspace_size", "mac_beam_select",
+           "mac_reorder_tables", "mac_reorder_state")
 MAC_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -101,6 +103,10 @@ def load() -> ctypes.CDLL:
     L.mac_write_kv.argtypes = [P(mac_config), vp, vp, i64, vp, i64, vp, i64, vp, vp, i32, P(mac_kv), vp, vp]
     L.mac_chunk_attention.argtypes = [P(mac_config), vp, vp, vp, vp, i32, P(mac_kv), vp, vp, vp]
     L.mac_cross_attention.argtypes = [P(mac_config), vp, vp, vp, i32, vp, i32, P(mac_kv), vp, vp, vp]
+    L.mac_beam_workspace_size.argtypes = [P(mac_config), i32, i32, i32, P(ctypes.c_size_t)]
+    L.mac_beam_select.argtypes = [P(mac_config), vp, i32, vp, i32, i64, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.mac_reorder_tables.argtypes = [P(mac_config), vp, P(mac_pages), i32, vp, vp, vp, vp, vp, vp, vp]
+    L.mac_reorder_state.argtypes = [P(mac_config), vp, vp, i32, vp, P(mac_kv), vp]
     L.mac_status_string.argtypes = [ctypes.c_int]
     L.mac_status_string.restype = ctypes.c_char_p
     L.mac_threshold_sq.argtypes = [P(mac_config)]
@@ -294,6 +300,49 @@ def mac_cross_attention(cfg, chunk_ws, q, q_start, group, mem_len, n_tokens, kv:
                                       _ptr(q_start), int(group), _ptr(mem_len), n, ctypes.byref(kv) if kv is not None else None,
                                       _whole(out, rows * cfg.head_dim, "mac_cross_attention: out"),
                                       _whole(lse, rows, "mac_cross_attention: lse"), _stream(stream)), "mac_cross_attention")
+
+
+def mac_beam_workspace_size(cfg: mac_config, n_beams: int, vocab: int, n_out: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mac_beam_workspace_size(ctypes.byref(cfg), int(n_beams), int(vocab), int(n_out), ctypes.byref(n)),
+           "mac_beam_workspace_size")
+    return n.value
+
+
+def mac_beam_select(cfg, beam_ws, n_beams, logits, scores, done, end_token, n_out, placed, scores_out, parent, token, done_out=None,
+                    stream=None):
+    """The n_out best next tokens of every group's beams.  logits: a [slots,
+    vocab] tensor of bf16 or fp32, its rows any distance apart."""
+    import torch
+    what, S, groups = "mac_beam_select", cfg.batch, cfg.batch // max(1, int(n_beams)) * int(n_out)
+    kinds = {torch.bfloat16: MAC_BF16, torch.float32: MAC_F32}
+    if logits.dim() != 2 or logits.shape[0] < S or logits.dtype not in kinds or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise MacError(f"{what}: logits must be {S} rows of bf16 or fp32, a row's elements end to end")
+    stride = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]  # (one row's stride may be anything)
+    _check(load().mac_beam_select(ctypes.byref(cfg), _ptr(beam_ws), int(n_beams), _ptr(logits), kinds[logits.dtype], stride,
+                                  logits.shape[1], _whole(scores, S, f"{what}: scores"), _whole(done, S, f"{what}: done"),
+                                  int(end_token), int(n_out), int(placed), _whole(scores_out, groups, f"{what}: scores_out"),
+                                  _whole(parent, groups, f"{what}: parent"), _whole(token, groups, f"{what}: token"),
+                                  _whole(done_out, groups, f"{what}: done_out"), _stream(stream)), what)
+
+
+def mac_reorder_tables(cfg, chunk_ws, pages: mac_pages | None, n_beams, parent, len_in, len_out, shared_in, shared_out, moves,
+                       stream=None):
+    """Slots take over their parents' pages, lengths and common positions; moves
+    ([slots, 8] int32) says what mac_reorder_state has to move."""
+    what, S, n = "mac_reorder_tables", cfg.batch, int(n_beams)
+    _check(load().mac_reorder_tables(ctypes.byref(cfg), _ptr(chunk_ws), ctypes.byref(pages) if pages is not None else None, n,
+                                     _whole(parent, S, f"{what}: parent"), _whole(len_in, S, f"{what}: len_in"),
+                                     _whole(len_out, S, f"{what}: len_out"), _whole(shared_in, S * n, f"{what}: shared_in"),
+                                     _whole(shared_out, S * n, f"{what}: shared_out"), _whole(moves, S * 8, f"{what}: moves"),
+                                     _stream(stream)), what)
+
+
+def mac_reorder_state(cfg, chunk_ws, ring, n_beams, moves, kv: mac_kv | None, stream=None):
+    """One layer's part of the moves: its rings (or None) and its cache (or None), in place."""
+    _check(load().mac_reorder_state(ctypes.byref(cfg), _ptr(chunk_ws), _ptr(ring), int(n_beams),
+                                    _whole(moves, cfg.batch * 8, "mac_reorder_state: moves"),
+                                    ctypes.byref(kv) if kv is not None else None, _stream(stream)), "mac_reorder_state")
 
 
 def mac_status_string(code: int) -> str:
