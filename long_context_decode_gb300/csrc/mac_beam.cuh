@@ -9,12 +9,14 @@ namespace mac {
 constexpr int kMaxBeams = MAC_MAX_BEAMS;
 constexpr int kMaxPicks = MAC_MAX_CANDIDATES;  // candidates that a selection returns per group
 constexpr int kMaxVocab = 1 << 20;
-// A CTA of the selection's scan takes kScanThreads * per logits of a row, per one of 8, 16, 32.
-constexpr int kScanThreads = 256, kScanLeast = 8;
+// The selection's scan cuts a row into at most kMaxPieces pieces, of a number of
+// steps: 16 bytes for each thread of a CTA.
+constexpr int kScanThreads = 256, kMaxPieces = 64;
 
 struct SelectParams {
   int S, n, V, n_out, placed, end;
-  int per, segs;                  // logits per thread, CTAs per row
+  int steps, segs;                // of a piece; pieces of a row
+  unsigned long long lists_inv, segs_inv;  // 2^40 / (n segs) and / segs, rounded up: i times it, shifted, is the quotient
   int64_t stride;                 // elements between rows
   const void *logits;
   const float *scores;            // [S]
@@ -22,7 +24,7 @@ struct SelectParams {
   float *scores_out;              // [S / n][n_out]
   int32_t *parent, *token, *done_out;
   float2 *ml;                     // [S][segs] maximum and sum of exp of a CTA's logits
-  unsigned long long *keys;       // [S][segs][n_out] its best ones; 0: none
+  unsigned long long *keys;       // [S][n_out][segs] its best ones; 0: none
   uint32_t *status;
 };
 

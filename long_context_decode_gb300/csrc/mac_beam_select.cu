@@ -4,13 +4,14 @@
 //   L_j = ln sum_v exp x_jv;   s_jv = c_j + x_jv - L_j;
 // the n_out largest s of the group, ties to the lowest (j, v).
 //
-// scan_kernel reads every logit once: a CTA holds a piece of a row in
-// registers, so the piece's maximum, its sum of exponentials and its best
-// logits come from one trip to memory.  Within a row the order of s is that
-// of x, so a piece's n_out best by (x, lowest v) are all that can be chosen of
-// it.  They are found by a threshold: the n_out-th largest of the maxima of
-// 32 groups of threads is a lower bound that few logits pass; those are
-// ranked by counting.  pick_kernel, a CTA per group, joins the pieces and
+// scan_kernel reads every logit once, a CTA a piece of a row: its threads keep
+// running sums of exponentials and their largest logit.  Within a row the order
+// of s is that of x, so a piece's n_out best by (x, lowest v) are all that can
+// be chosen of it.  They are found by a threshold: the n_out-th largest of the
+// maxima of 32 groups of threads is a lower bound that few logits pass.  The
+// logits of the few threads whose largest one passes are read again, by all
+// threads (by themselves they took half of all instructions, as nearly every
+// warp has such a thread); what passes is ranked by counting.  pick_kernel, a CTA per group, joins the pieces and
 // ranks the beams' candidates against one another.
 //
 // Across beams the order depends on L.  The sums are in fp32, so L is known to
@@ -18,9 +19,11 @@
 // (two beams' scores within twice that: once in some thousand groups), the
 // beams in question are summed again to 2^-38 and the candidates ranked anew.
 // So the choice is that of the exact scores, however the card adds.
+#include <cuda_bf16.h>
 #include <math.h>
 
 #include "mac_beam.cuh"
+#include "mac_tc.cuh"
 
 namespace mac {
 namespace {
@@ -28,11 +31,15 @@ namespace {
 constexpr int kThr = kScanThreads, kWarps = kThr / 32, kGroups8 = kThr / 8;
 static_assert(kGroups8 == 32 && kMaxPicks <= kGroups8, "a lane holds a group's maximum; the threshold is one of them");
 constexpr int kRoom = 1024;  // candidates that are ranked at once
-// Bound of the error of L.  An exponent t = (x - m) log2 e is off by 3 2^-24 |t|
-// (the difference, the product, the constant), and the mean of (m - x) under the
-// softmax is at most ln V <= 13.9: 2.5e-6 of the sum.  ex2 adds 2^-22, twice; a
-// thread's sum 10 2^-24, a CTA's 8 2^-24, the logarithm 2^-23: 4.2e-6 in all.
-constexpr double kSlack = 1.0 / (1 << 17);
+constexpr int kEarly = 4;    // keys that a thread of pick_kernel holds
+// Bound of the error of L, relative to the sum.  An exponent (x - ref) log2 e is
+// off by 2.3 2^-24 of itself (the difference, the product, the constant), and the
+// mean of ref - x under the softmax is at most ln V + 1 <= 14.9: 2.0e-6.  ex2 is
+// off by 2^-22: of a term, of the moves of its reference (1.6 with every move by
+// e^-1 or less), of the joins in a CTA and of the pieces: 1.1e-6.  Sums round 7, 8 and
+// 7 times by 2^-24 (a thread's batches are added with their rounded parts): 1.3e-6.
+// The logarithm 2^-23.  4.5e-6 in all.
+constexpr double kSlack = 5.0 / (1 << 20);
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ unsigned long long key_of(float x, int v) {
@@ -45,17 +52,34 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
 }
 __device__ __forceinline__ int token_of(unsigned long long key) { return (int)(0xffffffffu - (uint32_t)key); }
 
-// The n-th largest of the lanes' values (1 <= n <= 32).
-template <typename F>
-__device__ __forceinline__ F nth_largest(F g, int n) {
-  const int lane = threadIdx.x & 31;
+// Leaves the n-th largest of 32 values in *nth (1 <= n <= 32): eight threads rank a value.
+__device__ __forceinline__ void find_nth(const float *values, int n, float *nth) {
+  const int k = threadIdx.x >> 3, part = threadIdx.x & 7;
+  const float g = values[k];
+  const float4 o = reinterpret_cast<const float4 *>(values)[part];
   int above = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const F o = __shfl_sync(0xffffffffu, g, j);
-    above += o > g || (o == g && j < lane);
+  for (int j = 0; j < 4; ++j) {
+    const float x = j == 0 ? o.x : j == 1 ? o.y : j == 2 ? o.z : o.w;
+    above += x > g || (x == g && part * 4 + j < k);
   }
-  return __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == n - 1)) - 1);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) above += __shfl_xor_sync(0xffffffffu, above, d);
+  if (part == 0 && above == n - 1) *nth = g;
+}
+
+// put(i, rank of i) for each of c things, four threads to one; above(i, j): j goes before i.
+template <typename A, typename P>
+__device__ __forceinline__ void rank_all(int c, A above, P put) {
+  for (int i0 = 0; i0 < c; i0 += kThr / 4) {
+    const int i = i0 + (threadIdx.x >> 2);
+    int rank = 0;
+    if (i < c)
+      for (int j = threadIdx.x & 3; j < c; j += 4) rank += above(i, j);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (i < c && (threadIdx.x & 3) == 0) put(i, rank);
+  }
 }
 
 // Whether a beam has next tokens at all: not finished, with a finite score.
@@ -64,119 +88,197 @@ __device__ __forceinline__ bool goes_on(const SelectParams &p, int b) {
   return !(p.done && p.done[b] != 0) && c > -INFINITY && c < INFINITY;
 }
 
-template <typename T, int PER>
-__global__ void __launch_bounds__(kThr) scan_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int VEC = 16 / (int)sizeof(T), NV = PER / VEC;
-  __shared__ float gmax[kGroups8], wsum[kWarps];
+// The logits of a row: `head` elements up to a 16-byte boundary, `full` vectors of 16 bytes, a tail.
+template <typename T>
+struct Row {
+  static constexpr int VEC = 16 / (int)sizeof(T);
+  const T *at;
+  int head, full, tail0, V;
+  __device__ Row(const SelectParams &p, int b) {
+    at = (const T *)p.logits + b * p.stride;
+    V = p.V;
+    const int behind = (int)(((uintptr_t)at & 15) / sizeof(T));
+    head = behind ? min(VEC - behind, V) : 0;
+    full = (V - head) / VEC;
+    tail0 = head + full * VEC;
+  }
+  __device__ int token(int i) const { return head + i * VEC; }  // of vector i's first element
+  __device__ const uint4 *vec(int i) const { return reinterpret_cast<const uint4 *>(at + token(i)); }
+  // Element k of the head and the tail, -1: there is none.
+  __device__ int loose(int k) const {
+    const int v = k < head ? k : tail0 + k - head;
+    return k < head + V - tail0 ? v : -1;
+  }
+};
+
+// A running sum of exponentials, sh + sl relative to e^ref.  The reference moves
+// only when a logit is above it by more than 1, so that what a move rounds
+// counts for less with every later one.
+struct Running {
+  float ref = -INFINITY, sh = 0.f, sl = 0.f, mx = -INFINITY;
+  __device__ __forceinline__ void reach(float top) {
+    mx = fmaxf(mx, top);
+    if (top > ref + 1.f) {
+      const float f = ex2((ref - top) * kLog2e);
+      sh *= f;
+      sl *= f;
+      ref = top;
+    }
+  }
+  __device__ __forceinline__ float origin() const { return ref == -INFINITY ? 0.f : ref; }
+  __device__ __forceinline__ void add(float x) {  // rounded parts kept
+    const float a = sh + x, b = a - sh;
+    sl += (sh - (a - b)) + (x - b);
+    sh = a;
+  }
+};
+
+__device__ __forceinline__ float top_of(const uint4 &u, uint16_t) {
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float top_of(const uint4 &u, float) {
+  return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+
+// U vectors of a thread at a time, the next ones on their way meanwhile.
+template <typename T, int U>
+__global__ void __launch_bounds__(kThr, 4) scan_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int VEC = Row<T>::VEC;
+  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+  __shared__ __align__(16) float gmax[kGroups8];
+  __shared__ float wsum[kWarps], nth;
   __shared__ unsigned long long room[kRoom];
   __shared__ unsigned long long wbest[kWarps];
-  __shared__ int count;
+  __shared__ uint8_t passed[kThr];
+  __shared__ int count, n_passed;
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, seg = blockIdx.x, b = blockIdx.y;
   if (!goes_on(p, b)) return;
-  const T *row = (const T *)p.logits + b * p.stride;
-  // pieces start on 16-byte boundaries: the row starts `shift` elements behind one
-  const int shift = (int)(((uintptr_t)row & 15) / sizeof(T));
-  const int v0 = seg * (kThr * PER) + tid * VEC - shift;
-  uint4 raw[NV];
+  const Row<T> row(p, b);
+  const int i0 = seg * p.steps * kThr + tid;
+  if (tid == 0) count = n_passed = 0;
+
+  Running r;
+  uint4 cur[U], next[U];
+  auto load = [&](uint4 *x, int k) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = v0 + i * kThr * VEC;
-    constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-    raw[i] = make_uint4(kNone, kNone, kNone, kNone);
-    if (v >= 0 && v + VEC <= p.V) {
-      raw[i] = __ldcs(reinterpret_cast<const uint4 *>(row + v));
-    } else if (v < p.V && v + VEC > 0) {  // the row's ends
-      uint32_t *w = &raw[i].x;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (v + e >= 0 && v + e < p.V) {
-          if (sizeof(T) == 4) w[e] = reinterpret_cast<const uint32_t *>(row)[v + e];
-          else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (uint32_t)row[v + e] << 16 : (w[e / 2] & 0xffff0000u) | (uint32_t)row[v + e];
-        }
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + (k + u) * kThr;
+      x[u] = make_uint4(kNone, kNone, kNone, kNone);
+      if (k + u < p.steps && i < row.full) x[u] = *row.vec(i);
     }
-  }
-  if (tid == 0) count = 0;
-  float mx = -INFINITY;
+  };
+  load(cur, 0);
+  const int extra = seg == p.segs - 1 ? row.loose(tid) : -1;  // the last piece takes the row's ends
+  const float loose = extra >= 0 ? elem_f32<T>(row.at, extra) : -INFINITY;
+  for (int k = 0; k < p.steps; k += U) {
+    if (k + U < p.steps) load(next, k + U);
+    float top = top_of(cur[0], T());
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float f[VEC];
-    unpack16<T>(raw[i], f);
+    for (int u = 1; u < U; ++u) top = fmaxf(top, top_of(cur[u], T()));
+    r.reach(top);
+    const float o = -r.origin();
+    float2 acc[4] = {};
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) mx = fmaxf(mx, f[e]);
+    for (int u = 0; u < U; ++u) {
+      float f[VEC];
+      unpack16<T>(cur[u], f);
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        const float2 t = fma2(add2(make_float2(f[e], f[e + 1]), make_float2(o, o)), make_float2(kLog2e, kLog2e), make_float2(0.f, 0.f));
+        acc[e / 2 & 3] = add2(acc[e / 2 & 3], make_float2(ex2(t.x), ex2(t.y)));
+      }
+    }
+    const float2 s = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+    r.add(s.x + s.y);
+#pragma unroll
+    for (int u = 0; u < U; ++u) cur[u] = next[u];
   }
+  if (extra >= 0) {
+    r.reach(loose);
+    r.add(ex2((loose - r.origin()) * kLog2e));
+  }
+  const float mx = r.mx;
   float g = mx;
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
   if ((lane & 7) == 0) gmax[tid >> 3] = g;
   __syncthreads();
+  find_nth(gmax, p.n_out, &nth);
   g = gmax[lane];
-  const float least = nth_largest(g, p.n_out);
 #pragma unroll
   for (int d = 16; d; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
-  const float m = g, ref = m == -INFINITY ? 0.f : m;
-  // the sum; NaN and +inf make it NaN
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float f[VEC];
-    unpack16<T>(raw[i], f);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) sum[e & 3] += ex2((f[e] - ref) * kLog2e);
-  }
-  float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  const float m = g;
+  // NaN and +inf among the logits make the sum NaN
+  float s = r.sh + r.sl;
+  if (m > -INFINITY) s *= ex2((r.ref - m) * kLog2e);
 #pragma unroll
   for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   if (lane == 0) wsum[warp] = s;
-  if (mx >= least && mx > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float f[VEC];
-      unpack16<T>(raw[i], f);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (f[e] >= least && f[e] > -INFINITY) {
-          const int at = atomicAdd(&count, 1);
-          if (at < kRoom) room[at] = key_of(f[e], v0 + i * kThr * VEC + e);
-        }
+  __syncthreads();
+  const float least = nth;
+  // the threads whose logits may pass, looked through by all of them
+  if (mx >= least && mx > -INFINITY) passed[atomicAdd(&n_passed, 1)] = (uint8_t)tid;
+  __syncthreads();
+  auto take = [&](float x, int v) {
+    if (x >= least && x > -INFINITY) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kRoom) room[at] = key_of(x, v);
     }
+  };
+  const int n_vecs = n_passed * p.steps;
+  for (int q = tid; q < n_vecs; q += kThr) {
+    const int k = q / n_passed, i = (seg * p.steps + k) * kThr + passed[q - k * n_passed];
+    if (i >= row.full) continue;
+    const uint4 u = *row.vec(i);
+    float x[VEC];
+    unpack16<T>(u, x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) take(x[e], row.token(i) + e);
   }
+  if (extra >= 0) take(loose, extra);
   __syncthreads();
   const int c = count;
-  const int64_t piece = (int64_t)b * p.segs + seg;
-  unsigned long long *out = p.keys + piece * p.n_out;
+  unsigned long long *out = p.keys + (int64_t)b * p.n_out * p.segs + seg;  // its r-th best at out[r * segs]
   if (tid == 0) {
-    float all = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) all += wsum[w];
-    p.ml[piece] = make_float2(m, all);
+    float all = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
+    all += (wsum[4] + wsum[5]) + (wsum[6] + wsum[7]);
+    p.ml[(int64_t)b * p.segs + seg] = make_float2(m, all);
   }
   if (c <= kRoom) {
-    for (int i = tid; i < c; i += kThr) {
-      const unsigned long long k = room[i];
-      int rank = 0;
-      for (int j = 0; j < c; ++j) rank += room[j] > k;
-      if (rank < p.n_out) out[rank] = k;
-    }
-    for (int i = c + tid; i < p.n_out; i += kThr) out[i] = 0;
+    rank_all(c, [&](int i, int j) { return room[j] > room[i]; }, [&](int i, int rank) {
+      if (rank < p.n_out) out[rank * p.segs] = room[i];
+    });
+    for (int i = c + tid; i < p.n_out; i += kThr) out[i * p.segs] = 0;
     return;
   }
   // more logits of one value than there is room for: one at a time, the best below the last
-  unsigned long long last = ~0ull;
-  for (int r = 0; r < p.n_out; ++r) {
-    unsigned long long best = 0;
+  // f(value, token) of this thread's logits, read again
+  auto each = [&](auto f) {
+#pragma unroll 1
+    for (int k = 0; k < p.steps; ++k) {
+      const int i = i0 + k * kThr;
+      if (i >= row.full) break;
+      const uint4 u = *row.vec(i);
+      float x[VEC];
+      unpack16<T>(u, x);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float f[VEC];
-      unpack16<T>(raw[i], f);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (f[e] > -INFINITY) {
-          const unsigned long long k = key_of(f[e], v0 + i * kThr * VEC + e);
-          if (k < last && k > best) best = k;
-        }
+      for (int e = 0; e < VEC; ++e) f(x[e], row.token(i) + e);
     }
+    if (extra >= 0) f(loose, extra);
+  };
+  unsigned long long last = ~0ull;
+  for (int q = 0; q < p.n_out; ++q) {
+    unsigned long long best = 0;
+    each([&](float x, int v) {
+      if (x > -INFINITY) {
+        const unsigned long long k = key_of(x, v);
+        if (k < last && k > best) best = k;
+      }
+    });
 #pragma unroll
     for (int d = 16; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
     __syncthreads();  // the last round's have been read
@@ -184,10 +286,11 @@ __global__ void __launch_bounds__(kThr) scan_kernel(const __grid_constant__ Sele
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) best = max(best, wbest[w]);
-    if (tid == 0) out[r] = best;
+    if (tid == 0) out[q * p.segs] = best;
     last = best;
   }
 }
+static_assert(kWarps == 8, "the sum over the warps");
 
 // ---- the sum again, to 2^-38 ----------------------------------------------------
 // exp d for d <= 0 as an unevaluated sum of two floats, by the table method (P. T. P.
@@ -247,30 +350,64 @@ __device__ double precise_sum(const SelectParams &p, int b, float m, const Preci
 }
 
 // ---- the beams against one another -------------------------------------------------
-struct Pick {
-  double s;
-  int beam, token;
-};
-// x before y
-__device__ __forceinline__ bool before(const Pick &x, const Pick &y) {
-  return x.s > y.s || (x.s == y.s && (x.beam < y.beam || (x.beam == y.beam && x.token < y.token)));
+// fp64 is slow here (a warp's instruction takes 16 cycles of an SM), so
+// scores are compared as whole numbers, and the candidates that come into
+// question are found by their scores in fp32, less what those may be off by.
+__device__ __forceinline__ unsigned long long ordered(double s) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(s + 0.0);  // -0 and 0 are one score
+  return u >> 63 ? ~u : u | 1ull << 63;
 }
+__device__ __forceinline__ double of_ordered(unsigned long long u) {
+  return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
+}
+// A candidate: its score, ordered, and its place (beam << 20 | token).
+struct Pick {
+  unsigned long long s;
+  uint32_t at;
+  __device__ int beam() const { return (int)(at >> 20); }
+  __device__ int token() const { return (int)(at & (kMaxVocab - 1)); }
+};
+static_assert(kMaxVocab == 1 << 20 && kMaxBeams <= 1 << 11, "a place in 32 bits");
+// x before y
+__device__ __forceinline__ bool before(const Pick &x, const Pick &y) { return x.s > y.s || (x.s == y.s && x.at < y.at); }
 
 template <typename T>
 __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ SelectParams p) {
   __shared__ double base[kMaxBeams];      // c - L + its largest logit; of a finished beam c
-  __shared__ float top[kMaxBeams];        // its largest logit
+  __shared__ float base_f[kMaxBeams], top[kMaxBeams];  // base in fp32; its largest logit
   __shared__ int kind[kMaxBeams];         // 0: no candidates, 1: its tokens, 2: finished
-  __shared__ double gmax[kGroups8], wsum[kWarps];
+  __shared__ float wmax[kWarps][32];
+  __shared__ __align__(16) float gmax[32];
+  __shared__ double wsum[kWarps];
   __shared__ Pick room[kRoom];
   __shared__ Pick best[kMaxPicks], wbest[kWarps];
+  __shared__ uint16_t sorted[kRoom];      // places in `room`, best first
   __shared__ Precise precise;
+  __shared__ float nth;
   __shared__ int count, open;             // candidates in `room`; beams whose L is not known well enough
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = blockIdx.x * p.n;
   uint32_t status = 0;
+  // The group's keys, the pieces' best ones first, one to a thread in turn; the
+  // first of them are on their way before anything else is waited for.
+  const int lists = p.n * p.segs, n_keys = lists * p.n_out;
+  const unsigned long long *keys = p.keys + (int64_t)first * p.n_out * p.segs;
+  auto load_key = [&](int i, int *beam) {
+    const int rank = (int)((unsigned long long)i * p.lists_inv >> 40), list = i - rank * lists;
+    *beam = (int)((unsigned long long)list * p.segs_inv >> 40);
+    return keys[(int64_t)(*beam * p.n_out + rank) * p.segs + list - *beam * p.segs];
+  };
+  unsigned long long early[kEarly];
+  int early_beam[kEarly];
+#pragma unroll
+  for (int q = 0; q < kEarly; ++q) {
+    early[q] = early_beam[q] = 0;
+    if (tid + q * kThr < n_keys) early[q] = load_key(tid + q * kThr, &early_beam[q]);
+  }
   for (int j = warp; j < p.n; j += kWarps) {
+    const float2 *ml = p.ml + (int64_t)(first + j) * p.segs;
+    const float2 mine = lane < p.segs ? ml[lane] : make_float2(-INFINITY, 0.f);  // whatever it is worth: no wait for the score
     const float c = p.scores[first + j];
     int what = goes_on(p, first + j) ? 1 : 0;
     if (!what && c == c && c < INFINITY && c > -INFINITY) what = 2;
@@ -278,104 +415,113 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
     double l = 0.0;
     float m = -INFINITY;
     if (what == 1) {
-      const float2 *ml = p.ml + (int64_t)(first + j) * p.segs;
-      for (int i = lane; i < p.segs; i += 32) m = fmaxf(m, ml[i].x);
+      m = mine.x;
+      for (int i = lane + 32; i < p.segs; i += 32) m = fmaxf(m, ml[i].x);
 #pragma unroll
       for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      double sum = 0.0;
-      for (int i = lane; i < p.segs; i += 32) sum += (double)ml[i].y * (double)(ml[i].x == -INFINITY ? (ml[i].y == 0.f ? 0.f : ml[i].y) : ex2((ml[i].x - m) * kLog2e));
+      // an empty piece has sum 0, or NaN
+      auto share = [&](float2 x) { return x.x == -INFINITY ? x.y : x.y * ex2((x.x - m) * kLog2e); };
+      float sum = share(mine);
+      for (int i = lane + 32; i < p.segs; i += 32) sum += share(ml[i]);
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (!(sum < 1e30) || m == INFINITY) {  // NaN or +inf among the logits
+      if (!(sum < 1e30f) || m == INFINITY) {  // NaN or +inf among the logits
         what = 0;
         status |= MAC_DEV_NONFINITE_LOGIT;
       } else if (m == -INFINITY) {
         what = 0;
-      } else {
-        const float f = (float)sum;  // 1 <= sum <= 2^20
-        const int e = (int)(__float_as_uint(f) >> 23) - 127;
-        l = e * 0.6931471805599453 + (double)logf(f * __uint_as_float((uint32_t)(127 - e) << 23));
+      } else {  // 1 <= sum <= 2^20
+        const int e = (int)(__float_as_uint(sum) >> 23) - 127;
+        l = e * 0.6931471805599453 + (double)logf(sum * __uint_as_float((uint32_t)(127 - e) << 23));
       }
     }
     if (lane == 0) {
       kind[j] = what;
       base[j] = (double)c - l;
+      base_f[j] = (float)base[j];
       top[j] = m;
     }
   }
-  const int per_beam = p.segs * p.n_out, n_keys = p.n * per_beam;
-  const unsigned long long *keys = p.keys + (int64_t)first * per_beam;
-  // candidate i of the group; false: there is none
-  auto candidate = [&](int i, Pick &c) {
-    if (i >= n_keys) {  // a finished beam goes on as it is
-      c.beam = i - n_keys;
-      c.token = p.end;
-      c.s = base[c.beam];
-      return kind[c.beam] == 2;
+  // f(beam, key) of this thread's candidates; a finished beam's key is that of its end
+  auto candidates = [&](auto f) {
+#pragma unroll
+    for (int q = 0; q < kEarly; ++q)
+      if (early[q] != 0 && kind[early_beam[q]] == 1) f(early_beam[q], early[q]);
+    for (int i = tid + kEarly * kThr; i < n_keys; i += kThr) {
+      int beam;
+      const unsigned long long k = load_key(i, &beam);
+      if (kind[beam] == 1 && k != 0) f(beam, k);
     }
-    c.beam = i / per_beam;
-    if (kind[c.beam] != 1) return false;
-    const unsigned long long k = keys[i];
-    c.token = token_of(k);
-    c.s = base[c.beam] + ((double)value_of(k) - (double)top[c.beam]);
-    return k != 0;
+    if (tid < p.n && kind[tid] == 2) f(tid, 1ull);
+  };
+  auto rough = [&](int beam, unsigned long long k) { return kind[beam] == 2 ? base_f[beam] : base_f[beam] + (value_of(k) - top[beam]); };
+  auto exactly = [&](int beam, unsigned long long k) {
+    Pick x;
+    const bool end = kind[beam] == 2;
+    x.s = ordered(end ? base[beam] : base[beam] + ((double)value_of(k) - (double)top[beam]));
+    x.at = (uint32_t)beam << 20 | (uint32_t)(end ? p.end : token_of(k));
+    return x;
   };
   for (int pass = 0; pass < 2; ++pass) {
     if (tid == 0) count = open = 0;
     __syncthreads();
-    // a lower bound of the n_out-th best, from the maxima of groups of threads
-    double g = -INFINITY;
-    for (int i = tid; i < n_keys + p.n; i += kThr) {
-      Pick c;
-      if (candidate(i, c)) g = fmax(g, c.s);
-    }
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) g = fmax(g, __shfl_xor_sync(0xffffffffu, g, d));
-    if ((lane & 7) == 0) gmax[tid >> 3] = g;
+    // a lower bound of the n_out-th best, from the maxima of 32 groups of threads, those of a lane
+    float g = -INFINITY;
+    candidates([&](int beam, unsigned long long k) { g = fmaxf(g, rough(beam, k)); });
+    wmax[warp][lane] = g;
     __syncthreads();
-    const double least = nth_largest(gmax[lane], p.n_out) - 2 * kSlack;
-    for (int i = tid; i < n_keys + p.n; i += kThr) {
-      Pick c;
-      if (candidate(i, c) && c.s >= least) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kRoom) room[at] = c;
-      }
+    if (warp == 0) {
+      for (int w = 1; w < kWarps; ++w) g = fmaxf(g, wmax[w][lane]);
+      gmax[lane] = g;
     }
+    __syncthreads();
+    find_nth(gmax, p.n_out, &nth);
+    float widest = 0.f;
+    for (int j = 0; j < p.n; ++j)
+      if (kind[j]) widest = fmaxf(widest, fabsf(base_f[j]));
+    __syncthreads();
+    // rough scores are off by 2^-24 of the base, of the difference and of the sum: 2^-22 (|base| + |s|) in all, twice
+    const float least = nth == -INFINITY ? nth : nth - (2.f * (float)kSlack + (widest + fabsf(nth)) * (1.f / (1 << 20)));
+    candidates([&](int beam, unsigned long long k) {
+      if (rough(beam, k) >= least) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kRoom) room[at] = exactly(beam, k);
+      }
+    });
     __syncthreads();
     const int c = count;
     if (c <= kRoom) {
-      for (int i = tid; i < c; i += kThr) {
-        const Pick x = room[i];
-        int rank = 0, near = 0;
-        for (int j = 0; j < c; ++j) {
-          const Pick y = room[j];
-          rank += before(y, x);
-          if (y.beam != x.beam && fabs(y.s - x.s) <= 2 * kSlack && (kind[x.beam] == 1 || kind[y.beam] == 1))
-            near |= 1 << x.beam | 1 << y.beam;
-        }
-        if (rank < p.n_out) {
-          best[rank] = x;
-          if (near) atomicOr(&open, near);
-        }
+      rank_all(c, [&](int i, int j) { return before(room[j], room[i]); }, [&](int i, int rank) {
+        sorted[rank] = (uint16_t)i;
+        if (rank < p.n_out) best[rank] = room[i];
+      });
+      __syncthreads();
+      if (pass == 1) break;
+      // Neighbours of two beams whose order is open, down to where no candidate that counts is in question
+      for (int i = tid; i + 1 < c; i += kThr) {
+        const Pick x = room[sorted[i]], y = room[sorted[i + 1]];
+        if (x.beam() == y.beam() || (kind[x.beam()] == 2 && kind[y.beam()] == 2)) continue;
+        const double s = of_ordered(x.s);
+        if (s - of_ordered(y.s) <= 2 * kSlack && (i < p.n_out || of_ordered(best[p.n_out - 1].s) - s <= 2 * kSlack))
+          atomicOr(&open, 1 << x.beam() | 1 << y.beam());
       }
       __syncthreads();
-      if (pass == 1 || open == 0) break;
+      if (open == 0) break;
     } else if (pass == 0) {
       if (tid == 0) open = (1 << p.n) - 1;
       __syncthreads();
     } else {  // too many of one score: one at a time
       for (int r = 0; r < p.n_out; ++r) {
-        Pick x = {-INFINITY, kMaxBeams, 0};
-        for (int i = tid; i < n_keys + p.n; i += kThr) {
-          Pick y;
-          if (candidate(i, y) && before(y, x) && (r == 0 || before(best[r - 1], y))) x = y;
-        }
+        Pick x = {0, ~0u};
+        candidates([&](int beam, unsigned long long k) {
+          const Pick y = exactly(beam, k);
+          if (before(y, x) && (r == 0 || before(best[r - 1], y))) x = y;
+        });
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
           Pick y;
           y.s = __shfl_xor_sync(0xffffffffu, x.s, d);
-          y.beam = __shfl_xor_sync(0xffffffffu, x.beam, d);
-          y.token = __shfl_xor_sync(0xffffffffu, x.token, d);
+          y.at = __shfl_xor_sync(0xffffffffu, x.at, d);
           if (before(y, x)) x = y;
         }
         if (lane == 0) wbest[warp] = x;
@@ -400,7 +546,10 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
     for (int j = 0; j < p.n; ++j) {
       if (!(redo >> j & 1) || kind[j] != 1) continue;
       const double sum = precise_sum<T>(p, first + j, top[j], precise, wsum);
-      if (tid == 0) base[j] = (double)p.scores[first + j] - log(sum);
+      if (tid == 0) {
+        base[j] = (double)p.scores[first + j] - log(sum);
+        base_f[j] = (float)base[j];
+      }
     }
     __syncthreads();
   }
@@ -408,31 +557,35 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
   if (status && lane == 0) set_status(p.status, status);
   if (warp > 0) return;
   // results: lane i has the i-th best
-  Pick x = {-INFINITY, -1, -1};
-  if (lane < found) x = best[lane];
-  int over = lane >= found || x.token == p.end;
-  if (lane < found && kind[x.beam] == 2) over = 1;
+  float score = -INFINITY;
+  int beam = -1, token = -1;
+  if (lane < found) {
+    const Pick x = best[lane];
+    score = (float)of_ordered(x.s);
+    beam = x.beam();
+    token = x.token();
+  }
+  const int over = lane >= found || token == p.end || kind[max(beam, 0)] == 2;
   int at = lane;
   if (p.placed) {  // the best child of a surviving parent goes to the parent's slot, the others fill up in order
-    const bool live = lane < found;
-    bool eldest = live;
+    bool eldest = lane < found;
     for (int i = 0; i < p.n; ++i) {
-      const int o = __shfl_sync(0xffffffffu, x.beam, i);
-      if (i < lane && o == x.beam) eldest = false;
+      const int o = __shfl_sync(0xffffffffu, beam, i);
+      if (i < lane && o == beam) eldest = false;
     }
-    const uint32_t taken = __reduce_or_sync(0xffffffffu, eldest ? 1u << x.beam : 0u);
+    const uint32_t taken = __reduce_or_sync(0xffffffffu, eldest ? 1u << beam : 0u);
     const uint32_t rest = __ballot_sync(0xffffffffu, !eldest && lane < p.n);
     int k = __popc(rest & ((1u << lane) - 1));
-    if (eldest) at = x.beam;
+    if (eldest) at = beam;
     else
       for (at = 0; at < 31; ++at)
         if (!(taken >> at & 1) && k-- == 0) break;
   }
   if (lane < p.n_out) {
     const int64_t o = (int64_t)blockIdx.x * p.n_out + at;
-    p.scores_out[o] = (float)x.s;
-    p.parent[o] = x.beam;
-    p.token[o] = x.token;
+    p.scores_out[o] = score;
+    p.parent[o] = beam;
+    p.token[o] = token;
     if (p.done_out) p.done_out[o] = over;
   }
 }
@@ -440,9 +593,7 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
 template <typename T>
 cudaError_t launch(const SelectParams &p, cudaStream_t s) {
   const dim3 grid(p.segs, p.S);
-  cudaError_t e = p.per == 32   ? launch_dependent(scan_kernel<T, 32>, grid, kThr, 0, s, p)
-                  : p.per == 16 ? launch_dependent(scan_kernel<T, 16>, grid, kThr, 0, s, p)
-                                : launch_dependent(scan_kernel<T, 8>, grid, kThr, 0, s, p);
+  cudaError_t e = p.steps == 1 ? launch_dependent(scan_kernel<T, 1>, grid, kThr, 0, s, p) : launch_dependent(scan_kernel<T, 4>, grid, kThr, 0, s, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(pick_kernel<T>, p.S / p.n, kThr, 0, s, p);
 }

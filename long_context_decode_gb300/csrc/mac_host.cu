@@ -293,19 +293,27 @@ int check_select(const mac_config *c, int32_t n_beams, int32_t vocab, int32_t n_
   return vocab > kMaxVocab || n_out > kMaxPicks ? MAC_ERR_UNSUPPORTED : MAC_OK;
 }
 
-// CTAs of a row with `per` logits per thread, rows starting up to `shift`
-// elements behind a 16-byte boundary.
-int select_segs(int vocab, int per, int shift) {
-  return (vocab + shift + kScanThreads * per - 1) / (kScanThreads * per);
+// Steps of 16 bytes per thread that a row of the selection takes, and its
+// pieces where a card of `sms` SMs is to have four CTAs on each.
+int select_steps(int vocab, int es) {
+  const int per = kScanThreads * (16 / es);
+  return (vocab + per - 1) / per;
+}
+int select_pieces(int rows, int vocab, int es, int sms) {
+  const int steps = select_steps(vocab, es);
+  int pieces = (4 * sms + rows - 1) / rows;
+  if (pieces > kMaxPieces) pieces = kMaxPieces;
+  return pieces < steps ? pieces : steps;
 }
 
 // Selection workspace: the status word, then every piece's maximum and sum,
-// and its best logits.  Laid out for the smallest pieces.
+// and its best logits.  Laid out for the most pieces.
 struct SelectLayout {
   size_t ctl, ml, keys, total;
 };
 SelectLayout select_layout(const mac_config *c, int32_t vocab, int32_t n_out) {
-  const size_t pieces = (size_t)c->batch * select_segs(vocab, kScanLeast, 7);
+  const int steps = select_steps(vocab, 4);
+  const size_t pieces = (size_t)c->batch * (steps < kMaxPieces ? steps : kMaxPieces);
   SelectLayout L;
   size_t off = 0;
   L.ctl = off;   off = align_up(off + 64 * 4, 256);
@@ -857,10 +865,11 @@ int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const
   p.parent = parent;
   p.token = token;
   p.done_out = done_out;
-  const int shift = aligned16(logits) && row_stride * es % 16 == 0 ? 0 : 16 / es - 1;
-  p.per = 32;
-  while (p.per > kScanLeast && (int64_t)p.S * select_segs(vocab, p.per, shift) < 2 * sms) p.per /= 2;
-  p.segs = select_segs(vocab, p.per, shift);
+  const int steps = select_steps(vocab, es);
+  p.steps = (steps + select_pieces(p.S, vocab, es, sms) - 1) / select_pieces(p.S, vocab, es, sms);
+  p.segs = (steps + p.steps - 1) / p.steps;
+  p.lists_inv = ((1ull << 40) - 1) / ((unsigned long long)p.segs * n_beams) + 1;
+  p.segs_inv = ((1ull << 40) - 1) / p.segs + 1;
   const SelectLayout L = select_layout(cfg, vocab, n_out);
   uint8_t *ws = (uint8_t *)beam_ws;
   p.status = (uint32_t *)(ws + L.ctl);
