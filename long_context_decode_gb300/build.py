@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmac_gb300.so")
 SOURCES = ["mac_host.cu", "mac_append.cu", "mac_step_bf16.cu", "mac_step_f32.cu", "mac_step_bf16_sink.cu",
            "mac_step_f32_sink.cu", "mac_step_bf16_trace.cu", "mac_ring_bf16_g8.cu", "mac_ring_f32_g8.cu", "mac_batch.cu",
-           "mac_chunk_f32.cu", "mac_chunk_bf16.cu", "mac_chunk_merge.cu", "mac_beam_select.cu", "mac_reorder.cu"]
+           "mac_chunk_f32.cu", "mac_chunk_bf16.cu", "mac_chunk_merge.cu", "mac_beam_select.cu", "mac_reorder.cu", "mac_cross_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -9,6 +9,7 @@
 namespace mac {
 
 constexpr int kPage = 16;         // tokens per page of a paged cache
+constexpr int kMaxTokens = 1 << 24;
 
 struct TablesParams {
   int B, T;
@@ -75,12 +76,14 @@ struct ChunkBf16 {
   static constexpr int kStart = 12, kTile = 4, kTileHalf = 3, kMinShare = 16, kCut = 35;
   static constexpr bool kHalves = true;  // units of half the rows, where there are CTAs for all of them
   static constexpr bool kCross = false;
+  static constexpr long long kMost = kMaxTokens;  // rows of a batch
 };
 struct ChunkF32 {
   static constexpr int kRows = 128, kKeys = 64;
   static constexpr int kStart = 3, kTile = 1, kTileHalf = 1, kMinShare = 4, kCut = 4;
   static constexpr bool kHalves = false;
   static constexpr bool kCross = false;
+  static constexpr long long kMost = kMaxTokens;
 };
 // Cross attention: every row of a request attends all of its memory.
 struct CrossBf16 : ChunkBf16 {
@@ -89,8 +92,21 @@ struct CrossBf16 : ChunkBf16 {
 struct CrossF32 : ChunkF32 {
   static constexpr bool kCross = true;
 };
+// The same for few rows per source (mac_cross_few.cu), in quarters of a tile's
+// 64 KB of keys and values, 1.4 us at an SM's share of HBM.
+constexpr int kFewRows = 32;          // most rows of a source, on average
+template <int ROWS, int KEYS>
+struct CrossFew {
+  static constexpr int kRows = ROWS, kKeys = KEYS;
+  static constexpr int kStart = 5, kTile = 4, kTileHalf = 4, kMinShare = 9, kCut = 12;
+  static constexpr bool kHalves = false, kCross = true;
+  static constexpr long long kMost = (long long)kFewRows * kMaxUnits;
+};
+template <int ROWS>
+struct FewBf16 : CrossFew<ROWS, 128> {};
+template <int ROWS>
+struct FewF32 : CrossFew<ROWS, 64> {};
 constexpr int kChunkStride = kHeadDim + 8;  // floats per row of a partial: o[d], m, l, and to a multiple of 32 bytes
-constexpr int kMaxTokens = 1 << 24;
 
 // Launch with programmatic stream serialization: the kernel may start while
 // the previous one on the stream finishes, and waits (griddep_wait) before it
@@ -135,6 +151,8 @@ cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s);
 // The same with every row attending all of its request's keys.
 cudaError_t launch_cross_f32(const ChunkParams &p, int grid, cudaStream_t s);
 cudaError_t launch_cross_bf16(const ChunkParams &p, int grid, cudaStream_t s);
+// For few rows per source, in units of `rows` 16 or 32 (mac_cross_few.cu).
+cudaError_t launch_cross_few(const ChunkParams &p, int rows, bool f32, int grid, cudaStream_t s);
 // The cut units of an attention launch of `grid` CTAs.
 cudaError_t launch_chunk_merge(const ChunkParams &p, int grid, bool f32, cudaStream_t s);
 

@@ -59,7 +59,7 @@ struct ChunkPlan {
 
   // of all requests before b, all KV heads: cost; units, those of half the rows
   // in the upper 32 bits
-  static_assert(8LL * kMaxTokens / (C::kHalves ? ROWS / 2 : ROWS) * kMaxUnits < 1LL << 31, "units, each request with every row of the batch");
+  static_assert(8 * C::kMost / (C::kHalves ? ROWS / 2 : ROWS) * kMaxUnits < 1LL << 31, "units, each request with every row of the batch");
   long long prefix[2][kMaxUnits + 1];
   long long warp_tot[2][32];
   long long share;

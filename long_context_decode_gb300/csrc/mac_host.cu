@@ -477,8 +477,11 @@ int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int3
   note_launch(s, nullptr, nullptr);
   const bool f32 = cfg->dtype == MAC_F32;
   const int grid = sms < kChunkGrid ? sms : kChunkGrid;
-  if ((cross ? (f32 ? launch_cross_f32(p, grid, s) : launch_cross_bf16(p, grid, s))
-             : (f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s))) != cudaSuccess)
+  const int64_t rows = (int64_t)n_tokens * p.G;
+  const int few = cross && rows <= (int64_t)kFewRows * p.B ? (rows <= 16LL * p.B ? 16 : 32) : 0;
+  if ((few     ? launch_cross_few(p, few, f32, grid, s)
+       : cross ? (f32 ? launch_cross_f32(p, grid, s) : launch_cross_bf16(p, grid, s))
+               : (f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s))) != cudaSuccess)
     return MAC_ERR_CUDA;
   // No unit is cut when a CTA is there for each and none is long, whatever
   // the lengths on the device: then nothing needs merging.
@@ -487,6 +490,11 @@ int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int3
     const int64_t tiles = (C::kMinShare + C::kCut - C::kStart) / tile_cost;  // an equal share is at least kMinShare
     return (n_tokens / (rows / p.G) + (int64_t)p.B) * p.Hkv <= grid && p.max_len <= tiles * C::kKeys;
   };
+  if (few)
+    return (few == 16 ? f32 ? each(FewF32<16>{}, 16, FewF32<16>::kTile) : each(FewBf16<16>{}, 16, FewBf16<16>::kTile)
+                      : f32 ? each(FewF32<32>{}, 32, FewF32<32>::kTile) : each(FewBf16<32>{}, 32, FewBf16<32>::kTile)) ||
+                   launch_chunk_merge(p, grid, f32, s) == cudaSuccess
+               ? MAC_OK : MAC_ERR_CUDA;
   if (f32 ? each(ChunkF32{}, ChunkF32::kRows, ChunkF32::kTile)
           : each(ChunkBf16{}, ChunkBf16::kRows, ChunkBf16::kTile) || each(ChunkBf16{}, ChunkBf16::kRows / 2, ChunkBf16::kTileHalf))
     return MAC_OK;
