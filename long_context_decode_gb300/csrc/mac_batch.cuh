@@ -53,6 +53,7 @@ struct ChunkParams {
   void *out;
   float *lse;                     // or null
   uint32_t *status;
+  uint32_t *counts;               // [kChunkGrid] or null: pieces done of the cut unit whose first tile a CTA holds (few rows)
   int4 *notes;                    // [kChunkGrid] the cut unit whose first tile a CTA holds
   float *part;                    // [2 * grid][part_rows][kChunkStride]
   int part_rows;
@@ -95,6 +96,8 @@ struct CrossF32 : ChunkF32 {
 // The same for few rows per source (mac_cross_few.cu), in quarters of a tile's
 // 64 KB of keys and values, 1.4 us at an SM's share of HBM.
 constexpr int kFewRows = 32;          // most rows of a source, on average
+// Pieces of a unit, on average, that the last of them joins by itself (more: the merge kernel).
+constexpr int kFewPieces = 24;
 template <int ROWS, int KEYS>
 struct CrossFew {
   static constexpr int kRows = ROWS, kKeys = KEYS;

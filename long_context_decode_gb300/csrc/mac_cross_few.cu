@@ -5,20 +5,29 @@
 //   x_j = q . k_j log2(e)/sqrt(d);  m a running reference of the row's maximum;
 //   l = sum 2^(x_j - m);  o = sum 2^(x_j - m) v_j;  out = o / l;  lse = m ln 2 + ln l.
 // A unit is up to 16 MT packed rows (token-major, the G heads of a token
-// together) of one KV head, cut over the CTAs as chunk attention's units are.
-// Bound by HBM: every key and value is read once for a unit, and 16 rows are few
-// enough for the warps' own matrix instructions (m16n8, 32 to 128 of them per
-// 8 KB), which start on 4 KB of keys where a tcgen05 tile wants 128 rows and 32 KB.
+// together) of one KV head.  Bound by HBM: every key and value is read once for a
+// unit, and 16 rows are few enough for the warps' own matrix instructions (m16n8,
+// 32 to 96 of them per 8 KB), which start on 4 KB of keys where a tcgen05 tile
+// wants 128 rows and 32 KB.
 //
 // One CTA per SM, eight warps.  Within a key tile a warp has keys of its own,
 // copies them into stages of its own and keeps maximum, sum and output of its
 // own: no warp waits for another until a piece ends, and the copies of the next
-// piece are under way by then.  There the eight states are joined through shared
-// memory, 16 or 32 columns at a time.
+// piece are under way by then.  There the eight states are joined through the
+// stages that have been read last.
 //
-// fp32: a = a0 + a1 of 11 bits each (rounded, so a1 is exact to 2^-22 of a), and
-//   a b = a0 b0 + a0 b1 + a1 b0 + a1 b1: four products in tf32, exact in the sums,
-// each off by at most 2^-21 of its size.
+// Units are cut over the CTAs as chunk attention's are: they lie end to end on a
+// cost axis and a CTA takes an equal span of it, or a whole unit where there are
+// CTAs for all and none is long.  Every warp works out its CTA's pieces for
+// itself, as its copies reach them: a small call waits for code that has not been
+// fetched yet (some 5 ns an instruction), so the plan is short rather than
+// shared.  Of a cut unit's pieces the one that is done last joins them all, if
+// they are few; else the merge kernel of chunk attention does.
+//
+// fp32: a = a0 + a1 of 11 bits each (rounded, so a1 is good to 2^-22 of a), and
+//   a b = a0 b0 + a0 b1 + a1 b0 + (a1 b1, up to 2^-22 of a b, left out):
+// three products in tf32, each exact in the sums, so a product is off by at most
+// 2^-20 of its size (2^-24 on average).
 #include <math.h>
 
 #include "mac_tc.cuh"
@@ -27,7 +36,8 @@ namespace mac {
 namespace {
 
 constexpr int kWarps = 8, kThr = kWarps * 32;
-constexpr int kStep = 8192;                   // bytes of a warp's keys and values in a tile
+constexpr int kStep = 8192;                   // bytes of a warp's keys and values in a tile; of 16 rows of output
+static_assert(kStep == 16 * kHeadDim * 4, "a stage that has been read takes the outputs of a row tile");
 
 template <typename T>
 constexpr int kKeysOf = sizeof(T) == 4 ? 8 : 16;  // keys of a warp in a tile
@@ -47,15 +57,13 @@ struct Shared {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int kRows = 16 * MT;
   static constexpr int kStages = kF32 && MT == 2 ? 2 : 3;
-  // columns joined at a time, and floats between their rows: no two of a store's lanes in a bank
-  static constexpr int kCols = !kF32 && MT == 2 ? 16 : 32, kStride = kCols + (kF32 ? 4 : 8);
+  // One bf16 row tile's queries stay in registers; two, and fp32's (both parts), lie here.
+  static constexpr bool kQShared = kF32 || MT == 2;
   uint8_t stage[kWarps][kStages][kStep];
-  union {
-    float join[kWarps][kRows][kStride];
-    float q[kF32 ? 2 : 1][kF32 ? kRows : 1][kF32 ? kQStride : 1];  // fp32: the two parts of the queries
-  };
+  uint8_t q[kF32 ? 2 : 1][kQShared ? kRows * (kF32 ? kQStride * 4 : kHeadDim * 2) : 16];
   float2 ml[kWarps][kRows];
-  Piece pieces[8];
+  Piece pieces[kWarps][4];
+  uint32_t arrived[2];   // pieces of a cut unit that were done before this CTA's
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
@@ -88,13 +96,6 @@ __device__ __forceinline__ void mma_tf32(float *c, const float *a, float b0, flo
                : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
                  "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
-// c += a b of two parts each, smallest products first
-__device__ __forceinline__ void mma_parts(float *c, const float *a0, const float *a1, float b00, float b01, float b10, float b11) {
-  mma_tf32(c, a1, b10, b11);
-  mma_tf32(c, a0, b10, b11);
-  mma_tf32(c, a1, b00, b01);
-  mma_tf32(c, a0, b00, b01);
-}
 __device__ __forceinline__ float tf32(float x) {
   uint32_t u;
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(u) : "f"(x));
@@ -113,87 +114,277 @@ __device__ __forceinline__ int place(int row, int chunk, bool values) {
   return row * 512 + ((chunk ^ (values ? (row >> 1 & 3) << 1 : (row & 1) << 2)) << 4);
 }
 
-// A warp's way through its steps: the piece (its number in the CTA) and tile.
-struct Steps {
-  int piece, tile;
+// a / b for a >= 0, b > 0
+__device__ __forceinline__ long long div_down(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? div_s64(a, b) : (uint32_t)a / (uint32_t)b;
+}
+
+// A source, as the plan sees it.
+struct Source {
+  int row0, n, keys;   // first row, rows (0: nothing to attend), states
+  int units, tiles;    // of all its KV heads; key tiles
+  bool odd;            // rows that are not attended: bad lengths, or no states
 };
+
+// The pieces of a CTA, worked out by every warp for itself (all lanes call it).
+template <typename C>
+struct Walk {
+  static constexpr int START = C::kStart, TILE = C::kTile;
+  int lt;              // log2 of the tokens of a unit
+  int b, k;            // source, unit (KV head by head, in each its rows' blocks)
+  Source src;
+  bool whole, odd;     // a unit per CTA; some source is odd
+  long long x, end, share, at;  // this CTA's span; the unit's place
+
+  __device__ __forceinline__ Source source(const ChunkParams &p, int i) const {
+    Source s;
+    const int r0 = p.q_start[i * p.group], r1 = p.q_start[(i + 1) * p.group], m = p.seq_len[i];
+    const bool in = r0 >= 0 && r1 >= r0 && r1 <= p.T;
+    s.row0 = r0;
+    s.keys = m;
+    s.odd = !in || (r1 > r0 && (m < 1 || m > p.max_len));
+    s.n = s.odd ? 0 : r1 - r0;
+    s.units = ((s.n + (1 << lt) - 1) >> lt) * p.Hkv;
+    s.tiles = (int)(((long long)m + C::kKeys - 1) / C::kKeys);
+    return s;
+  }
+  __device__ __forceinline__ long long cost(const Source &s) const { return START + (long long)TILE * s.tiles; }
+
+  // false: nothing to do
+  __device__ bool start(const ChunkParams &p) {
+    const int lane = threadIdx.x & 31;
+    lt = log2i(C::kRows) - (31 - __clz(p.G));
+    long long total = 0, units = 0, top = 0;
+    odd = false;
+    Source mine;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      mine = {};
+      if (b0 + lane < p.B) mine = source(p, b0 + lane);
+      odd |= mine.odd;
+      if (mine.units) {
+        total += mine.units * cost(mine);
+        units += mine.units;
+        top = max(top, cost(mine));
+      }
+    }
+    odd = __any_sync(0xffffffffu, odd);
+#pragma unroll 1
+    for (int d = 16; d; d >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, d);
+      units += __shfl_xor_sync(0xffffffffu, units, d);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    const long long ctas = max(1, (int)min(total / C::kMinShare, (long long)gridDim.x));
+    whole = units <= gridDim.x && (top - C::kCut - 1) * ctas < total;
+    share = whole ? 1 : div_down(total + ctas - 1, ctas);
+    x = blockIdx.x * share;
+    end = min(whole ? units : total, x + share);
+    if (x >= end) return false;
+    long long before = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
+      if (p.B > 32) {
+        mine = {};
+        if (b0 + lane < p.B) mine = source(p, b0 + lane);
+      }
+      const long long v = whole ? mine.units : mine.units ? mine.units * cost(mine) : 0;
+      long long sum = v;
+#pragma unroll 1
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, x < before + sum);
+      if (!past) {
+        before += __shfl_sync(0xffffffffu, sum, 31);
+        continue;
+      }
+      const int hit = __ffs(past) - 1;
+      b = b0 + hit;
+      src.row0 = __shfl_sync(0xffffffffu, mine.row0, hit);
+      src.n = __shfl_sync(0xffffffffu, mine.n, hit);
+      src.keys = __shfl_sync(0xffffffffu, mine.keys, hit);
+      src.units = __shfl_sync(0xffffffffu, mine.units, hit);
+      src.tiles = __shfl_sync(0xffffffffu, mine.tiles, hit);
+      before += __shfl_sync(0xffffffffu, sum - v, hit);
+      found = true;
+    }
+    if (!found) return false;  // (not while the arrays stay as they are)
+    k = (int)(whole ? x - before : div_down(x - before, cost(src)));
+    at = before + (whole ? k : k * cost(src));
+    return true;
+  }
+
+  // The next piece with a tile; one without: the CTA's work is done.
+  __device__ Piece next(const ChunkParams &p) {
+    while (x < end) {
+      int t0 = 0, t1 = src.tiles;
+      const long long first = at + START, last = first + (long long)TILE * (src.tiles - 1);  // of its first and last tile
+      if (whole) {
+        x = ++at;
+      } else {
+        if (x > first) t0 = (int)((x - first + TILE - 1) / TILE);
+        if (end <= last) t1 = end > first ? (int)((end - first + TILE - 1) / TILE) : 0;
+        at = x = last + TILE;
+      }
+      const int blocks = src.units / p.Hkv, g = k / blocks, i = k - g * blocks;
+      Piece q = {b, g, src.row0 + (i << lt), min(1 << lt, src.n - (i << lt)), src.keys, t0, t1, -1, -1};
+      if (t1 - t0 < src.tiles && t0 < t1) {
+        q.c0 = (int)div_down(first, share);
+        q.c1 = (int)div_down(last, share);
+      }
+      if (++k == src.units && x < end) {
+        k = 0;
+        do {
+          if (++b == p.B) {  // (nor this)
+            x = end;
+            break;
+          }
+          src = source(p, b);
+        } while (src.units == 0);
+      }
+      if (t0 < t1) return q;
+    }
+    return Piece{};
+  }
+};
+
+// One more piece of a cut unit is done: how many were before.  What the CTA
+// wrote ahead of the barrier that thread 0 has come through is seen by whoever
+// finds it counted.
+__device__ __forceinline__ uint32_t arrive(uint32_t *count) {
+  uint32_t before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+  return before;
+}
+
+// Row `at` of a unit: 4 columns from 4 col and 64 + 4 col on.
+template <typename T>
+__device__ __forceinline__ void write_row(const ChunkParams &p, const Piece &q, int at, int col, float4 x, float4 y, float m, float l) {
+  const int64_t to = (int64_t)(q.tok0 + at / p.G) * p.Hq + q.g * p.G + at % p.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T *dst = (T *)p.out + to * kHeadDim + col * 4;
+  store_out(dst, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+  store_out(dst + 64, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+  if (p.lse && col == 0) p.lse[to] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+}
 
 template <typename T, int MT, bool PAGED, typename C>
 __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ ChunkParams p) {
   using SM = Shared<T, MT>;
-  using Plan = ChunkPlan<C>;
-  constexpr bool F32 = SM::kF32;
-  constexpr int KW = kKeysOf<T>, ROWS = SM::kRows, COLS = SM::kCols, NST = SM::kStages, AHEAD = NST - 1;
+  constexpr bool F32 = SM::kF32, QS = SM::kQShared;
+  constexpr int KW = kKeysOf<T>, ROWS = SM::kRows, NST = SM::kStages, AHEAD = NST - 1;
   static_assert(C::kRows == ROWS && C::kKeys == kWarps * KW && KW * kHeadDim * (int)sizeof(T) * 2 == kStep, "tiles");
-  static_assert(sizeof(Plan) <= sizeof(SM::stage), "the plan is made where the stages go");
-  static_assert(AHEAD <= 2, "a piece's three successors are known");
+  static_assert(AHEAD <= 2, "the copies are at most three pieces ahead, and their place in the ring is free");
   extern __shared__ __align__(1024) uint8_t smem[];
   SM &sm = *reinterpret_cast<SM *>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   griddep_launch_dependents();
   griddep_wait();
-  Plan &plan = *reinterpret_cast<Plan *>(smem);
-  plan.build(p);
-  if (plan.any_bad()) chunk_bad_requests<T, Plan>(p);
-  if (!plan.has_work(p)) {
-    if (tid == 0) leave_note(p, make_int4(0, 0, 0, 0));
+  Walk<C> walk;
+  const bool work = walk.start(p);
+  if (walk.odd) chunk_bad_requests<T, ChunkPlan<C>>(p);
+  if (!work) {
+    if (tid == 0 && !p.counts) leave_note(p, make_int4(0, 0, 0, 0));
     return;
   }
-  // The last warp works out the pieces: when a piece begins, the three after it are
-  // known, as far as the copies of two more tiles and the place after them may reach.
-  ChunkWalk<C> walk;
-  auto walk_on = [&](int i) {
-    ChunkPiece x = {};
-    Piece q = {};
-    if (walk.next(p, x)) {
-      const ChunkUnit &u = x.u;
-      const bool cut = x.cut();
-      q = {u.b, u.g, u.tok0, u.n_tok, u.pos0, x.t0, x.t1, cut ? walk.cta_of(u, 0) : -1, cut ? walk.cta_of(u, u.tiles - 1) : -1};
-    }
-    if (lane == 0) sm.pieces[i & 7] = q;
+  int known = 0;  // pieces worked out
+  auto walk_on = [&] {
+    const Piece q = walk.next(p);
+    if (lane == 0) sm.pieces[warp][known & 3] = q;
+    ++known;
+    __syncwarp();
   };
-  if (warp == kWarps - 1) {
-    walk.start(p, plan);
-    for (int i = 0; i < 4; ++i) walk_on(i);
-  }
-  __syncthreads();  // the plan has been read: its place is the stages'
+
+  // ---- queries: one bf16 row tile as the products' operands, the others by way of
+  // registers into shared memory, which a piece's end must leave first
+  constexpr int UNITS = kHeadDim * (int)sizeof(T) / 16, NQ = QS ? ROWS * UNITS / kThr : 1;  // 16-byte parts of a row; of a thread
+  uint32_t qa[QS ? 1 : 8][4];
+  uint4 fresh[NQ];
+  auto load_q = [&](const Piece &q) {
+    const int n_rows = q.n_tok * p.G;
+    auto q_row = [&](int r) { return (const uint8_t *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim * sizeof(T); };
+    if constexpr (QS) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int e = i * kThr + tid, r = e / UNITS;
+        fresh[i] = r < n_rows ? *reinterpret_cast<const uint4 *>(q_row(r) + e % UNITS * 16) : make_uint4(0, 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(q_row(min(h * 8 + g, n_rows - 1))) + t;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          qa[c][h] = src[c * 8];
+          qa[c][h + 2] = src[c * 8 + 4];
+        }
+      }
+    }
+  };
+  auto put_q = [&] {
+    if constexpr (QS) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int e = i * kThr + tid, r = e / UNITS, c = e % UNITS;
+        if constexpr (F32) {
+          const float *f = reinterpret_cast<const float *>(&fresh[i]);
+          float4 hi, lo;
+          split(f[0], hi.x, lo.x);
+          split(f[1], hi.y, lo.y);
+          split(f[2], hi.z, lo.z);
+          split(f[3], hi.w, lo.w);
+          *reinterpret_cast<float4 *>(sm.q[0] + r * kQStride * 4 + c * 16) = hi;
+          *reinterpret_cast<float4 *>(sm.q[F32] + r * kQStride * 4 + c * 16) = lo;
+        } else {
+          *reinterpret_cast<uint4 *>(sm.q[0] + place<T>(r, c, false)) = fresh[i];
+        }
+      }
+      __syncthreads();
+    }
+  };
 
   // ---- copies
   const uint32_t stages = smem_addr(sm.stage[warp]);
-  const bool paged = PAGED;
   uint32_t status = 0;
   int stage_in = 0;
-  Steps in = {0, sm.pieces[0].t0};
+  Piece in;           // the piece that is copied, and its next tile
+  int in_tile = 0;
   uint32_t gone = 0;  // steps in flight whose page does not exist, the last issued in bit 0
   // page of the warp's keys in a tile (contiguous: 0), -1: none, -2: no keys
-  auto page_of = [&](const Steps &s) {
-    const Piece &q = sm.pieces[s.piece & 7];
-    const int key0 = s.tile * C::kKeys + warp * KW;
-    if (q.t1 <= q.t0 || key0 >= q.keys) return -2;
-    if (!paged) return 0;
-    const int id = p.kv.page_table[(int64_t)q.b * p.kv.max_pages + key0 / kPage];
+  auto page_of = [&] {
+    const int key0 = in_tile * C::kKeys + warp * KW;
+    if (in.t1 <= in.t0 || key0 >= in.keys) return -2;
+    if (!PAGED) return 0;
+    const int id = p.kv.page_table[(int64_t)in.b * p.kv.max_pages + key0 / kPage];
     return id >= 0 && id < p.kv.n_pages ? id : -1;
   };
-  int page = page_of(in);
+  auto enter = [&] {  // the next piece
+    walk_on();
+    in = sm.pieces[warp][known - 1 & 3];
+    in_tile = in.t0;
+  };
+  enter();
+  load_q(in);
+  int page = page_of();
   // A lane's part of a step: bf16 16 bytes of every second row, fp32 of every row.
   // A row's 16-byte parts are swizzled by bits of the row, which change from
   // copy to copy by an exclusive or of the lane's first place.
-  constexpr int N = kStep / 2 / 512, PER_ROW = kHeadDim * (int)sizeof(T) / 16;
-  const uint32_t to_k = stages + place<T>(lane / PER_ROW, lane % PER_ROW, false);
-  const uint32_t to_v = stages + kStep / 2 + place<T>(lane / PER_ROW, lane % PER_ROW, true);
+  constexpr int N = kStep / 2 / 512;
+  const uint32_t to_k = stages + place<T>(lane / UNITS, lane % UNITS, false);
+  const uint32_t to_v = stages + kStep / 2 + place<T>(lane / UNITS, lane % UNITS, true);
   auto swizzle = [](int i, bool values) {  // of copy i against copy 0
     return F32 ? (uint32_t)(values ? (i >> 1 & 3) << 5 : (i & 1) << 6) : (uint32_t)((2 * i & 6) << 4);
   };
   auto issue = [&] {
-    const Piece &q = sm.pieces[in.piece & 7];
-    const int key0 = in.tile * C::kKeys + warp * KW;
     gone = gone << 1 | (page == -1);
     if (page >= 0) {
-      const int64_t row0 = paged ? ((int64_t)page * p.Hkv + q.g) * kPage + key0 % kPage : ((int64_t)q.b * p.Hkv + q.g) * p.kv.capacity + key0;
+      const int key0 = in_tile * C::kKeys + warp * KW;
+      const int64_t row0 = PAGED ? ((int64_t)page * p.Hkv + in.g) * kPage + key0 % kPage : ((int64_t)in.b * p.Hkv + in.g) * p.kv.capacity + key0;
       const uint8_t *k = (const uint8_t *)p.kv.k + row0 * kHeadDim * sizeof(T) + lane * 16;
       const uint8_t *v = (const uint8_t *)p.kv.v + row0 * kHeadDim * sizeof(T) + lane * 16;
       const uint32_t dk = to_k + stage_in * kStep, dv = to_v + stage_in * kStep;
-      const int n = q.keys - key0;
+      const int n = in.keys - key0;
       if (n >= KW) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -203,7 +394,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
       } else {  // rows behind the last are not read
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {
-          const bool there = i * (32 / PER_ROW) + lane / PER_ROW < n;
+          const bool there = i * (32 / UNITS) + lane / UNITS < n;
           const int at = there ? i * 512 : -lane * 16;
           copy16_if((dk ^ swizzle(i, false)) + i * 512, k + at, there);
           copy16_if((dv ^ swizzle(i, true)) + i * 512, v + at, there);
@@ -211,56 +402,28 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
       }
     }
     copies_end();
-    if (q.t1 <= q.t0) return;
+    if (in.t1 <= in.t0) return;
     if (++stage_in == NST) stage_in = 0;
-    if (++in.tile == q.t1) in = {in.piece + 1, sm.pieces[(in.piece + 1) & 7].t0};
-    page = page_of(in);
+    if (++in_tile == in.t1) enter();
+    page = page_of();
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < AHEAD; ++i) issue();
+  put_q();
 
   const float scale = p.q_scale, lazy = 8.f / scale;
   // a lane's rows of the bf16 operands; two 16-byte parts further on are an exclusive or away
   const uint32_t of_k = place<uint16_t>((lane & 7) + (lane >> 4 << 3), lane >> 3 & 1, false);
   const uint32_t of_v = place<uint16_t>(lane & 15, lane >> 4, true);
-  int stage = 0;
+  const uint32_t of_q = smem_addr(sm.q) + (QS && !F32 ? place<uint16_t>(lane & 15, lane >> 4, false) : 0);
   int4 note = make_int4(0, 0, 0, 0);
+  int stage = 0;
+  Piece cut[2];        // the cut units of this CTA's first and last piece
+  int n_cut = 0;
+#pragma unroll 1
   for (int number = 0;; ++number) {
-    const Piece q = sm.pieces[number & 7];
+    const Piece q = sm.pieces[warp][number & 3];
     if (q.t1 <= q.t0) break;
-    const int n_rows = q.n_tok * p.G;
-    auto q_row = [&](int r) { return (const T *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim; };
-    // the queries: bf16 as the products' operands, fp32 split into shared memory
-    uint32_t qa[F32 ? 1 : MT][F32 ? 1 : 8][4];
-    if constexpr (F32) {
-      for (int e = tid; e < ROWS * (kHeadDim / 4); e += kThr) {
-        const int r = e / (kHeadDim / 4), c = e % (kHeadDim / 4) * 4;
-        const float4 x = r < n_rows ? *reinterpret_cast<const float4 *>(q_row(r) + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 hi, lo;
-        split(x.x, hi.x, lo.x);
-        split(x.y, hi.y, lo.y);
-        split(x.z, hi.z, lo.z);
-        split(x.w, hi.w, lo.w);
-        *reinterpret_cast<float4 *>(&sm.q[0][r][c]) = hi;
-        *reinterpret_cast<float4 *>(&sm.q[1][r][c]) = lo;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = i * 16 + h * 8 + g;
-          const uint32_t *src = reinterpret_cast<const uint32_t *>(q_row(min(r, n_rows - 1)));
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            qa[i][s][h] = src[s * 8 + t];
-            qa[i][s][h + 2] = src[s * 8 + 4 + t];
-          }
-        }
-    }
-    if (warp == kWarps - 1) walk_on(number + 4);  // known to all from the barriers at the piece's end
-    if (F32) __syncthreads();
-
     float o[MT][16][4], m[MT][2], l[MT][2];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -269,6 +432,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
       m[i][0] = m[i][1] = -INFINITY;
       l[i][0] = l[i][1] = 0.f;
     }
+#pragma unroll 1
     for (int tile = q.t0; tile < q.t1; ++tile) {
       __syncwarp();  // the stage that comes next has been read
       issue();
@@ -283,16 +447,18 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
         status |= MAC_DEV_BAD_PAGE;
         continue;
       }
-      // scores: KW keys, 8 per column tile
-      constexpr int NT = KW / 8;
+      // scores: KW keys, 8 per column tile.  A product waits 21 cycles for one into
+      // the same sums, so with one row tile there are four sums in turn
+      constexpr int NT = KW / 8, SUMS = F32 ? (MT == 1 ? 4 : 2) : (MT == 1 ? 2 : 1);
       float s[MT][NT][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
       if constexpr (F32) {
         // column order within 16: a lane's four neighbours are columns t and t + 4 of two products
-#pragma unroll 4
+        float x[MT][SUMS][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < SUMS * 4; ++e) x[i][e >> 2][e & 3] = 0.f;
+#pragma unroll 2
         for (int c = 0; c < kHeadDim / 16; ++c) {
           const float4 kx = *reinterpret_cast<const float4 *>(kp + place<T>(g, c * 4 + t, false));
           float h[4], r[4];
@@ -302,27 +468,52 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
           split(kx.w, h[3], r[3]);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            const int at = c * 16 + t * 4;
-            const float4 x0 = *reinterpret_cast<const float4 *>(&sm.q[0][i * 16 + g][at]), x1 = *reinterpret_cast<const float4 *>(&sm.q[0][i * 16 + g + 8][at]);
-            const float4 y0 = *reinterpret_cast<const float4 *>(&sm.q[1][i * 16 + g][at]), y1 = *reinterpret_cast<const float4 *>(&sm.q[1][i * 16 + g + 8][at]);
+            const uint8_t *at = sm.q[0] + (i * 16 + g) * kQStride * 4 + c * 64 + t * 16, *at1 = at + (sm.q[F32] - sm.q[0]);
+            const float4 x0 = *reinterpret_cast<const float4 *>(at), x1 = *reinterpret_cast<const float4 *>(at + 8 * kQStride * 4);
+            const float4 y0 = *reinterpret_cast<const float4 *>(at1), y1 = *reinterpret_cast<const float4 *>(at1 + 8 * kQStride * 4);
             const float a0[4] = {x0.x, x1.x, x0.y, x1.y}, a1[4] = {y0.x, y1.x, y0.y, y1.y};
-            mma_parts(s[i][0], a0, a1, h[0], h[1], r[0], r[1]);
             const float b0[4] = {x0.z, x1.z, x0.w, x1.w}, b1[4] = {y0.z, y1.z, y0.w, y1.w};
-            mma_parts(s[i][0], b0, b1, h[2], h[3], r[2], r[3]);
+            mma_tf32(x[i][0], a1, h[0], h[1]);
+            mma_tf32(x[i][1], b1, h[2], h[3]);
+            mma_tf32(x[i][SUMS - 2], a0, h[0], h[1]);
+            mma_tf32(x[i][SUMS - 1], b0, h[2], h[3]);
+            mma_tf32(x[i][0], a0, r[0], r[1]);
+            mma_tf32(x[i][1], b0, r[2], r[3]);
           }
         }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][0][e] = (SUMS == 4 ? x[i][SUMS - 2][e] + x[i][SUMS - 1][e] : 0.f) + (x[i][0][e] + x[i][1][e]);
       } else {
+        float x[MT][SUMS][2][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < SUMS * 8; ++e) x[i][e >> 3][e >> 2 & 1][e & 3] = 0.f;
         const uint32_t at = kb + of_k;
+        uint32_t b[2][4];
+        ldm4(b[0], at);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t b[4];
-          ldm4(b, (at ^ (c & 3) << 5) + (c >> 2) * 128);
+          uint32_t a[QS ? MT : 1][4];
+          if constexpr (QS) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) ldm4(a[i], (of_q ^ (c & 3) << 5) + (c >> 2) * 128 + i * 16 * 256);
+          }
+          if (c < 7) ldm4(b[c + 1 & 1], (at ^ (c + 1 & 3) << 5) + (c + 1 >> 2) * 128);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            mma_bf16(s[i][0], qa[i][c], b[0], b[1]);
-            mma_bf16(s[i][NT - 1], qa[i][c], b[2], b[3]);
+            mma_bf16(x[i][c % SUMS][0], QS ? a[QS ? i : 0] : qa[QS ? 0 : c], b[c & 1][0], b[c & 1][1]);
+            mma_bf16(x[i][c % SUMS][1], QS ? a[QS ? i : 0] : qa[QS ? 0 : c], b[c & 1][2], b[c & 1][3]);
           }
         }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][j][e] = SUMS == 2 ? x[i][0][j][e] + x[i][SUMS - 1][j][e] : x[i][0][j][e];
       }
       if (left < KW) {
 #pragma unroll
@@ -334,7 +525,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
               if (j * 8 + t * 2 + (e & 1) >= left) s[i][j][e] = -INFINITY;
       }
       // weights
-      uint32_t pa[MT][4];      // bf16: the weights as an operand
+      uint32_t pa[MT][4];          // bf16: the weights as an operand
       float ph[MT][4], pl[MT][4];  // fp32: their parts
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -342,9 +533,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            top[e >> 1] = fmaxf(top[e >> 1], s[i][j][e]);
-          }
+          for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[i][j][e]);
         bool grows = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -396,32 +585,44 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
           const float4 v0 = *reinterpret_cast<const float4 *>(vp + place<T>(2 * t, c * 8 + g, true));
           const float4 v1 = *reinterpret_cast<const float4 *>(vp + place<T>(2 * t + 1, c * 8 + g, true));
           const float a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
+          float ah[4], al[4], bh[4], bl[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float ah, al, bh, bl;
-            split(a[e], ah, al);
-            split(b[e], bh, bl);
+            split(a[e], ah[e], al[e]);
+            split(b[e], bh[e], bl[e]);
+          }
 #pragma unroll
-            for (int i = 0; i < MT; ++i) mma_parts(o[i][c * 4 + e], ph[i], pl[i], ah, bh, al, bl);
+          for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma_tf32(o[i][c * 4 + e], pl[i], ah[e], bh[e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma_tf32(o[i][c * 4 + e], ph[i], al[e], bl[e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma_tf32(o[i][c * 4 + e], ph[i], ah[e], bh[e]);
           }
         }
       } else {
         const uint32_t at = vb + of_v;
+        uint32_t b[2][4];
+        ldm4t(b[0], at);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t b[4];
-          ldm4t(b, (at ^ (c & 3) << 5) + (c >> 2) * 128);
+          if (c < 7) ldm4t(b[c + 1 & 1], (at ^ (c + 1 & 3) << 5) + (c + 1 >> 2) * 128);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            mma_bf16(o[i][2 * c], pa[i], b[0], b[1]);
-            mma_bf16(o[i][2 * c + 1], pa[i], b[2], b[3]);
+            mma_bf16(o[i][2 * c], pa[i], b[c & 1][0], b[c & 1][1]);
+            mma_bf16(o[i][2 * c + 1], pa[i], b[c & 1][2], b[c & 1][3]);
           }
         }
       }
     }
 
-    // ---- the warps' states joined
-    if (F32) __syncthreads();  // the queries have been read: their place is the joint's
+    // ---- the piece's end: the warps' states joined
+    const Piece after = sm.pieces[warp][number + 1 & 3];
+    if (after.t1 > after.t0) load_q(after);  // on its way meanwhile
+    const int last = stage == 0 ? NST - 1 : stage - 1;  // the stage that has been read
+    const int n_rows = q.n_tok * p.G, c = blockIdx.x;
+    const bool whole = q.c0 < 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -430,74 +631,106 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
         l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 2);
         if (t == 0) sm.ml[warp][i * 16 + h * 8 + g] = make_float2(m[i][h] * scale, l[i][h]);  // base 2
       }
-    const int c = blockIdx.x;
-    const bool whole = q.c0 < 0;
-    constexpr int PER_ROW = COLS / 4;            // threads per row of the joint
-    const int row = tid / PER_ROW, col = tid % PER_ROW * 4;
-    const bool mine = row < ROWS && row < n_rows;
-    float f[kWarps], big = -INFINITY, sum = 0.f;
-    float *part = p.part + ((int64_t)(2 * c + (c == q.c0 ? 1 : 0)) * p.part_rows + row) * kChunkStride;
-    const int64_t out_row = (int64_t)(q.tok0 + row / p.G) * p.Hq + q.g * p.G + row % p.G;
-    float norm = 1.f;
+    // A row tile's outputs take the warps' stages that have been read last: rows of
+    // 512 bytes, 16 bytes swizzled by the row, so that neither a store's lanes nor a
+    // load's meet a bank twice.
+    const int row = tid >> 4, col = tid & 15;  // a thread joins columns 4 col .. and 64 + 4 col .. of a row
+    auto joint = [&](int w, int r, int unit) { return reinterpret_cast<float *>(sm.stage[w][last] + r * 512 + ((unit ^ (r & 7)) << 4)); };
 #pragma unroll
-    for (int j = 0; j < kHeadDim / COLS; ++j) {
+    for (int i = 0; i < MT; ++i) {
+      if (i > 0) __syncthreads();  // the last row tile's have been read
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        const int r = h * 8 + g;
         if constexpr (F32) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float *dst = &sm.join[warp][i * 16 + h * 8 + g][t * 8];
-            *reinterpret_cast<float4 *>(dst) = make_float4(o[i][j * 4][2 * h], o[i][j * 4 + 1][2 * h], o[i][j * 4 + 2][2 * h], o[i][j * 4 + 3][2 * h]);
-            *reinterpret_cast<float4 *>(dst + 4) =
+          for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<float4 *>(joint(warp, r, j * 8 + t * 2)) =
+                make_float4(o[i][j * 4][2 * h], o[i][j * 4 + 1][2 * h], o[i][j * 4 + 2][2 * h], o[i][j * 4 + 3][2 * h]);
+            *reinterpret_cast<float4 *>(joint(warp, r, j * 8 + t * 2 + 1)) =
                 make_float4(o[i][j * 4][2 * h + 1], o[i][j * 4 + 1][2 * h + 1], o[i][j * 4 + 2][2 * h + 1], o[i][j * 4 + 3][2 * h + 1]);
           }
         } else {
 #pragma unroll
-          for (int n = 0; n < COLS / 8; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<float2 *>(&sm.join[warp][i * 16 + h * 8 + g][n * 8 + t * 2]) =
-                  make_float2(o[i][j * (COLS / 8) + n][2 * h], o[i][j * (COLS / 8) + n][2 * h + 1]);
+          for (int j = 0; j < 16; ++j)
+            *reinterpret_cast<float2 *>(joint(warp, r, j * 2 + (t >> 1)) + (t & 1) * 2) = make_float2(o[i][j][2 * h], o[i][j][2 * h + 1]);
         }
       }
       __syncthreads();
-      if (mine) {
-        if (j == 0) {
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.ml[w][row].x);
-          const float ref = big == -INFINITY ? 0.f : big;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 x = sm.ml[w][row];
-            f[w] = ex2(x.x - ref);
-            sum = fmaf(f[w], x.y, sum);
-          }
-          if (whole) norm = sum == 0.f ? 0.f : 1.f / sum;
-        }
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int at = i * 16 + row;
+      if (at < n_rows) {
+        float2 ml[kWarps];
+        float big = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float4 y = *reinterpret_cast<const float4 *>(&sm.join[w][row][col]);
-          x.x = fmaf(f[w], y.x, x.x);
-          x.y = fmaf(f[w], y.y, x.y);
-          x.z = fmaf(f[w], y.z, x.z);
-          x.w = fmaf(f[w], y.w, x.w);
+          ml[w] = sm.ml[w][at];
+          big = fmaxf(big, ml[w].x);
         }
-        x = make_float4(x.x * norm, x.y * norm, x.z * norm, x.w * norm);
-        if (whole) store_out((T *)p.out + out_row * kHeadDim + j * COLS + col, x);
-        else *reinterpret_cast<float4 *>(part + j * COLS + col) = x;
+        const float ref = big == -INFINITY ? 0.f : big;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(ml[w].x - ref);
+          sum = fmaf(f, ml[w].y, sum);
+          const float4 u = *reinterpret_cast<const float4 *>(joint(w, row, col)), v = *reinterpret_cast<const float4 *>(joint(w, row, col + 16));
+          x = make_float4(fmaf(f, u.x, x.x), fmaf(f, u.y, x.y), fmaf(f, u.z, x.z), fmaf(f, u.w, x.w));
+          y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+        }
+        if (whole) {
+          write_row<T>(p, q, at, col, x, y, big, sum);
+        } else {
+          float *dst = p.part + ((int64_t)(2 * c + (c == q.c0 ? 1 : 0)) * p.part_rows + at) * kChunkStride;
+          *reinterpret_cast<float4 *>(dst + col * 4) = x;
+          *reinterpret_cast<float4 *>(dst + 64 + col * 4) = y;
+          if (col == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = make_float2(big, sum);
+        }
       }
-      __syncthreads();
     }
-    if (mine && col == 0) {
-      if (!whole) *reinterpret_cast<float2 *>(part + kHeadDim) = make_float2(big, sum);
-      else if (p.lse) p.lse[out_row] = sum == 0.f ? -INFINITY : big * kLn2 + logf(sum);
-    }
+    __syncthreads();  // the stages are free again, the partials written
+    put_q();
+    if (whole) continue;
     if (c == q.c0) note = make_int4(q.tok0, q.g, n_rows, q.c1);
+    if (p.counts) {
+      cut[n_cut] = q;
+      if (tid == 0) sm.arrived[n_cut] = arrive(p.counts + q.c0);
+      ++n_cut;
+    }
   }
   copies_wait<0>();
-  if (tid == 0) leave_note(p, note);
   if (status && lane == 0) set_status(p.status, status);
+  if (!p.counts) {
+    if (tid == 0) leave_note(p, note);
+    return;
+  }
+  // ---- cut units whose last piece was this CTA's
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < n_cut; ++i) {
+    const Piece q = i ? cut[1] : cut[0];
+    const int n = q.c1 - q.c0 + 1, n_rows = q.n_tok * p.G;
+    if (sm.arrived[i] + 1 != (uint32_t)n) continue;
+    if (tid == 0) p.counts[q.c0] = 0;  // for the next call
+    const int col = tid & 15;
+    for (int at = tid >> 4; at < n_rows; at += 16) {
+      auto part = [&](int j) { return p.part + ((int64_t)(2 * (q.c0 + j) + (j == 0)) * p.part_rows + at) * kChunkStride; };
+      float big = -INFINITY, sum = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) big = fmaxf(big, __ldcg(reinterpret_cast<const float2 *>(part(j) + kHeadDim)).x);
+      const float ref = big == -INFINITY ? 0.f : big;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(j) + kHeadDim));
+        const float4 u = __ldcg(reinterpret_cast<const float4 *>(part(j) + col * 4)), v = __ldcg(reinterpret_cast<const float4 *>(part(j) + 64 + col * 4));
+        const float f = ex2(ml.x - ref);
+        sum = fmaf(f, ml.y, sum);
+        x = make_float4(fmaf(f, u.x, x.x), fmaf(f, u.y, x.y), fmaf(f, u.z, x.z), fmaf(f, u.w, x.w));
+        y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+      }
+      write_row<T>(p, q, at, col, x, y, big, sum);
+    }
+  }
 }
 
 template <typename T, int MT, typename C>

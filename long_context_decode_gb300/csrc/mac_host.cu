@@ -243,10 +243,11 @@ AppendParams append_params(const mac_config *c, const mac_ring_layout &R, uint8_
 }
 
 // Chunk workspace: the status word first (where mac_last_status reads a
-// scratch's), the CTAs' notes of cut units, then the units' pieces.  Only
-// the status word outlives a call.
+// scratch's), the CTAs' notes of cut units, counts of their pieces (zero
+// before and after a call), then the units' pieces.  Only the status word
+// outlives a call.
 struct ChunkLayout {
-  size_t ctl, notes, part, total;
+  size_t ctl, notes, counts, part, total;
   int part_rows;
 };
 
@@ -259,6 +260,7 @@ ChunkLayout chunk_layout(const mac_config *c, int32_t n_tokens) {
   size_t off = 0;
   L.ctl = off;    off = align_up(off + 64 * 4, 256);
   L.notes = off;  off = align_up(off + (size_t)kChunkGrid * sizeof(int4), 256);
+  L.counts = off; off = align_up(off + (size_t)kChunkGrid * 4, 256);
   L.part = off;   off = align_up(off + 2 * (size_t)kChunkGrid * L.part_rows * kChunkStride * 4, 256);
   L.total = off;
   return L;
@@ -479,6 +481,8 @@ int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int3
   const int grid = sms < kChunkGrid ? sms : kChunkGrid;
   const int64_t rows = (int64_t)n_tokens * p.G;
   const int few = cross && rows <= (int64_t)kFewRows * p.B ? (rows <= 16LL * p.B ? 16 : 32) : 0;
+  // (the kernel's last piece joins a unit's pieces, if there are units enough for each to have few)
+  if (few && (int64_t)p.B * p.Hkv * kFewPieces >= grid) p.counts = (uint32_t *)(ws + L.counts);
   if ((few     ? launch_cross_few(p, few, f32, grid, s)
        : cross ? (f32 ? launch_cross_f32(p, grid, s) : launch_cross_bf16(p, grid, s))
                : (f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s))) != cudaSuccess)
@@ -490,11 +494,11 @@ int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int3
     const int64_t tiles = (C::kMinShare + C::kCut - C::kStart) / tile_cost;  // an equal share is at least kMinShare
     return (n_tokens / (rows / p.G) + (int64_t)p.B) * p.Hkv <= grid && p.max_len <= tiles * C::kKeys;
   };
-  if (few)
-    return (few == 16 ? f32 ? each(FewF32<16>{}, 16, FewF32<16>::kTile) : each(FewBf16<16>{}, 16, FewBf16<16>::kTile)
-                      : f32 ? each(FewF32<32>{}, 32, FewF32<32>::kTile) : each(FewBf16<32>{}, 32, FewBf16<32>::kTile)) ||
-                   launch_chunk_merge(p, grid, f32, s) == cudaSuccess
-               ? MAC_OK : MAC_ERR_CUDA;
+  if (few) {
+    const bool one = few == 16 ? f32 ? each(FewF32<16>{}, 16, FewF32<16>::kTile) : each(FewBf16<16>{}, 16, FewBf16<16>::kTile)
+                               : f32 ? each(FewF32<32>{}, 32, FewF32<32>::kTile) : each(FewBf16<32>{}, 32, FewBf16<32>::kTile);
+    return one || p.counts || launch_chunk_merge(p, grid, f32, s) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+  }
   if (f32 ? each(ChunkF32{}, ChunkF32::kRows, ChunkF32::kTile)
           : each(ChunkBf16{}, ChunkBf16::kRows, ChunkBf16::kTile) || each(ChunkBf16{}, ChunkBf16::kRows / 2, ChunkBf16::kTileHalf))
     return MAC_OK;
