@@ -95,20 +95,22 @@ struct CrossF32 : ChunkF32 {
 };
 // The same for few rows per source (mac_cross_few.cu), in quarters of a tile's
 // 64 KB of keys and values, 1.4 us at an SM's share of HBM.
-constexpr int kFewRows = 32;          // most rows of a source, on average
+// Against the kernels above (us): one row over 57 keys 4.6 and 7.8; 16 rows of 16
+// sources of 400 to 1500 keys 15.9 and 18.3; in fp32 16 rows over 4 x 32768 196 and
+// 308.  With two row tiles of 16 it was no faster than they are: 20 rows of 4 sources
+// of 8192 to 32768 keys 56.8 and 53.4, 32 in fp32 over 4 x 32768 357 and 308.
+constexpr int kFewRows = 16;          // most rows of a source, on average
 // Pieces of a unit, on average, that the last of them joins by itself (more: the merge kernel).
 constexpr int kFewPieces = 24;
-template <int ROWS, int KEYS>
+template <int KEYS>
 struct CrossFew {
-  static constexpr int kRows = ROWS, kKeys = KEYS;
+  static constexpr int kRows = kFewRows, kKeys = KEYS;
   static constexpr int kStart = 5, kTile = 4, kTileHalf = 4, kMinShare = 9, kCut = 12;
   static constexpr bool kHalves = false, kCross = true;
   static constexpr long long kMost = (long long)kFewRows * kMaxUnits;
 };
-template <int ROWS>
-struct FewBf16 : CrossFew<ROWS, 128> {};
-template <int ROWS>
-struct FewF32 : CrossFew<ROWS, 64> {};
+struct FewBf16 : CrossFew<128> {};
+struct FewF32 : CrossFew<64> {};
 constexpr int kChunkStride = kHeadDim + 8;  // floats per row of a partial: o[d], m, l, and to a multiple of 32 bytes
 
 // Launch with programmatic stream serialization: the kernel may start while
@@ -154,8 +156,8 @@ cudaError_t launch_chunk_bf16(const ChunkParams &p, int grid, cudaStream_t s);
 // The same with every row attending all of its request's keys.
 cudaError_t launch_cross_f32(const ChunkParams &p, int grid, cudaStream_t s);
 cudaError_t launch_cross_bf16(const ChunkParams &p, int grid, cudaStream_t s);
-// For few rows per source, in units of `rows` 16 or 32 (mac_cross_few.cu).
-cudaError_t launch_cross_few(const ChunkParams &p, int rows, bool f32, int grid, cudaStream_t s);
+// For few rows per source (mac_cross_few.cu).
+cudaError_t launch_cross_few(const ChunkParams &p, bool f32, int grid, cudaStream_t s);
 // The cut units of an attention launch of `grid` CTAs.
 cudaError_t launch_chunk_merge(const ChunkParams &p, int grid, bool f32, cudaStream_t s);
 

@@ -4,11 +4,11 @@
 // For a row with query q, over the keys of its source's memory:
 //   x_j = q . k_j log2(e)/sqrt(d);  m a running reference of the row's maximum;
 //   l = sum 2^(x_j - m);  o = sum 2^(x_j - m) v_j;  out = o / l;  lse = m ln 2 + ln l.
-// A unit is up to 16 MT packed rows (token-major, the G heads of a token
-// together) of one KV head.  Bound by HBM: every key and value is read once for a
-// unit, and 16 rows are few enough for the warps' own matrix instructions (m16n8,
-// 32 to 96 of them per 8 KB), which start on 4 KB of keys where a tcgen05 tile
-// wants 128 rows and 32 KB.
+// A unit is up to 16 packed rows (token-major, the G heads of a token together)
+// of one KV head.  Bound by HBM: every key and value is read once for a unit, and
+// 16 rows are few enough for the warps' own matrix instructions (m16n8, 32 to 96
+// of them per 8 KB), which start on 4 KB of keys where a tcgen05 tile wants 128
+// rows and 32 KB.
 //
 // One CTA per SM, eight warps.  Within a key tile a warp has keys of its own,
 // copies them into stages of its own and keeps maximum, sum and output of its
@@ -35,12 +35,13 @@
 namespace mac {
 namespace {
 
-constexpr int kWarps = 8, kThr = kWarps * 32;
+constexpr int kWarps = 8, kThr = kWarps * 32, kRows = 16, kStages = 3;
 constexpr int kStep = 8192;                   // bytes of a warp's keys and values in a tile; of 16 rows of output
 static_assert(kStep == 16 * kHeadDim * 4, "a stage that has been read takes the outputs of a row tile");
 
 template <typename T>
 constexpr int kKeysOf = sizeof(T) == 4 ? 8 : 16;  // keys of a warp in a tile
+constexpr int kLoads = 8;                     // pieces of a row that are read at once
 constexpr int kQStride = kHeadDim + 16;       // floats between rows of the fp32 queries' parts
 
 // A piece of a unit.
@@ -49,18 +50,16 @@ struct Piece {
   int tok0, n_tok;    // first row of the batch, rows
   int keys;           // of the memory
   int t0, t1;         // key tiles; none: the walk has ended
-  int c0, c1;         // a cut unit's first and last CTA; else -1
+  int tiles;          // of the unit
+  long long first;    // place of the unit's first tile on the cost axis
+  __device__ bool cut() const { return t1 - t0 < tiles; }
 };
 
-template <typename T, int MT>
+template <typename T>
 struct Shared {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kRows = 16 * MT;
-  static constexpr int kStages = kF32 && MT == 2 ? 2 : 3;
-  // One bf16 row tile's queries stay in registers; two, and fp32's (both parts), lie here.
-  static constexpr bool kQShared = kF32 || MT == 2;
   uint8_t stage[kWarps][kStages][kStep];
-  uint8_t q[kF32 ? 2 : 1][kQShared ? kRows * (kF32 ? kQStride * 4 : kHeadDim * 2) : 16];
+  float q[kF32 ? 2 : 1][kF32 ? kRows * kQStride : 4];  // fp32: the queries' parts (bf16's stay in registers)
   float2 ml[kWarps][kRows];
   Piece pieces[kWarps][4];
   uint32_t arrived[2];   // pieces of a cut unit that were done before this CTA's
@@ -119,6 +118,12 @@ __device__ __forceinline__ long long div_down(long long a, long long b) {
   return (unsigned long long)(a | b) >> 32 ? div_s64(a, b) : (uint32_t)a / (uint32_t)b;
 }
 
+// Sum over the warp's lanes, each up to 2^52.
+__device__ __forceinline__ long long warp_sum(long long v) {
+  const uint32_t a = (uint32_t)v & 0x3ffffff, b = (uint32_t)(v >> 26);
+  return ((long long)__reduce_add_sync(0xffffffffu, b) << 26) + __reduce_add_sync(0xffffffffu, a);
+}
+
 // A source, as the plan sees it.
 struct Source {
   int row0, n, keys;   // first row, rows (0: nothing to attend), states
@@ -148,13 +153,14 @@ struct Walk {
     s.tiles = (int)(((long long)m + C::kKeys - 1) / C::kKeys);
     return s;
   }
-  __device__ __forceinline__ long long cost(const Source &s) const { return START + (long long)TILE * s.tiles; }
+  __device__ __forceinline__ int cost(const Source &s) const { return START + TILE * s.tiles; }  // tiles <= 2^25
 
   // false: nothing to do
   __device__ bool start(const ChunkParams &p) {
     const int lane = threadIdx.x & 31;
     lt = log2i(C::kRows) - (31 - __clz(p.G));
-    long long total = 0, units = 0, top = 0;
+    long long total = 0;
+    int units = 0, top = 0;  // 2^24 and 2^28 at most
     odd = false;
     Source mine;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -162,20 +168,17 @@ struct Walk {
       if (b0 + lane < p.B) mine = source(p, b0 + lane);
       odd |= mine.odd;
       if (mine.units) {
-        total += mine.units * cost(mine);
+        total += (long long)mine.units * cost(mine);
         units += mine.units;
         top = max(top, cost(mine));
       }
     }
     odd = __any_sync(0xffffffffu, odd);
-#pragma unroll 1
-    for (int d = 16; d; d >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, d);
-      units += __shfl_xor_sync(0xffffffffu, units, d);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    }
+    total = warp_sum(total);
+    units = __reduce_add_sync(0xffffffffu, units);
+    top = __reduce_max_sync(0xffffffffu, top);
     const long long ctas = max(1, (int)min(total / C::kMinShare, (long long)gridDim.x));
-    whole = units <= gridDim.x && (top - C::kCut - 1) * ctas < total;
+    whole = units <= (int)gridDim.x && (top - C::kCut - 1) * ctas < total;
     share = whole ? 1 : div_down(total + ctas - 1, ctas);
     x = blockIdx.x * share;
     end = min(whole ? units : total, x + share);
@@ -187,9 +190,9 @@ struct Walk {
         mine = {};
         if (b0 + lane < p.B) mine = source(p, b0 + lane);
       }
-      const long long v = whole ? mine.units : mine.units ? mine.units * cost(mine) : 0;
+      const long long v = whole ? mine.units : mine.units ? (long long)mine.units * cost(mine) : 0;
       long long sum = v;
-#pragma unroll 1
+#pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += o;
@@ -211,9 +214,13 @@ struct Walk {
     }
     if (!found) return false;  // (not while the arrays stay as they are)
     k = (int)(whole ? x - before : div_down(x - before, cost(src)));
-    at = before + (whole ? k : k * cost(src));
+    at = before + (whole ? k : (long long)k * cost(src));
     return true;
   }
+
+  // CTAs that hold a cut unit's first and last tile.
+  __device__ int first_cta(const Piece &q) const { return (int)div_down(q.first, share); }
+  __device__ int last_cta(const Piece &q) const { return (int)div_down(q.first + (long long)TILE * (q.tiles - 1), share); }
 
   // The next piece with a tile; one without: the CTA's work is done.
   __device__ Piece next(const ChunkParams &p) {
@@ -228,11 +235,7 @@ struct Walk {
         at = x = last + TILE;
       }
       const int blocks = src.units / p.Hkv, g = k / blocks, i = k - g * blocks;
-      Piece q = {b, g, src.row0 + (i << lt), min(1 << lt, src.n - (i << lt)), src.keys, t0, t1, -1, -1};
-      if (t1 - t0 < src.tiles && t0 < t1) {
-        q.c0 = (int)div_down(first, share);
-        q.c1 = (int)div_down(last, share);
-      }
+      const Piece q = {b, g, src.row0 + (i << lt), min(1 << lt, src.n - (i << lt)), src.keys, t0, t1, src.tiles, first};
       if (++k == src.units && x < end) {
         k = 0;
         do {
@@ -258,6 +261,13 @@ __device__ __forceinline__ uint32_t arrive(uint32_t *count) {
   return before;
 }
 
+// A state of weight f joins (x, y, sum).
+__device__ __forceinline__ void add_state(float4 &x, float4 &y, float &sum, float f, float4 u, float4 v, float l) {
+  sum = fmaf(f, l, sum);
+  x = make_float4(fmaf(f, u.x, x.x), fmaf(f, u.y, x.y), fmaf(f, u.z, x.z), fmaf(f, u.w, x.w));
+  y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+}
+
 // Row `at` of a unit: 4 columns from 4 col and 64 + 4 col on.
 template <typename T>
 __device__ __forceinline__ void write_row(const ChunkParams &p, const Piece &q, int at, int col, float4 x, float4 y, float m, float l) {
@@ -269,12 +279,12 @@ __device__ __forceinline__ void write_row(const ChunkParams &p, const Piece &q, 
   if (p.lse && col == 0) p.lse[to] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-template <typename T, int MT, bool PAGED, typename C>
+template <typename T, bool PAGED, typename C>
 __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ ChunkParams p) {
-  using SM = Shared<T, MT>;
-  constexpr bool F32 = SM::kF32, QS = SM::kQShared;
-  constexpr int KW = kKeysOf<T>, ROWS = SM::kRows, NST = SM::kStages, AHEAD = NST - 1;
-  static_assert(C::kRows == ROWS && C::kKeys == kWarps * KW && KW * kHeadDim * (int)sizeof(T) * 2 == kStep, "tiles");
+  using SM = Shared<T>;
+  constexpr bool F32 = SM::kF32;
+  constexpr int KW = kKeysOf<T>, AHEAD = kStages - 1;
+  static_assert(C::kRows == kRows && C::kKeys == kWarps * KW && KW * kHeadDim * (int)sizeof(T) * 2 == kStep, "tiles");
   static_assert(AHEAD <= 2, "the copies are at most three pieces ahead, and their place in the ring is free");
   extern __shared__ __align__(1024) uint8_t smem[];
   SM &sm = *reinterpret_cast<SM *>(smem);
@@ -296,19 +306,19 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     __syncwarp();
   };
 
-  // ---- queries: one bf16 row tile as the products' operands, the others by way of
-  // registers into shared memory, which a piece's end must leave first
-  constexpr int UNITS = kHeadDim * (int)sizeof(T) / 16, NQ = QS ? ROWS * UNITS / kThr : 1;  // 16-byte parts of a row; of a thread
-  uint32_t qa[QS ? 1 : 8][4];
-  uint4 fresh[NQ];
+  // ---- queries: bf16 as the products' operands; fp32 by way of registers into
+  // shared memory, which a piece's end must leave first
+  constexpr int UNITS = kHeadDim * (int)sizeof(T) / 16;  // 16-byte parts of a row
+  uint32_t qa[F32 ? 1 : 8][4];
+  float4 fresh[F32 ? kRows * kHeadDim / 4 / kThr : 1];
   auto load_q = [&](const Piece &q) {
     const int n_rows = q.n_tok * p.G;
-    auto q_row = [&](int r) { return (const uint8_t *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim * sizeof(T); };
-    if constexpr (QS) {
+    auto q_row = [&](int r) { return (const T *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim; };
+    if constexpr (F32) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
+      for (int i = 0; i < kRows * kHeadDim / 4 / kThr; ++i) {
         const int e = i * kThr + tid, r = e / UNITS;
-        fresh[i] = r < n_rows ? *reinterpret_cast<const uint4 *>(q_row(r) + e % UNITS * 16) : make_uint4(0, 0, 0, 0);
+        fresh[i] = r < n_rows ? *reinterpret_cast<const float4 *>(q_row(r) + e % UNITS * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     } else {
 #pragma unroll
@@ -323,22 +333,17 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     }
   };
   auto put_q = [&] {
-    if constexpr (QS) {
+    if constexpr (F32) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int e = i * kThr + tid, r = e / UNITS, c = e % UNITS;
-        if constexpr (F32) {
-          const float *f = reinterpret_cast<const float *>(&fresh[i]);
-          float4 hi, lo;
-          split(f[0], hi.x, lo.x);
-          split(f[1], hi.y, lo.y);
-          split(f[2], hi.z, lo.z);
-          split(f[3], hi.w, lo.w);
-          *reinterpret_cast<float4 *>(sm.q[0] + r * kQStride * 4 + c * 16) = hi;
-          *reinterpret_cast<float4 *>(sm.q[F32] + r * kQStride * 4 + c * 16) = lo;
-        } else {
-          *reinterpret_cast<uint4 *>(sm.q[0] + place<T>(r, c, false)) = fresh[i];
-        }
+      for (int i = 0; i < kRows * kHeadDim / 4 / kThr; ++i) {
+        const int e = i * kThr + tid, at = e / UNITS * kQStride + e % UNITS * 4;
+        float4 hi, lo;
+        split(fresh[i].x, hi.x, lo.x);
+        split(fresh[i].y, hi.y, lo.y);
+        split(fresh[i].z, hi.z, lo.z);
+        split(fresh[i].w, hi.w, lo.w);
+        *reinterpret_cast<float4 *>(sm.q[0] + at) = hi;
+        *reinterpret_cast<float4 *>(sm.q[F32] + at) = lo;
       }
       __syncthreads();
     }
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     }
     copies_end();
     if (in.t1 <= in.t0) return;
-    if (++stage_in == NST) stage_in = 0;
+    if (++stage_in == kStages) stage_in = 0;
     if (++in_tile == in.t1) enter();
     page = page_of();
   };
@@ -415,7 +420,6 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
   // a lane's rows of the bf16 operands; two 16-byte parts further on are an exclusive or away
   const uint32_t of_k = place<uint16_t>((lane & 7) + (lane >> 4 << 3), lane >> 3 & 1, false);
   const uint32_t of_v = place<uint16_t>(lane & 15, lane >> 4, true);
-  const uint32_t of_q = smem_addr(sm.q) + (QS && !F32 ? place<uint16_t>(lane & 15, lane >> 4, false) : 0);
   int4 note = make_int4(0, 0, 0, 0);
   int stage = 0;
   Piece cut[2];        // the cut units of this CTA's first and last piece
@@ -424,14 +428,9 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
   for (int number = 0;; ++number) {
     const Piece q = sm.pieces[warp][number & 3];
     if (q.t1 <= q.t0) break;
-    float o[MT][16][4], m[MT][2], l[MT][2];
+    float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
-      m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = 0.f;
-    }
+    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 #pragma unroll 1
     for (int tile = q.t0; tile < q.t1; ++tile) {
       __syncwarp();  // the stage that comes next has been read
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
       __syncwarp();
       const uint32_t kb = stages + stage * kStep, vb = kb + kStep / 2;
       const uint8_t *kp = sm.stage[warp][stage], *vp = kp + kStep / 2;
-      if (++stage == NST) stage = 0;
+      if (++stage == kStages) stage = 0;
       const int left = q.keys - (tile * C::kKeys + warp * KW);  // keys of the warp's that exist
       if (left <= 0) continue;
       if (gone >> AHEAD & 1) {
@@ -448,17 +447,14 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
         continue;
       }
       // scores: KW keys, 8 per column tile.  A product waits 21 cycles for one into
-      // the same sums, so with one row tile there are four sums in turn
-      constexpr int NT = KW / 8, SUMS = F32 ? (MT == 1 ? 4 : 2) : (MT == 1 ? 2 : 1);
-      float s[MT][NT][4];
+      // the same sums, so there are four sums in turn
+      constexpr int NT = KW / 8;
+      float s[NT][4], x[4][4];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e >> 2][e & 3] = 0.f;
       if constexpr (F32) {
         // column order within 16: a lane's four neighbours are columns t and t + 4 of two products
-        float x[MT][SUMS][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < SUMS * 4; ++e) x[i][e >> 2][e & 3] = 0.f;
-#pragma unroll 2
         for (int c = 0; c < kHeadDim / 16; ++c) {
           const float4 kx = *reinterpret_cast<const float4 *>(kp + place<T>(g, c * 4 + t, false));
           float h[4], r[4];
@@ -466,120 +462,86 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
           split(kx.y, h[1], r[1]);
           split(kx.z, h[2], r[2]);
           split(kx.w, h[3], r[3]);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const uint8_t *at = sm.q[0] + (i * 16 + g) * kQStride * 4 + c * 64 + t * 16, *at1 = at + (sm.q[F32] - sm.q[0]);
-            const float4 x0 = *reinterpret_cast<const float4 *>(at), x1 = *reinterpret_cast<const float4 *>(at + 8 * kQStride * 4);
-            const float4 y0 = *reinterpret_cast<const float4 *>(at1), y1 = *reinterpret_cast<const float4 *>(at1 + 8 * kQStride * 4);
-            const float a0[4] = {x0.x, x1.x, x0.y, x1.y}, a1[4] = {y0.x, y1.x, y0.y, y1.y};
-            const float b0[4] = {x0.z, x1.z, x0.w, x1.w}, b1[4] = {y0.z, y1.z, y0.w, y1.w};
-            mma_tf32(x[i][0], a1, h[0], h[1]);
-            mma_tf32(x[i][1], b1, h[2], h[3]);
-            mma_tf32(x[i][SUMS - 2], a0, h[0], h[1]);
-            mma_tf32(x[i][SUMS - 1], b0, h[2], h[3]);
-            mma_tf32(x[i][0], a0, r[0], r[1]);
-            mma_tf32(x[i][1], b0, r[2], r[3]);
-          }
+          const float *at = sm.q[0] + g * kQStride + c * 16 + t * 4, *at1 = sm.q[F32] + g * kQStride + c * 16 + t * 4;
+          const float4 x0 = *reinterpret_cast<const float4 *>(at), x1 = *reinterpret_cast<const float4 *>(at + 8 * kQStride);
+          const float4 y0 = *reinterpret_cast<const float4 *>(at1), y1 = *reinterpret_cast<const float4 *>(at1 + 8 * kQStride);
+          const float a0[4] = {x0.x, x1.x, x0.y, x1.y}, a1[4] = {y0.x, y1.x, y0.y, y1.y};
+          const float b0[4] = {x0.z, x1.z, x0.w, x1.w}, b1[4] = {y0.z, y1.z, y0.w, y1.w};
+          mma_tf32(x[0], a1, h[0], h[1]);
+          mma_tf32(x[1], b1, h[2], h[3]);
+          mma_tf32(x[2], a0, h[0], h[1]);
+          mma_tf32(x[3], b0, h[2], h[3]);
+          mma_tf32(x[0], a0, r[0], r[1]);
+          mma_tf32(x[1], b0, r[2], r[3]);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][0][e] = (SUMS == 4 ? x[i][SUMS - 2][e] + x[i][SUMS - 1][e] : 0.f) + (x[i][0][e] + x[i][1][e]);
+        for (int e = 0; e < 4; ++e) s[0][e] = (x[2][e] + x[3][e]) + (x[0][e] + x[1][e]);
       } else {
-        float x[MT][SUMS][2][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < SUMS * 8; ++e) x[i][e >> 3][e >> 2 & 1][e & 3] = 0.f;
         const uint32_t at = kb + of_k;
         uint32_t b[2][4];
         ldm4(b[0], at);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t a[QS ? MT : 1][4];
-          if constexpr (QS) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) ldm4(a[i], (of_q ^ (c & 3) << 5) + (c >> 2) * 128 + i * 16 * 256);
-          }
           if (c < 7) ldm4(b[c + 1 & 1], (at ^ (c + 1 & 3) << 5) + (c + 1 >> 2) * 128);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            mma_bf16(x[i][c % SUMS][0], QS ? a[QS ? i : 0] : qa[QS ? 0 : c], b[c & 1][0], b[c & 1][1]);
-            mma_bf16(x[i][c % SUMS][1], QS ? a[QS ? i : 0] : qa[QS ? 0 : c], b[c & 1][2], b[c & 1][3]);
-          }
+          mma_bf16(x[c & 1], qa[c], b[c & 1][0], b[c & 1][1]);
+          mma_bf16(x[2 + (c & 1)], qa[c], b[c & 1][2], b[c & 1][3]);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][j][e] = SUMS == 2 ? x[i][0][j][e] + x[i][SUMS - 1][j][e] : x[i][0][j][e];
+          for (int e = 0; e < 4; ++e) s[j][e] = x[2 * j][e] + x[2 * j + 1][e];
       }
       if (left < KW) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j * 8 + t * 2 + (e & 1) >= left) s[i][j][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            if (j * 8 + t * 2 + (e & 1) >= left) s[j][e] = -INFINITY;
       }
       // weights
-      uint32_t pa[MT][4];          // bf16: the weights as an operand
-      float ph[MT][4], pl[MT][4];  // fp32: their parts
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        float top[2] = {-INFINITY, -INFINITY};
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
+      bool grows = false;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[i][j][e]);
-        bool grows = false;
+      for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+        grows |= top[h] > m[h] + lazy;
+      }
+      if (__any_sync(0xffffffffu, grows)) {  // the reference moves where the maximum has grown by 8 in base 2
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-          grows |= top[h] > m[i][h] + lazy;
-        }
-        if (__any_sync(0xffffffffu, grows)) {
+          const float mn = fmaxf(m[h], top[h]), ms = mn == -INFINITY ? 0.f : mn;
+          const float corr = ex2((m[h] - ms) * scale);
+          m[h] = mn;
+          l[h] *= corr;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mn = fmaxf(m[i][h], top[h]), ms = mn == -INFINITY ? 0.f : mn;
-            const float corr = ex2((m[i][h] - ms) * scale);
-            m[i][h] = mn;
-            l[i][h] *= corr;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              o[i][j][2 * h] *= corr;
-              o[i][j][2 * h + 1] *= corr;
-            }
+          for (int j = 0; j < 16; ++j) {
+            o[j][2 * h] *= corr;
+            o[j][2 * h + 1] *= corr;
           }
-        }
-        float ms[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) ms[h] = m[i][h] == -INFINITY ? 0.f : m[i][h] * scale;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[i][j][e] = ex2(fmaf(s[i][j][e], scale, -ms[e >> 1]));
-            l[i][e >> 1] += s[i][j][e];
-          }
-        if constexpr (F32) {
-          // the key order of the products is (2 t, 2 t + 1) for columns t and t + 4: what a lane has
-          const float w[4] = {s[i][0][0], s[i][0][2], s[i][0][1], s[i][0][3]};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split(w[e], ph[i][e], pl[i][e]);
-        } else {
-          // the weights to bf16, as chunk attention's: the product takes both factors so
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[i][0]) : "f"(s[i][0][1]), "f"(s[i][0][0]));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[i][1]) : "f"(s[i][0][3]), "f"(s[i][0][2]));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[i][2]) : "f"(s[i][NT - 1][1]), "f"(s[i][NT - 1][0]));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[i][3]) : "f"(s[i][NT - 1][3]), "f"(s[i][NT - 1][2]));
         }
       }
+      float ms[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ms[h] = m[h] == -INFINITY ? 0.f : m[h] * scale;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[j][e] = ex2(fmaf(s[j][e], scale, -ms[e >> 1]));
+          l[e >> 1] += s[j][e];
+        }
       // values
       if constexpr (F32) {
+        // the key order of the products is (2 t, 2 t + 1) for columns t and t + 4: what a lane has
+        const float w[4] = {s[0][0], s[0][2], s[0][1], s[0][3]};
+        float ph[4], pl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split(w[e], ph[e], pl[e]);
 #pragma unroll
         for (int c = 0; c < kHeadDim / 32; ++c) {  // 32 columns: a lane's four neighbours are a column of four products
           const float4 v0 = *reinterpret_cast<const float4 *>(vp + place<T>(2 * t, c * 8 + g, true));
@@ -592,27 +554,27 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
             split(b[e], bh[e], bl[e]);
           }
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
+          for (int e = 0; e < 4; ++e) mma_tf32(o[c * 4 + e], pl, ah[e], bh[e]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma_tf32(o[i][c * 4 + e], pl[i], ah[e], bh[e]);
+          for (int e = 0; e < 4; ++e) mma_tf32(o[c * 4 + e], ph, al[e], bl[e]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma_tf32(o[i][c * 4 + e], ph[i], al[e], bl[e]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mma_tf32(o[i][c * 4 + e], ph[i], ah[e], bh[e]);
-          }
+          for (int e = 0; e < 4; ++e) mma_tf32(o[c * 4 + e], ph, ah[e], bh[e]);
         }
       } else {
+        // the weights to bf16, as chunk attention's: the product takes both factors so
+        uint32_t pa[4];
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[0]) : "f"(s[0][1]), "f"(s[0][0]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[1]) : "f"(s[0][3]), "f"(s[0][2]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[2]) : "f"(s[NT - 1][1]), "f"(s[NT - 1][0]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pa[3]) : "f"(s[NT - 1][3]), "f"(s[NT - 1][2]));
         const uint32_t at = vb + of_v;
         uint32_t b[2][4];
         ldm4t(b[0], at);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           if (c < 7) ldm4t(b[c + 1 & 1], (at ^ (c + 1 & 3) << 5) + (c + 1 >> 2) * 128);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            mma_bf16(o[i][2 * c], pa[i], b[c & 1][0], b[c & 1][1]);
-            mma_bf16(o[i][2 * c + 1], pa[i], b[c & 1][2], b[c & 1][3]);
-          }
+          mma_bf16(o[2 * c], pa, b[c & 1][0], b[c & 1][1]);
+          mma_bf16(o[2 * c + 1], pa, b[c & 1][2], b[c & 1][3]);
         }
       }
     }
@@ -620,80 +582,70 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     // ---- the piece's end: the warps' states joined
     const Piece after = sm.pieces[warp][number + 1 & 3];
     if (after.t1 > after.t0) load_q(after);  // on its way meanwhile
-    const int last = stage == 0 ? NST - 1 : stage - 1;  // the stage that has been read
+    const int last = stage == 0 ? kStages - 1 : stage - 1;  // the stage that has been read
     const int n_rows = q.n_tok * p.G, c = blockIdx.x;
-    const bool whole = q.c0 < 0;
+    const bool whole = !q.cut();
+    const int c0 = whole ? 0 : walk.first_cta(q);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 1);
-        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 2);
-        if (t == 0) sm.ml[warp][i * 16 + h * 8 + g] = make_float2(m[i][h] * scale, l[i][h]);  // base 2
-      }
-    // A row tile's outputs take the warps' stages that have been read last: rows of
-    // 512 bytes, 16 bytes swizzled by the row, so that neither a store's lanes nor a
-    // load's meet a bank twice.
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (t == 0) sm.ml[warp][h * 8 + g] = make_float2(m[h] * scale, l[h]);  // base 2
+    }
+    // The outputs take the warps' stages that have been read last: rows of 512 bytes,
+    // 16 bytes swizzled by the row, so that neither a store's lanes nor a load's
+    // meet a bank twice.
     const int row = tid >> 4, col = tid & 15;  // a thread joins columns 4 col .. and 64 + 4 col .. of a row
     auto joint = [&](int w, int r, int unit) { return reinterpret_cast<float *>(sm.stage[w][last] + r * 512 + ((unit ^ (r & 7)) << 4)); };
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (i > 0) __syncthreads();  // the last row tile's have been read
-      __syncwarp();
+    for (int h = 0; h < 2; ++h) {
+      const int r = h * 8 + g;
+      if constexpr (F32) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = h * 8 + g;
-        if constexpr (F32) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            *reinterpret_cast<float4 *>(joint(warp, r, j * 8 + t * 2)) =
-                make_float4(o[i][j * 4][2 * h], o[i][j * 4 + 1][2 * h], o[i][j * 4 + 2][2 * h], o[i][j * 4 + 3][2 * h]);
-            *reinterpret_cast<float4 *>(joint(warp, r, j * 8 + t * 2 + 1)) =
-                make_float4(o[i][j * 4][2 * h + 1], o[i][j * 4 + 1][2 * h + 1], o[i][j * 4 + 2][2 * h + 1], o[i][j * 4 + 3][2 * h + 1]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            *reinterpret_cast<float2 *>(joint(warp, r, j * 2 + (t >> 1)) + (t & 1) * 2) = make_float2(o[i][j][2 * h], o[i][j][2 * h + 1]);
+        for (int j = 0; j < 4; ++j) {
+          *reinterpret_cast<float4 *>(joint(warp, r, j * 8 + t * 2)) = make_float4(o[j * 4][2 * h], o[j * 4 + 1][2 * h], o[j * 4 + 2][2 * h], o[j * 4 + 3][2 * h]);
+          *reinterpret_cast<float4 *>(joint(warp, r, j * 8 + t * 2 + 1)) =
+              make_float4(o[j * 4][2 * h + 1], o[j * 4 + 1][2 * h + 1], o[j * 4 + 2][2 * h + 1], o[j * 4 + 3][2 * h + 1]);
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<float2 *>(joint(warp, r, j * 2 + (t >> 1)) + (t & 1) * 2) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
       }
-      __syncthreads();
-      const int at = i * 16 + row;
-      if (at < n_rows) {
-        float2 ml[kWarps];
-        float big = -INFINITY, sum = 0.f;
+    }
+    __syncthreads();
+    if (row < n_rows) {
+      float2 ml[kWarps];
+      float big = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ml[w] = sm.ml[w][at];
-          big = fmaxf(big, ml[w].x);
-        }
-        const float ref = big == -INFINITY ? 0.f : big;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      for (int w = 0; w < kWarps; ++w) {
+        ml[w] = sm.ml[w][row];
+        big = fmaxf(big, ml[w].x);
+      }
+      const float ref = big == -INFINITY ? 0.f : big;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2(ml[w].x - ref);
-          sum = fmaf(f, ml[w].y, sum);
-          const float4 u = *reinterpret_cast<const float4 *>(joint(w, row, col)), v = *reinterpret_cast<const float4 *>(joint(w, row, col + 16));
-          x = make_float4(fmaf(f, u.x, x.x), fmaf(f, u.y, x.y), fmaf(f, u.z, x.z), fmaf(f, u.w, x.w));
-          y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
-        }
-        if (whole) {
-          write_row<T>(p, q, at, col, x, y, big, sum);
-        } else {
-          float *dst = p.part + ((int64_t)(2 * c + (c == q.c0 ? 1 : 0)) * p.part_rows + at) * kChunkStride;
-          *reinterpret_cast<float4 *>(dst + col * 4) = x;
-          *reinterpret_cast<float4 *>(dst + 64 + col * 4) = y;
-          if (col == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = make_float2(big, sum);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 u = *reinterpret_cast<const float4 *>(joint(w, row, col)), v = *reinterpret_cast<const float4 *>(joint(w, row, col + 16));
+        add_state(x, y, sum, ex2(ml[w].x - ref), u, v, ml[w].y);
+      }
+      if (whole) {
+        write_row<T>(p, q, row, col, x, y, big, sum);
+      } else {
+        float *dst = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + row) * kChunkStride;
+        *reinterpret_cast<float4 *>(dst + col * 4) = x;
+        *reinterpret_cast<float4 *>(dst + 64 + col * 4) = y;
+        if (col == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = make_float2(big, sum);
       }
     }
     __syncthreads();  // the stages are free again, the partials written
     put_q();
     if (whole) continue;
-    if (c == q.c0) note = make_int4(q.tok0, q.g, n_rows, q.c1);
+    if (c == c0) note = make_int4(q.tok0, q.g, n_rows, walk.last_cta(q));
     if (p.counts) {
       cut[n_cut] = q;
-      if (tid == 0) sm.arrived[n_cut] = arrive(p.counts + q.c0);
+      if (tid == 0) sm.arrived[n_cut] = arrive(p.counts + c0);
       ++n_cut;
     }
   }
@@ -708,50 +660,61 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
 #pragma unroll 1
   for (int i = 0; i < n_cut; ++i) {
     const Piece q = i ? cut[1] : cut[0];
-    const int n = q.c1 - q.c0 + 1, n_rows = q.n_tok * p.G;
+    const int c0 = walk.first_cta(q), n = walk.last_cta(q) - c0 + 1, n_rows = q.n_tok * p.G;
     if (sm.arrived[i] + 1 != (uint32_t)n) continue;
-    if (tid == 0) p.counts[q.c0] = 0;  // for the next call
-    const int col = tid & 15;
-    for (int at = tid >> 4; at < n_rows; at += 16) {
-      auto part = [&](int j) { return p.part + ((int64_t)(2 * (q.c0 + j) + (j == 0)) * p.part_rows + at) * kChunkStride; };
-      float big = -INFINITY, sum = 0.f;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) big = fmaxf(big, __ldcg(reinterpret_cast<const float2 *>(part(j) + kHeadDim)).x);
-      const float ref = big == -INFINITY ? 0.f : big;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(j) + kHeadDim));
-        const float4 u = __ldcg(reinterpret_cast<const float4 *>(part(j) + col * 4)), v = __ldcg(reinterpret_cast<const float4 *>(part(j) + 64 + col * 4));
-        const float f = ex2(ml.x - ref);
-        sum = fmaf(f, ml.y, sum);
-        x = make_float4(fmaf(f, u.x, x.x), fmaf(f, u.y, x.y), fmaf(f, u.z, x.z), fmaf(f, u.w, x.w));
-        y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+    if (tid == 0) p.counts[c0] = 0;  // for the next call
+    const int row = tid >> 4, col = tid & 15;
+    if (row >= n_rows) continue;
+    float big = -INFINITY, sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += kLoads) {  // in one trip to L2 for so many pieces
+      float2 ml[kLoads];
+      float4 u[kLoads], v[kLoads];
+      float most = big;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const float *part = p.part + ((int64_t)(2 * (c0 + j0 + j) + (j0 + j == 0)) * p.part_rows + row) * kChunkStride;
+        ml[j] = make_float2(-INFINITY, 0.f);
+        u[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + j < n) {
+          ml[j] = __ldcg(reinterpret_cast<const float2 *>(part + kHeadDim));
+          u[j] = __ldcg(reinterpret_cast<const float4 *>(part + col * 4));
+          v[j] = __ldcg(reinterpret_cast<const float4 *>(part + 64 + col * 4));
+        }
       }
-      write_row<T>(p, q, at, col, x, y, big, sum);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) most = fmaxf(most, ml[j].x);
+      const float ref = most == -INFINITY ? 0.f : most, keep = ex2(big - ref);
+      sum *= keep;
+      x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+      y = make_float4(y.x * keep, y.y * keep, y.z * keep, y.w * keep);
+      big = most;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) add_state(x, y, sum, ex2(ml[j].x - ref), u[j], v[j], ml[j].y);
     }
+    write_row<T>(p, q, row, col, x, y, big, sum);
   }
 }
 
-template <typename T, int MT, typename C>
+template <typename T, typename C>
 cudaError_t launch(const ChunkParams &p, int grid, cudaStream_t s) {
-  constexpr int kBytes = sizeof(Shared<T, MT>);
+  constexpr int kBytes = sizeof(Shared<T>);
   static_assert(kBytes <= (int)kMaxSmem, "shared memory of a CTA");
   static DeviceFlags done[2];
   cudaError_t e;
   if (p.kv.paged) {
-    if ((e = prepare_chunk(few_kernel<T, MT, true, C>, done[1], kBytes, 0)) != cudaSuccess) return e;
-    return launch_dependent(few_kernel<T, MT, true, C>, grid, kThr, kBytes, s, p);
+    if ((e = prepare_chunk(few_kernel<T, true, C>, done[1], kBytes, 0)) != cudaSuccess) return e;
+    return launch_dependent(few_kernel<T, true, C>, grid, kThr, kBytes, s, p);
   }
-  if ((e = prepare_chunk(few_kernel<T, MT, false, C>, done[0], kBytes, 0)) != cudaSuccess) return e;
-  return launch_dependent(few_kernel<T, MT, false, C>, grid, kThr, kBytes, s, p);
+  if ((e = prepare_chunk(few_kernel<T, false, C>, done[0], kBytes, 0)) != cudaSuccess) return e;
+  return launch_dependent(few_kernel<T, false, C>, grid, kThr, kBytes, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_few(const ChunkParams &p, int rows, bool f32, int grid, cudaStream_t s) {
-  if (rows == 16) return f32 ? launch<float, 1, FewF32<16>>(p, grid, s) : launch<uint16_t, 1, FewBf16<16>>(p, grid, s);
-  return f32 ? launch<float, 2, FewF32<32>>(p, grid, s) : launch<uint16_t, 2, FewBf16<32>>(p, grid, s);
+cudaError_t launch_cross_few(const ChunkParams &p, bool f32, int grid, cudaStream_t s) {
+  return f32 ? launch<float, FewF32>(p, grid, s) : launch<uint16_t, FewBf16>(p, grid, s);
 }
 
 }  // namespace mac

@@ -479,11 +479,10 @@ int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int3
   note_launch(s, nullptr, nullptr);
   const bool f32 = cfg->dtype == MAC_F32;
   const int grid = sms < kChunkGrid ? sms : kChunkGrid;
-  const int64_t rows = (int64_t)n_tokens * p.G;
-  const int few = cross && rows <= (int64_t)kFewRows * p.B ? (rows <= 16LL * p.B ? 16 : 32) : 0;
+  const bool few = cross && (int64_t)n_tokens * p.G <= (int64_t)kFewRows * p.B;
   // (the kernel's last piece joins a unit's pieces, if there are units enough for each to have few)
   if (few && (int64_t)p.B * p.Hkv * kFewPieces >= grid) p.counts = (uint32_t *)(ws + L.counts);
-  if ((few     ? launch_cross_few(p, few, f32, grid, s)
+  if ((few     ? launch_cross_few(p, f32, grid, s)
        : cross ? (f32 ? launch_cross_f32(p, grid, s) : launch_cross_bf16(p, grid, s))
                : (f32 ? launch_chunk_f32(p, grid, s) : launch_chunk_bf16(p, grid, s))) != cudaSuccess)
     return MAC_ERR_CUDA;
@@ -495,8 +494,7 @@ int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int3
     return (n_tokens / (rows / p.G) + (int64_t)p.B) * p.Hkv <= grid && p.max_len <= tiles * C::kKeys;
   };
   if (few) {
-    const bool one = few == 16 ? f32 ? each(FewF32<16>{}, 16, FewF32<16>::kTile) : each(FewBf16<16>{}, 16, FewBf16<16>::kTile)
-                               : f32 ? each(FewF32<32>{}, 32, FewF32<32>::kTile) : each(FewBf16<32>{}, 32, FewBf16<32>::kTile);
+    const bool one = f32 ? each(FewF32{}, kFewRows, FewF32::kTile) : each(FewBf16{}, kFewRows, FewBf16::kTile);
     return one || p.counts || launch_chunk_merge(p, grid, f32, s) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
   }
   if (f32 ? each(ChunkF32{}, ChunkF32::kRows, ChunkF32::kTile)
