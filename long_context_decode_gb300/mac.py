@@ -309,33 +309,44 @@ def mac_beam_workspace_size(cfg: mac_config, n_beams: int, vocab: int, n_out: in
     return n.value
 
 
+_LOGITS: dict = {}  # torch dtype -> MAC_*, filled at the first call
+
+
 def mac_beam_select(cfg, beam_ws, n_beams, logits, scores, done, end_token, n_out, placed, scores_out, parent, token, done_out=None,
                     stream=None):
     """The n_out best next tokens of every group's beams.  logits: a [slots,
     vocab] tensor of bf16 or fp32, its rows any distance apart."""
-    import torch
-    what, S, groups = "mac_beam_select", cfg.batch, cfg.batch // max(1, int(n_beams)) * int(n_out)
-    kinds = {torch.bfloat16: MAC_BF16, torch.float32: MAC_F32}
-    if logits.dim() != 2 or logits.shape[0] < S or logits.dtype not in kinds or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise MacError(f"{what}: logits must be {S} rows of bf16 or fp32, a row's elements end to end")
-    stride = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]  # (one row's stride may be anything)
-    _check(load().mac_beam_select(ctypes.byref(cfg), _ptr(beam_ws), int(n_beams), _ptr(logits), kinds[logits.dtype], stride,
-                                  logits.shape[1], _whole(scores, S, f"{what}: scores"), _whole(done, S, f"{what}: done"),
-                                  int(end_token), int(n_out), int(placed), _whole(scores_out, groups, f"{what}: scores_out"),
-                                  _whole(parent, groups, f"{what}: parent"), _whole(token, groups, f"{what}: token"),
-                                  _whole(done_out, groups, f"{what}: done_out"), _stream(stream)), what)
+    if not _LOGITS:
+        import torch
+        _LOGITS.update({torch.bfloat16: MAC_BF16, torch.float32: MAC_F32})
+    S, kind = cfg.batch, _LOGITS.get(logits.dtype)
+    groups = S // n_beams * n_out if n_beams > 0 else 0
+    try:
+        (rows, vocab), (stride, one) = logits.shape, logits.stride()
+    except ValueError:
+        rows = vocab = stride = one = 0
+    if kind is None or rows < S or (one != 1 and vocab > 1):
+        raise MacError(f"mac_beam_select: logits must be {S} rows of bf16 or fp32, a row's elements end to end")
+    if rows == 1:
+        stride = vocab  # (one row's stride may be anything)
+    _check(load().mac_beam_select(ctypes.byref(cfg), _ptr(beam_ws), n_beams, logits.data_ptr(), kind, stride, vocab,
+                                  _whole(scores, S, "mac_beam_select: scores"), _whole(done, S, "mac_beam_select: done"), end_token, n_out,
+                                  int(placed), _whole(scores_out, groups, "mac_beam_select: scores_out"),
+                                  _whole(parent, groups, "mac_beam_select: parent"), _whole(token, groups, "mac_beam_select: token"),
+                                  _whole(done_out, groups, "mac_beam_select: done_out"), _stream(stream)), "mac_beam_select")
 
 
 def mac_reorder_tables(cfg, chunk_ws, pages: mac_pages | None, n_beams, parent, len_in, len_out, shared_in, shared_out, moves,
                        stream=None):
     """Slots take over their parents' pages, lengths and common positions; moves
     ([slots, 8] int32) says what mac_reorder_state has to move."""
-    what, S, n = "mac_reorder_tables", cfg.batch, int(n_beams)
-    _check(load().mac_reorder_tables(ctypes.byref(cfg), _ptr(chunk_ws), ctypes.byref(pages) if pages is not None else None, n,
-                                     _whole(parent, S, f"{what}: parent"), _whole(len_in, S, f"{what}: len_in"),
-                                     _whole(len_out, S, f"{what}: len_out"), _whole(shared_in, S * n, f"{what}: shared_in"),
-                                     _whole(shared_out, S * n, f"{what}: shared_out"), _whole(moves, S * 8, f"{what}: moves"),
-                                     _stream(stream)), what)
+    S = cfg.batch
+    pairs = S * n_beams
+    _check(load().mac_reorder_tables(ctypes.byref(cfg), _ptr(chunk_ws), ctypes.byref(pages) if pages is not None else None, n_beams,
+                                     _whole(parent, S, "mac_reorder_tables: parent"), _whole(len_in, S, "mac_reorder_tables: len_in"),
+                                     _whole(len_out, S, "mac_reorder_tables: len_out"), _whole(shared_in, pairs, "mac_reorder_tables: shared_in"),
+                                     _whole(shared_out, pairs, "mac_reorder_tables: shared_out"), _whole(moves, S * 8, "mac_reorder_tables: moves"),
+                                     _stream(stream)), "mac_reorder_tables")
 
 
 def mac_reorder_state(cfg, chunk_ws, ring, n_beams, moves, kv: mac_kv | None, stream=None):
