@@ -370,6 +370,10 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     in_tile = in.t0;
   };
   enter();
+  if (in.t1 <= in.t0) {  // a span behind the last tile, or before the next unit's first
+    if (tid == 0 && !p.counts) leave_note(p, make_int4(0, 0, 0, 0));
+    return;
+  }
   load_q(in);
   int page = page_of();
   // A lane's part of a step: bf16 16 bytes of every second row, fp32 of every row.

@@ -555,7 +555,7 @@ cudaError_t launch_reorder(const ReorderParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_state(const StateParams &p, int sms, cudaStream_t s) {
-  if (p.n <= 4) return launch_dependent(state_kernel<4, 3>, sms * 3, kStateThr, 0, s, p);
+  if (p.n <= 4) return launch_dependent(state_kernel<4, 2>, sms * 2, kStateThr, 0, s, p);
   return p.n <= 8 ? launch_dependent(state_kernel<8, 2>, sms * 2, kStateThr, 0, s, p) : launch_dependent(state_kernel<16, 1>, sms, kStateThr, 0, s, p);
 }
 

@@ -329,3 +329,14 @@ def test_chunk_and_cross_share_a_workspace(dt):
     c.run()
     assert c.status() == 0 and torch.equal(own_out, ref_out) and torch.equal(own_lse, ref_lse)
     c.check()
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_cross_spans_without_a_tile(dt, paged):
+    # equal spans of the cost axis: the last CTA's may hold no key tile, and it must not look for queries
+    for keys in range(1300, 2700, 100):
+        c = Sources([0, keys], [0, 0, 0, 1], 2, 8, 8, dt, paged, seed=keys)
+        c.run()
+        assert c.status() == 0
+        c.check()
