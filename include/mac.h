@@ -328,7 +328,11 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
  * this cfg; the query is taken as it is.  A source without states (mem_len
  * 0) gives its rows out 0 and lse -inf.  Bad lengths, pages and rows are
  * reported and left out as there.  Cache rows beyond mem_len may hold
- * anything.  The numerics are mac_chunk_attention's. */
+ * anything.  The numerics are mac_chunk_attention's; where there are at most
+ * 16 rows of a KV head per source (n_tokens Hq / Hkv <= 16 B), in bf16 the
+ * probabilities are not rounded to bf16, and in fp32 each product is good to
+ * 2^-20 of its size (2^-24 on average) and elements beyond 3.39e38 count as
+ * infinite. */
 int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, const int32_t *q_start,
                         int32_t group, const int32_t *mem_len, int32_t n_tokens, const mac_kv *kv,
                         void *out, float *lse, void *stream);
@@ -355,12 +359,12 @@ int mac_beam_workspace_size(const mac_config *cfg, int32_t n_beams, int32_t voca
  * slot, row_stride >= vocab elements apart, on any element boundary.  scores:
  * f32 [batch], the beams' sums of log probabilities; -inf: the beam has no
  * candidates (all but one slot of a group before its first token), and its
- * logits are not read.  A candidate is (beam j, token v) with score s =
+ * logits may be anything.  A candidate is (beam j, token v) with score s =
  * scores[j] + x_jv - ln sum_v exp x_jv; logits of -inf are no candidates.
  * The order is that of the exact scores (by s, rounded no coarser than 2^-36),
  * ties to the lowest (j, v), whatever the card's sums in fp32 make of it.
  * done (int32 [batch] or NULL): a beam whose flag is set is finished and is
- * one candidate, end_token with the beam's score; its logits are not read.
+ * one candidate, end_token with the beam's score; its logits may be anything.
  * end_token: a token, or any other number if there is none (then done must be
  * NULL).
  * Outputs, [batch / n_beams][n_out], best first: scores_out f32; parent int32,

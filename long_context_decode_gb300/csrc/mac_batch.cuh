@@ -102,15 +102,17 @@ struct CrossF32 : ChunkF32 {
 constexpr int kFewRows = 16;          // most rows of a source, on average
 // Pieces of a unit, on average, that the last of them joins by itself (more: the merge kernel).
 constexpr int kFewPieces = 24;
-template <int KEYS>
+template <int KEYS, int START>
 struct CrossFew {
   static constexpr int kRows = kFewRows, kKeys = KEYS;
-  static constexpr int kStart = 5, kTile = 4, kTileHalf = 4, kMinShare = 9, kCut = 12;
+  static constexpr int kStart = START, kTile = 4, kTileHalf = 4, kMinShare = 9, kCut = 12;
   static constexpr bool kHalves = false, kCross = true;
   static constexpr long long kMost = (long long)kFewRows * kMaxUnits;
 };
-struct FewBf16 : CrossFew<128> {};
-struct FewF32 : CrossFew<64> {};
+// A start and end in bf16 as 7 quarters of a tile: 16 rows of 2 sources of 3000 keys
+// 10.4 us, as 5 12.7; in fp32, whose tiles take longer, as 5: 4 sources of 300 to 1500 13.9, as 7 14.9.
+struct FewBf16 : CrossFew<128, 7> {};
+struct FewF32 : CrossFew<64, 5> {};
 constexpr int kChunkStride = kHeadDim + 8;  // floats per row of a partial: o[d], m, l, and to a multiple of 32 bytes
 
 // Launch with programmatic stream serialization: the kernel may start while

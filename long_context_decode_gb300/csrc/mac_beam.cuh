@@ -65,6 +65,6 @@ struct StateParams {
 
 cudaError_t launch_reorder(const ReorderParams &p, cudaStream_t s);
 cudaError_t launch_state(const StateParams &p, int sms, cudaStream_t s);
-cudaError_t launch_select(const SelectParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_select(const SelectParams &p, int dtype, int sms, cudaStream_t s);
 
 }  // namespace mac

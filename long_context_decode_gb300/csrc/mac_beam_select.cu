@@ -31,7 +31,10 @@ namespace {
 constexpr int kThr = kScanThreads, kWarps = kThr / 32, kGroups8 = kThr / 8;
 static_assert(kGroups8 == 32 && kMaxPicks <= kGroups8, "a lane holds a group's maximum; the threshold is one of them");
 constexpr int kRoom = 1024;  // candidates that are ranked at once
-constexpr int kEarly = 4;    // keys that a thread of pick_kernel holds
+// Shared memory that a CTA of pick_kernel asks for where there is an SM for each:
+// launched while scan_kernel runs, they would else be put on few SMs together
+// (16 groups: 18.2 us where this takes 10.4).
+constexpr int kApart = 128 << 10;
 // Bound of the error of L, relative to the sum.  An exponent (x - ref) log2 e is
 // off by 2.3 2^-24 of itself (the difference, the product, the constant), and the
 // mean of ref - x under the softmax is at most ln V + 1 <= 14.9: 2.0e-6.  ex2 is
@@ -390,21 +393,16 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = blockIdx.x * p.n;
   uint32_t status = 0;
   // The group's keys, the pieces' best ones first, one to a thread in turn; the
-  // first of them are on their way before anything else is waited for.
+  // first of each are on their way before anything else is waited for.
   const int lists = p.n * p.segs, n_keys = lists * p.n_out;
   const unsigned long long *keys = p.keys + (int64_t)first * p.n_out * p.segs;
-  auto load_key = [&](int i, int *beam) {
+  auto key_at = [&](int i, int *beam) {
     const int rank = (int)((unsigned long long)i * p.lists_inv >> 40), list = i - rank * lists;
     *beam = (int)((unsigned long long)list * p.segs_inv >> 40);
-    return keys[(int64_t)(*beam * p.n_out + rank) * p.segs + list - *beam * p.segs];
+    return keys + (int64_t)(*beam * p.n_out + rank) * p.segs + list - *beam * p.segs;
   };
-  unsigned long long early[kEarly];
-  int early_beam[kEarly];
-#pragma unroll
-  for (int q = 0; q < kEarly; ++q) {
-    early[q] = early_beam[q] = 0;
-    if (tid + q * kThr < n_keys) early[q] = load_key(tid + q * kThr, &early_beam[q]);
-  }
+  int beam0 = 0;
+  const unsigned long long key0 = tid < n_keys ? *key_at(tid, &beam0) : 0;
   for (int j = warp; j < p.n; j += kWarps) {
     const float2 *ml = p.ml + (int64_t)(first + j) * p.segs;
     const float2 mine = lane < p.segs ? ml[lane] : make_float2(-INFINITY, 0.f);  // whatever it is worth: no wait for the score
@@ -442,15 +440,18 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
       top[j] = m;
     }
   }
-  // f(beam, key) of this thread's candidates; a finished beam's key is that of its end
+  // f(beam, key) of this thread's candidates; a finished beam's key is that of its
+  // end.  (A loop that is not unrolled: what a choice waits for is code that has
+  // not been fetched yet.)
   auto candidates = [&](auto f) {
-#pragma unroll
-    for (int q = 0; q < kEarly; ++q)
-      if (early[q] != 0 && kind[early_beam[q]] == 1) f(early_beam[q], early[q]);
-    for (int i = tid + kEarly * kThr; i < n_keys; i += kThr) {
-      int beam;
-      const unsigned long long k = load_key(i, &beam);
-      if (kind[beam] == 1 && k != 0) f(beam, k);
+    int beam = beam0, i = tid;
+    unsigned long long k = key0;
+#pragma unroll 1
+    for (;;) {
+      if (k != 0 && kind[beam] == 1) f(beam, k);
+      i += kThr;
+      if (i >= n_keys) break;
+      k = *key_at(i, &beam);
     }
     if (tid < p.n && kind[tid] == 2) f(tid, 1ull);
   };
@@ -591,17 +592,19 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
 }
 
 template <typename T>
-cudaError_t launch(const SelectParams &p, cudaStream_t s) {
+cudaError_t launch(const SelectParams &p, int sms, cudaStream_t s) {
   const dim3 grid(p.segs, p.S);
   cudaError_t e = p.steps == 1 ? launch_dependent(scan_kernel<T, 1>, grid, kThr, 0, s, p) : launch_dependent(scan_kernel<T, 4>, grid, kThr, 0, s, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(pick_kernel<T>, p.S / p.n, kThr, 0, s, p);
+  static DeviceFlags done;
+  if ((e = prepare_chunk(pick_kernel<T>, done, kApart, 0)) != cudaSuccess) return e;
+  return launch_dependent(pick_kernel<T>, p.S / p.n, kThr, p.S / p.n <= sms ? kApart : 0, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_select(const SelectParams &p, int dtype, cudaStream_t s) {
-  return dtype == MAC_F32 ? launch<float>(p, s) : launch<uint16_t>(p, s);
+cudaError_t launch_select(const SelectParams &p, int dtype, int sms, cudaStream_t s) {
+  return dtype == MAC_F32 ? launch<float>(p, sms, s) : launch<uint16_t>(p, sms, s);
 }
 
 }  // namespace mac

@@ -886,7 +886,7 @@ int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const
   p.ml = (float2 *)(ws + L.ml);
   p.keys = (unsigned long long *)(ws + L.keys);
   note_launch((cudaStream_t)stream, nullptr, nullptr);
-  return launch_select(p, logits_dtype, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+  return launch_select(p, logits_dtype, sms, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
 }
 
 int mac_reorder_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pages, int32_t n_beams,

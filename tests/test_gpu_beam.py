@@ -171,6 +171,22 @@ def test_select_ties_go_to_the_lowest(dt, V):
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
+def test_select_more_ties_than_are_ranked_at_once(dt):
+    # every piece of every beam offers 32 candidates of the same score, and the scores of beams are the same or differ
+    n, V = 16, 70001
+    s = Selection(2 * n, n, V, 32, dt)
+    s.logits.fill_(1.5)
+    s.scores.fill_(-2.0)
+    s.scores[n:] = -2.0 - torch.arange(n, device=DEV).flip(0) * 2.0 ** -21
+    s.run()
+    assert s.status() == 0
+    assert s.parent.tolist() == [[0] * 32, [n - 1] * 32] and s.token.tolist() == [list(range(32))] * 2
+    s.logits[5, 60000:60010] = 1.5078125  # a few above the rest
+    s.run()
+    assert s.parent[0].tolist() == [5] * 10 + [0] * 22 and s.token[0].tolist() == list(range(60000, 60010)) + list(range(22))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("V", [50, 9000, 33333])
 def test_select_orders_scores_that_fp32_sums_cannot_tell_apart(dt, V):
     # beams whose best tokens' scores lie within 2^-22 of one another, of other logits and of the same
@@ -413,7 +429,7 @@ class Histories:
 
 
 @pytest.mark.parametrize("paged", [True, False])
-@pytest.mark.parametrize("groups,n,width", [(1, 2, 8), (3, 4, 20), (2, 5, 6), (16, 4, 40), (4, 16, 12), (7, 8, 700), (5, 1, 9), (128, 8, 9)])
+@pytest.mark.parametrize("groups,n,width", [(1, 2, 8), (3, 4, 20), (2, 5, 6), (16, 4, 40), (4, 16, 12), (7, 8, 700), (5, 1, 9), (128, 8, 9), (1024, 1, 5), (64, 16, 6)])
 def test_reorder_tables(groups, n, width, paged):
     h = Histories(groups, n, width, paged, groups)
     h.grow(width * 9, {g * n for g in range(groups)})  # prompts in the first slot of every group
@@ -783,6 +799,7 @@ def test_beams_decode_as_if_everything_were_copied(groups, n, Hq, Hkv, aux, dt, 
                 assert torch.equal(x.rings[i].ring_view(part), y.rings[i].ring_view(part)), (step, i, part)
     for b in both:
         assert b.status() == [0, 0, 0, 0]
+    assert int(both[0].hits) == int(both[1].hits) > 0  # summaries are reused across reorderings
     if paged:  # histories have pages in common: fewer are held
         assert both[0].n_free.item() > both[1].n_free.item()
     for b in both:
