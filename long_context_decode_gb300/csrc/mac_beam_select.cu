@@ -401,8 +401,11 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
     *beam = (int)((unsigned long long)list * p.segs_inv >> 40);
     return keys + (int64_t)(*beam * p.n_out + rank) * p.segs + list - *beam * p.segs;
   };
-  int beam0 = 0;
-  const unsigned long long key0 = tid < n_keys ? *key_at(tid, &beam0) : 0;
+  unsigned long long early[2] = {0, 0};
+  int early_beam[2] = {0, 0};
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if (tid + q * kThr < n_keys) early[q] = *key_at(tid + q * kThr, &early_beam[q]);
   for (int j = warp; j < p.n; j += kWarps) {
     const float2 *ml = p.ml + (int64_t)(first + j) * p.segs;
     const float2 mine = lane < p.segs ? ml[lane] : make_float2(-INFINITY, 0.f);  // whatever it is worth: no wait for the score
@@ -444,14 +447,19 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
   // end.  (A loop that is not unrolled: what a choice waits for is code that has
   // not been fetched yet.)
   auto candidates = [&](auto f) {
-    int beam = beam0, i = tid;
-    unsigned long long k = key0;
+    int beam = early_beam[0];
+    unsigned long long k = early[0];
 #pragma unroll 1
-    for (;;) {
+    for (int i = tid;;) {
       if (k != 0 && kind[beam] == 1) f(beam, k);
       i += kThr;
       if (i >= n_keys) break;
-      k = *key_at(i, &beam);
+      if (i < 2 * kThr) {
+        k = early[1];
+        beam = early_beam[1];
+      } else {
+        k = *key_at(i, &beam);
+      }
     }
     if (tid < p.n && kind[tid] == 2) f(tid, 1ull);
   };
