@@ -28,6 +28,13 @@
 //   a b = a0 b0 + a0 b1 + a1 b0 + (a1 b1, up to 2^-22 of a b, left out):
 // three products in tf32, each exact in the sums, so a product is off by at most
 // 2^-20 of its size (2^-24 on average).
+//
+// In a graph (us; floor: bytes at 6.7 TB/s): 16 rows of each of 4 sources of 32768
+// keys, 32 / 8 heads, 86.3 (80.1; 6.2 TB/s), in fp32 196 (160); 64 rows over 16
+// sources of 1024 keys 10.2 from L2, 15.2 from HBM (10.2); of 400 to 1500 keys, cut,
+// 16.6 and 19.7 (9.6); one row over 57 keys 4.6.  What is left over the floor
+// is the start (4.5 us until the first keys are there) and, of cut units, join,
+// count and output behind the last key (3 us).
 #include <math.h>
 
 #include "mac_tc.cuh"

@@ -21,8 +21,8 @@ namespace {
 // nothing goes back, its CTAs do not wait for one another before they write.
 // Bound by its chain of trips to L2 (lengths and parents, common positions, ids,
 // the stack) and the barriers between: a step of 16 groups of 4 slots takes
-// TIME_STEP us, beams opened on 16 prompts of up to 32768 tokens (8 slots each, 120K
-// table entries) TIME_FORK.
+// 6.0 us, beams opened on 16 prompts of up to 32768 tokens (8 slots each, 120K
+// table entries) 11.9, most of it the instructions of 17K columns on eight SMs.
 constexpr int kKeeps = (int)0x80000000;  // no id: nothing to write
 constexpr int kLeastThr = 512, kMostThr = 1024, kCluster = 8;
 
@@ -361,6 +361,10 @@ cudaError_t launch(const ReorderParams &p, cudaStream_t s) {
 // slots may change places.  A warp takes an entry of a head (its query and
 // summary) or a row of a KV head (key and value).  Only positions that a slot
 // does not share with its parent are moved.
+// A step (32 slots, 12 positions apart at most, 32 / 8 bf16 heads, paged): 3.8 us,
+// its launch and three trips to memory.  Beams opened on two prompts (8 slots of
+// 8 / 2 fp32 heads, 119 MB read and written): 15.6 us from L2, 19.9 from HBM.  With
+// four CTAs per SM, and so 64 registers, they took 5.9 and 22.6, with three 4.4 and 15.6.
 constexpr int kStateThr = 256;
 
 struct StateShared {
