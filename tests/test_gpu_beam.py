@@ -119,6 +119,7 @@ class Selection:
     (1, 1, 1, 1, 0, 0), (2, 1, 3, 1, 0, 1), (1, 4, 5, 4, 2, 3), (3, 2, 8, 4, 0, 0), (2, 4, 100, 32, 1, 5), (1, 16, 1000, 16, 0, 0),
     (5, 4, 2047, 8, 1, 0), (2, 3, 2049, 3, 0, 1), (16, 4, 8192, 4, 0, 0), (1, 4, 32000, 4, 0, 0), (2, 8, 50001, 16, 7, 0),
     (3, 5, 50257, 10, 0, 0), (40, 4, 20000, 8, 3, 2), (1, 1, 128000, 32, 0, 0), (60, 16, 300, 32, 5, 1), (1, 2, 1 << 20, 4, 0, 0),
+    (1, 16, 1 << 20, 32, 1, 0),
 ])
 def test_select(groups, n, V, n_out, gap, offset, dt):
     for placed in (False, True) if n == n_out else (False,):
@@ -600,6 +601,73 @@ def test_reorder_state(groups, n, Hq, Hkv, K, dt):
     x.layer.release()
 
 
+@pytest.mark.parametrize("paged", [True, False])
+def test_reorder_tables_and_state_with_common_positions_that_cannot_be(paged):
+    """Whatever the caller's array of common positions holds, lengths and parted pages are right and nothing else is touched."""
+    h = Histories(3, 4, 12, paged, 4)
+    h.grow(150)
+    x = Layer(h.S, 4, 2, 40, 12 * PAGE, BF16, 1)
+    for seed in range(6):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        shared = torch.randint(-(1 << 31), (1 << 31) - 1, (h.S, 4), generator=g, device=DEV).int()
+        if seed % 2:
+            shared = torch.randint(-3, 200, (h.S, 4), generator=g, device=DEV).int()
+        parent = [h.rng.randrange(-1, 4) for _ in range(h.S)]
+        table, free, n_free = ints(h.table), ints(h.free), ints([h.n_free])
+        length, moves = ints(h.length), torch.zeros(h.S, 8, dtype=torch.int32, device=DEV)
+        mac.mac_reorder_tables(h.cfg, h.ws, mac.pages_view(table, free, n_free) if paged else None, 4, ints(parent), length, length, shared,
+                               torch.zeros_like(shared), moves)
+        want = [0 if p < 0 else h.length[s // 4 * 4 + p] for s, p in enumerate(parent)]
+        assert length.tolist() == want
+        assert mac.mac_last_status(h.cfg, h.ws) == 0
+        for s, m in enumerate(moves.tolist()):
+            assert m[0] == (-1 if parent[s] < 0 or parent[s] == s % 4 else s // 4 * 4 + parent[s])
+            if m[0] >= 0:
+                assert 1 <= m[1] <= min(h.length[s], want[s]) + 1 and m[2] == max(h.length[s], want[s]) and m[3] == want[s]
+            assert not paged or (0 <= n_free.item() <= h.n_pages)
+        mac.mac_reorder_state(x.cfg, h.ws, x.layer.ring, 4, moves, mac.kv_view(x.k, x.v))
+        assert mac.mac_last_status(h.cfg, h.ws) == 0
+    x.layer.release()
+
+
+@pytest.mark.parametrize("paged", [True, False])
+def test_reorder_state_of_rings_or_cache_alone(paged):
+    S, n, cap = 6, 3, 64
+    x = Layer(S, 2, 1, 16, cap, BF16, 2)
+    for s in range(S):
+        for p in range(1, 40):
+            x.append(s, p)
+    cfg = mac.config(S, 2, 1, ring_k=16, page_size=PAGE if paged else 0, max_context=cap)
+    ws = torch.zeros(mac.mac_chunk_workspace_size(cfg, 1), dtype=torch.uint8, device=DEV)
+    pool = [torch.randn(S * 4, 1, PAGE, D, device=DEV).to(BF16) for _ in range(2)]
+    cache = pool if paged else [x.k, x.v]
+    moves = ints([[2, 30, 39, 39, 3, 9, 7, 0], [0, 31, 39, 39, -1, -1, 0, 0], [-1, 0, 0, 0, -1, -1, 0, 0]] + [[-1, 0, 0, 0, -1, -1, 0, 0]] * 3)
+    rings, keep = [r.clone() for r in x.ring.values()], [c.clone() for c in cache]
+    mac.mac_reorder_state(cfg, ws, x.layer.ring, n, moves, None)
+    assert all(torch.equal(a, b) for a, b in zip(cache, keep))
+    at = [p % 16 for p in range(30, 40)]
+    for r, old in zip(x.ring.values(), rings):
+        if r.dim() == 2:
+            assert torch.equal(r[0, at], old[2, at]) and torch.equal(r[1, at[1:]], old[0, at[1:]]) and torch.equal(r[1, at[0]], old[1, at[0]])
+        else:
+            assert torch.equal(r[0, :, at], old[2, :, at]) and torch.equal(r[1, :, at[1:]], old[0, :, at[1:]])
+            assert torch.equal(r[1, :, at[0]], old[1, :, at[0]])
+        assert torch.equal(r[2:], old[2:])
+    rings = [r.clone() for r in x.ring.values()]
+    mac.mac_reorder_state(cfg, ws, None, n, moves, mac.kv_view(*cache, n_pages=S * 4))
+    assert all(torch.equal(a, b) for a, b in zip(x.ring.values(), rings))
+    for c, old in zip(cache, keep):
+        if paged:
+            assert torch.equal(c[9, :, :7], old[3, :, :7])
+            c[9] = old[9]
+            assert torch.equal(c, old)
+        else:
+            assert torch.equal(c[0, :, 29:39], old[2, :, 29:39]) and torch.equal(c[1, :, 30:39], old[0, :, 30:39])
+            assert torch.equal(c[:, :, :29], old[:, :, :29]) and torch.equal(c[2:], old[2:]) and torch.equal(c[:, :, 39:], old[:, :, 39:])
+    assert mac.mac_last_status(cfg, ws) == 0
+
+
 def test_reorder_state_refuses_moves_outside():
     S, n, cap = 8, 4, 64
     x = Layer(S, 2, 1, 16, cap, BF16, 1)
@@ -807,29 +875,37 @@ def test_beams_decode_as_if_everything_were_copied(groups, n, Hq, Hkv, aux, dt, 
             r.release()
 
 
-def test_beams_decode_in_a_captured_graph():
-    """One graph of a whole step, replayed, against the calls one by one."""
-    rng = random.Random(9)
-    tokens = [[rng.randrange(700) for _ in range(20 + 9 * g)] for g in range(3)]
-    plain, graphed = (Beams(True, 3, 4, 8, 2, BF16, True, 2) for _ in range(2))
-    for b in (plain, graphed):
-        b.hits = torch.zeros((), dtype=torch.int32, device=DEV)
-        b.scores.copy_(torch.tensor([0.0, -1, -2, -3]).repeat(3))
-        b.prompt(tokens)
-        b.step()
-    torch.cuda.synchronize()
-    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
-    # the library's calls take the stream of the capture
+def captured_step(b, side):
+    """A graph of one step; the library's calls take the stream of the capture."""
+    graph = torch.cuda.CUDAGraph()
     names = ("mac_build_tables", "mac_write_kv", "mac_cross_attention", "mac_beam_select", "mac_reorder_tables", "mac_reorder_state")
     keep = {x: getattr(mac, x) for x in names}
     for x in names:
         setattr(mac, x, lambda *a, f=keep[x]: f(*a, stream=torch.cuda.current_stream()))
     try:
         with torch.cuda.graph(graph, stream=side):
-            graphed.step()
+            b.step()
     finally:
         for x in names:
             setattr(mac, x, keep[x])
+    return graph
+
+
+def ready_beams(groups, n, dt, paged, seed):
+    rng = random.Random(seed)
+    b = Beams(True, groups, n, 8, 2, dt, paged, 2)
+    b.hits = torch.zeros((), dtype=torch.int32, device=DEV)
+    b.scores.copy_(torch.arange(n, device=DEV).neg().float().repeat(groups))
+    b.prompt([[rng.randrange(700) for _ in range(20 + 9 * g)] for g in range(groups)])
+    b.step()
+    torch.cuda.synchronize()
+    return b
+
+
+def test_beams_decode_in_a_captured_graph():
+    """One graph of a whole step, replayed, against the calls one by one."""
+    plain, graphed = (ready_beams(3, 4, BF16, True, 9) for _ in range(2))
+    graph = captured_step(graphed, torch.cuda.Stream())
     for _ in range(25):
         plain.step()
         graph.replay()
@@ -837,3 +913,32 @@ def test_beams_decode_in_a_captured_graph():
         for x in ("length", "parent", "token", "out", "cross", "scores", "table"):
             assert torch.equal(getattr(plain, x), getattr(graphed, x)), x
     assert plain.status() == graphed.status() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("paged", [True, False])
+def test_two_programs_of_beams_at_once(paged):
+    """Two programs, each its own stream, workspaces, cache and graph, replayed side by side: each leaves what it leaves alone."""
+    shapes = ((3, 4, BF16), (2, 5, F32))
+    alone = []
+    for groups, n, dt in shapes:
+        b = ready_beams(groups, n, dt, paged, n)
+        for _ in range(20):
+            b.step()
+        torch.cuda.synchronize()
+        alone.append(b)
+    both = [ready_beams(groups, n, dt, paged, n) for groups, n, dt in shapes]
+    sides = [torch.cuda.Stream() for _ in both]
+    graphs = [captured_step(b, side) for b, side in zip(both, sides)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, side in zip(graphs, sides):
+            with torch.cuda.stream(side):
+                g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(alone, both):
+        for name in ("length", "parent", "token", "out", "cross", "scores", "common"):
+            assert torch.equal(getattr(x, name), getattr(y, name)), name
+        for i in range(2):
+            for part in ("pos", "q", "o", "lse"):
+                assert torch.equal(x.rings[i].ring_view(part), y.rings[i].ring_view(part))
+        assert y.status() == [0, 0, 0, 0]

@@ -340,3 +340,24 @@ def test_cross_spans_without_a_tile(dt, paged):
         c.run()
         assert c.status() == 0
         c.check()
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_cross_wait_runs_out(dt, paged):
+    # many rows: the kernels that wait for copies and products.  A key stage that is never filled is reported and left
+    c = Sources([3000, 1500], [90, 90], 1, 8, 2, dt, paged, seed=9)
+    mac.mac_test_wait_budget(1 << 16, 1)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() & mac.MAC_DEV_WAIT_TIMEOUT
+    c.ws = torch.zeros_like(c.ws)
+    c.run()
+    assert c.status() == 0
+    c.check()
+    # few rows: nothing waits for another role, so no budget runs out
+    c = Sources([3000, 1500], [1, 1], 1, 8, 2, dt, paged, seed=9)
+    mac.mac_test_wait_budget(1, 0)
+    c.run()
+    assert c.status() == 0
+    c.check()
