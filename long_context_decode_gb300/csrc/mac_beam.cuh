@@ -25,6 +25,7 @@ struct SelectParams {
   int32_t *parent, *token, *done_out;
   float2 *ml;                     // [S][segs] maximum and sum of exp of a CTA's logits
   unsigned long long *keys;       // [S][n_out][segs] its best ones; 0: none
+  uint32_t *counts;               // [S / n] CTAs of a group that are done; zero before and after a call
   uint32_t *status;
 };
 
@@ -65,6 +66,6 @@ struct StateParams {
 
 cudaError_t launch_reorder(const ReorderParams &p, cudaStream_t s);
 cudaError_t launch_state(const StateParams &p, int sms, cudaStream_t s);
-cudaError_t launch_select(const SelectParams &p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_select(const SelectParams &p, int dtype, cudaStream_t s);
 
 }  // namespace mac

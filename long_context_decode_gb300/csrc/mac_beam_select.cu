@@ -4,15 +4,15 @@
 //   L_j = ln sum_v exp x_jv;   s_jv = c_j + x_jv - L_j;
 // the n_out largest s of the group, ties to the lowest (j, v).
 //
-// scan_kernel reads every logit once, a CTA a piece of a row: its threads keep
-// running sums of exponentials and their largest logit.  Within a row the order
-// of s is that of x, so a piece's n_out best by (x, lowest v) are all that can
-// be chosen of it.  They are found by a threshold: the n_out-th largest of the
+// One kernel.  Its CTAs read every logit once, a CTA a piece of a row: its threads
+// keep running sums of exponentials and their largest logit.  Within a row the
+// order of s is that of x, so a piece's n_out best by (x, lowest v) are all that
+// can be chosen of it.  They are found by a threshold: the n_out-th largest of the
 // maxima of 32 groups of threads is a lower bound that few logits pass.  The
 // logits of the few threads whose largest one passes are read again, by all
 // threads (by themselves they took half of all instructions, as nearly every
-// warp has such a thread); what passes is ranked by counting.  pick_kernel, a CTA per group, joins the pieces and
-// ranks the beams' candidates against one another.
+// warp has such a thread); what passes is ranked by counting.  The last of a
+// group's CTAs joins the pieces and ranks the beams' candidates against one another.
 //
 // Across beams the order depends on L.  The sums are in fp32, so L is known to
 // kSlack only; where that leaves the order of a candidate that counts open
@@ -20,13 +20,16 @@
 // beams in question are summed again to 2^-38 and the candidates ranked anew.
 // So the choice is that of the exact scores, however the card adds.
 //
-// In a graph (us; floor: bytes at 6.7 TB/s): 4 beams of 32000 bf16 logits 7.9 (0.04);
-// 64 of 128000 10.3 from L2, 11.8 from HBM (2.4); 256 of 50001 fp32 logits, 16 of
-// each 8 beams, 17.0 and 22.5 (7.6).  Bound by the two kernels' barriers and by code
-// that is fetched for the first time (about 4 us each), then by the scan's CTAs,
-// which end together: their thresholds and rankings overlap nothing.  With four
-// CTAs per SM aimed at; with eight 12.6 and 16.1, with twelve 14.5 and 18.9 of
-// 12.2 and 16.9.  A beam summed again takes 15 us in its group's CTA.
+// In a graph (us; floor: bytes at 6.7 TB/s): 4 beams of 32000 bf16 logits 8.0 (0.04);
+// 64 of 128000 11.6 from L2, 12.9 from HBM (2.4); 256 of 50001 fp32 logits, 16 of
+// each 8 beams, 16.6 and 22.0 (7.6).  Bound by barriers and by code that is fetched
+// for the first time (about 3 us of a scan, 4 of a choice), then by the scan's CTAs,
+// which end together: their thresholds and rankings overlap nothing.  Four CTAs per
+// SM aimed at: with three 11.7 and 20.1, with five 13.5 and 16.6 of 11.6 and 16.6.
+// With the choice a kernel of its own, whose CTAs start ahead, a graph takes 7.9,
+// 10.3 and 17.0, but calls from Python one after another 14.2, 15.8 and 22.0 where
+// this takes 11.0, 11.9 and 21.5.  A beam summed again takes its group's CTA 12 us
+// of 32000 logits, 65 of 128000 (instructions: some 100 for each logit).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -39,17 +42,13 @@ namespace {
 constexpr int kThr = kScanThreads, kWarps = kThr / 32, kGroups8 = kThr / 8;
 static_assert(kGroups8 == 32 && kMaxPicks <= kGroups8, "a lane holds a group's maximum; the threshold is one of them");
 constexpr int kRoom = 1024;  // candidates that are ranked at once
-// Shared memory that a CTA of pick_kernel asks for where there is an SM for each:
-// launched while scan_kernel runs, they would else be put on few SMs together
-// (16 groups: 18.2 us where this takes 10.4).
-constexpr int kApart = 128 << 10;
 // Bound of the error of L, relative to the sum.  An exponent (x - ref) log2 e is
 // off by 2.3 2^-24 of itself (the difference, the product, the constant), and the
 // mean of ref - x under the softmax is at most ln V + 1 <= 14.9: 2.0e-6.  ex2 is
 // off by 2^-22: of a term, of the moves of its reference (1.6 with every move by
 // e^-1 or less), of the joins in a CTA and of the pieces: 1.1e-6.  Sums round 7, 8 and
 // 7 times by 2^-24 (a thread's batches are added with their rounded parts): 1.3e-6.
-// The logarithm 2^-23.  4.5e-6 in all.
+// The logarithm 2^-22 ln 2.  4.6e-6 in all.
 constexpr double kSlack = 5.0 / (1 << 20);
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -153,24 +152,25 @@ __device__ __forceinline__ float top_of(const uint4 &u, float) {
   return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
 }
 
-// U vectors of a thread at a time, the next ones on their way meanwhile.
+struct ScanShared {
+  __align__(16) float gmax[kGroups8];
+  float wsum[kWarps], nth;
+  unsigned long long room[kRoom];
+  unsigned long long wbest[kWarps];
+  uint8_t passed[kThr];
+  int count, n_passed;
+};
+
+// Piece `seg` of beam b's row; U vectors of a thread at a time, the next ones on
+// their way meanwhile.
 template <typename T, int U>
-__global__ void __launch_bounds__(kThr, 4) scan_kernel(const __grid_constant__ SelectParams p) {
+__device__ __forceinline__ void scan_piece(const SelectParams &p, ScanShared &sm, int seg, int b) {
   constexpr int VEC = Row<T>::VEC;
   constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-  __shared__ __align__(16) float gmax[kGroups8];
-  __shared__ float wsum[kWarps], nth;
-  __shared__ unsigned long long room[kRoom];
-  __shared__ unsigned long long wbest[kWarps];
-  __shared__ uint8_t passed[kThr];
-  __shared__ int count, n_passed;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, seg = blockIdx.x, b = blockIdx.y;
-  if (!goes_on(p, b)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Row<T> row(p, b);
   const int i0 = seg * p.steps * kThr + tid;
-  if (tid == 0) count = n_passed = 0;
+  if (tid == 0) sm.count = sm.n_passed = 0;
 
   Running r;
   uint4 cur[U], next[U];
@@ -216,10 +216,10 @@ __global__ void __launch_bounds__(kThr, 4) scan_kernel(const __grid_constant__ S
   float g = mx;
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
-  if ((lane & 7) == 0) gmax[tid >> 3] = g;
+  if ((lane & 7) == 0) sm.gmax[tid >> 3] = g;
   __syncthreads();
-  find_nth(gmax, p.n_out, &nth);
-  g = gmax[lane];
+  find_nth(sm.gmax, p.n_out, &sm.nth);
+  g = sm.gmax[lane];
 #pragma unroll
   for (int d = 16; d; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
   const float m = g;
@@ -228,21 +228,21 @@ __global__ void __launch_bounds__(kThr, 4) scan_kernel(const __grid_constant__ S
   if (m > -INFINITY) s *= ex2((r.ref - m) * kLog2e);
 #pragma unroll
   for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if (lane == 0) wsum[warp] = s;
+  if (lane == 0) sm.wsum[warp] = s;
   __syncthreads();
-  const float least = nth;
+  const float least = sm.nth;
   // the threads whose logits may pass, looked through by all of them
-  if (mx >= least && mx > -INFINITY) passed[atomicAdd(&n_passed, 1)] = (uint8_t)tid;
+  if (mx >= least && mx > -INFINITY) sm.passed[atomicAdd(&sm.n_passed, 1)] = (uint8_t)tid;
   __syncthreads();
   auto take = [&](float x, int v) {
     if (x >= least && x > -INFINITY) {
-      const int at = atomicAdd(&count, 1);
-      if (at < kRoom) room[at] = key_of(x, v);
+      const int at = atomicAdd(&sm.count, 1);
+      if (at < kRoom) sm.room[at] = key_of(x, v);
     }
   };
-  const int n_vecs = n_passed * p.steps;
+  const int n_vecs = sm.n_passed * p.steps;
   for (int q = tid; q < n_vecs; q += kThr) {
-    const int k = q / n_passed, i = (seg * p.steps + k) * kThr + passed[q - k * n_passed];
+    const int k = q / sm.n_passed, i = (seg * p.steps + k) * kThr + sm.passed[q - k * sm.n_passed];
     if (i >= row.full) continue;
     const uint4 u = *row.vec(i);
     float x[VEC];
@@ -252,16 +252,16 @@ __global__ void __launch_bounds__(kThr, 4) scan_kernel(const __grid_constant__ S
   }
   if (extra >= 0) take(loose, extra);
   __syncthreads();
-  const int c = count;
+  const int c = sm.count;
   unsigned long long *out = p.keys + (int64_t)b * p.n_out * p.segs + seg;  // its r-th best at out[r * segs]
   if (tid == 0) {
-    float all = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
-    all += (wsum[4] + wsum[5]) + (wsum[6] + wsum[7]);
+    float all = (sm.wsum[0] + sm.wsum[1]) + (sm.wsum[2] + sm.wsum[3]);
+    all += (sm.wsum[4] + sm.wsum[5]) + (sm.wsum[6] + sm.wsum[7]);
     p.ml[(int64_t)b * p.segs + seg] = make_float2(m, all);
   }
   if (c <= kRoom) {
-    rank_all(c, [&](int i, int j) { return room[j] > room[i]; }, [&](int i, int rank) {
-      if (rank < p.n_out) out[rank * p.segs] = room[i];
+    rank_all(c, [&](int i, int j) { return sm.room[j] > sm.room[i]; }, [&](int i, int rank) {
+      if (rank < p.n_out) out[rank * p.segs] = sm.room[i];
     });
     for (int i = c + tid; i < p.n_out; i += kThr) out[i * p.segs] = 0;
     return;
@@ -293,10 +293,10 @@ __global__ void __launch_bounds__(kThr, 4) scan_kernel(const __grid_constant__ S
 #pragma unroll
     for (int d = 16; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
     __syncthreads();  // the last round's have been read
-    if (lane == 0) wbest[warp] = best;
+    if (lane == 0) sm.wbest[warp] = best;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) best = max(best, wbest[w]);
+    for (int w = 0; w < kWarps; ++w) best = max(best, sm.wbest[w]);
     if (tid == 0) out[q * p.segs] = best;
     last = best;
   }
@@ -315,10 +315,9 @@ struct Precise {
 };
 
 __device__ __forceinline__ float2 exp2f2(const Precise &t, float x, float m) {
-  float dh = x - m;
-  const float bb = dh - x;
-  const float dl = (x - (dh - bb)) + (-m - bb);  // x - m = dh + dl exactly
-  if (!(dh > -80.f)) return make_float2(0.f, 0.f);  // below 2^-115
+  const float d = x - m, bb = d - x;
+  const float dh = fmaxf(d, -80.f);  // no branch: a thread's logits are worked on together
+  const float dl = (x - (d - bb)) + (-m - bb);  // x - m = d + dl exactly
   const float k = rintf(dh * 92.332482616893657f);  // 64 / ln 2
   // ln 2 / 64 = c0 + c1 + c2; c0 and c1 have 9 bits, so k c0 and k c1 are exact for |k| < 2^13
   constexpr float c0 = 0.010833740234375f, c1 = -3.3155083656311035e-06f, c2 = -2.976022343684012e-11f;
@@ -334,20 +333,29 @@ __device__ __forceinline__ float2 exp2f2(const Precise &t, float x, float m) {
   const float h = T.x * rh, e = fmaf(T.x, rh, -h);
   const float sh = T.x + h;
   const float sl = (h - (sh - T.x)) + (e + (T.y + (T.x * lo + T.y * rh)));
+  if (!(d > -80.f)) return make_float2(0.f, 0.f);  // below 2^-115
   const float scale = __uint_as_float((uint32_t)((j >> 6) + 127) << 23);
   return make_float2(sh * scale, sl * scale);
 }
 
+// Logits of a thread that are loaded and worked on at a time (all four beams of 32000:
+// 56 us; 60 with 8, 69 with 4).
+constexpr int kAhead = 16;
 template <typename T>
 __device__ double precise_sum(const SelectParams &p, int b, float m, const Precise &t, double *wsum) {
   const T *row = (const T *)p.logits + b * p.stride;
   float sh = 0.f, sl = 0.f;
-#pragma unroll 4
-  for (int v = threadIdx.x; v < p.V; v += kThr) {
-    const float2 x = exp2f2(t, elem_f32<T>(row, v), m);
-    const float a = sh + x.x, bb = a - sh;
-    sl += ((sh - (a - bb)) + (x.x - bb)) + x.y;
-    sh = a;
+  for (int v0 = threadIdx.x; v0 < p.V; v0 += kAhead * kThr) {
+    float x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) x[u] = v0 + u * kThr < p.V ? elem_f32<T>(row, v0 + u * kThr) : -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float2 y = exp2f2(t, x[u], m);
+      const float a = sh + y.x, bb = a - sh;
+      sl += ((sh - (a - bb)) + (y.x - bb)) + y.y;
+      sh = a;
+    }
   }
   double s = (double)sh + (double)sl;
 #pragma unroll
@@ -382,23 +390,39 @@ static_assert(kMaxVocab == 1 << 20 && kMaxBeams <= 1 << 11, "a place in 32 bits"
 // x before y
 __device__ __forceinline__ bool before(const Pick &x, const Pick &y) { return x.s > y.s || (x.s == y.s && x.at < y.at); }
 
+// A load that is issued where it stands (the compiler moves others to their use).
+__device__ __forceinline__ unsigned long long load_now(const unsigned long long *at) {
+  unsigned long long v;
+  asm volatile("ld.global.cg.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 load_now(const float2 *at) {
+  float2 v;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(at) : "memory");
+  return v;
+}
+
+struct PickShared {
+  double base[kMaxBeams];                   // c - L + its largest logit; of a finished beam c
+  float base_f[kMaxBeams], top[kMaxBeams];  // base in fp32; its largest logit
+  float2 sum[kMaxBeams];                    // L, as a power of two and the rest
+  float score[kMaxBeams];                   // c
+  int kind[kMaxBeams];                      // 0: no candidates, 1: its tokens, 2: finished
+  float wmax[kWarps][32];
+  __align__(16) float gmax[32];
+  double wsum[kWarps];
+  Pick room[kRoom];
+  Pick best[kMaxPicks], wbest[kWarps];
+  uint16_t sorted[kRoom];                   // places in `room`, best first
+  Precise precise;
+  float nth;
+  int count, open;                          // candidates in `room`; beams whose L is not known well enough
+};
+
+// The choice of a group; its pieces were written by other CTAs too.
 template <typename T>
-__global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ double base[kMaxBeams];      // c - L + its largest logit; of a finished beam c
-  __shared__ float base_f[kMaxBeams], top[kMaxBeams];  // base in fp32; its largest logit
-  __shared__ int kind[kMaxBeams];         // 0: no candidates, 1: its tokens, 2: finished
-  __shared__ float wmax[kWarps][32];
-  __shared__ __align__(16) float gmax[32];
-  __shared__ double wsum[kWarps];
-  __shared__ Pick room[kRoom];
-  __shared__ Pick best[kMaxPicks], wbest[kWarps];
-  __shared__ uint16_t sorted[kRoom];      // places in `room`, best first
-  __shared__ Precise precise;
-  __shared__ float nth;
-  __shared__ int count, open;             // candidates in `room`; beams whose L is not known well enough
-  griddep_launch_dependents();
-  griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = blockIdx.x * p.n;
+__device__ __forceinline__ void pick(const SelectParams &p, PickShared &sm, int group) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = group * p.n;
   uint32_t status = 0;
   // The group's keys, the pieces' best ones first, one to a thread in turn; the
   // first of each are on their way before anything else is waited for.
@@ -413,25 +437,25 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
   int early_beam[2] = {0, 0};
 #pragma unroll
   for (int q = 0; q < 2; ++q)
-    if (tid + q * kThr < n_keys) early[q] = *key_at(tid + q * kThr, &early_beam[q]);
+    if (tid + q * kThr < n_keys) early[q] = load_now(key_at(tid + q * kThr, &early_beam[q]));
   for (int j = warp; j < p.n; j += kWarps) {
     const float2 *ml = p.ml + (int64_t)(first + j) * p.segs;
-    const float2 mine = lane < p.segs ? ml[lane] : make_float2(-INFINITY, 0.f);  // whatever it is worth: no wait for the score
+    // whatever it is worth: no wait for the score
+    const float2 mine = lane < p.segs ? load_now(ml + lane) : make_float2(-INFINITY, 0.f);
     const float c = p.scores[first + j];
     int what = goes_on(p, first + j) ? 1 : 0;
     if (!what && c == c && c < INFINITY && c > -INFINITY) what = 2;
     else if (!what && c != -INFINITY) status |= MAC_DEV_NONFINITE_LOGIT;
-    double l = 0.0;
-    float m = -INFINITY;
+    float m = -INFINITY, log2 = 0.f, rest = 0.f;  // L = (log2 + rest) ln 2
     if (what == 1) {
       m = mine.x;
-      for (int i = lane + 32; i < p.segs; i += 32) m = fmaxf(m, ml[i].x);
+      for (int i = lane + 32; i < p.segs; i += 32) m = fmaxf(m, __ldcg(ml + i).x);
 #pragma unroll
       for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       // an empty piece has sum 0, or NaN
       auto share = [&](float2 x) { return x.x == -INFINITY ? x.y : x.y * ex2((x.x - m) * kLog2e); };
       float sum = share(mine);
-      for (int i = lane + 32; i < p.segs; i += 32) sum += share(ml[i]);
+      for (int i = lane + 32; i < p.segs; i += 32) sum += share(__ldcg(ml + i));
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (!(sum < 1e30f) || m == INFINITY) {  // NaN or +inf among the logits
@@ -441,14 +465,16 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
         what = 0;
       } else {  // 1 <= sum <= 2^20
         const int e = (int)(__float_as_uint(sum) >> 23) - 127;
-        l = e * 0.6931471805599453 + (double)logf(sum * __uint_as_float((uint32_t)(127 - e) << 23));
+        log2 = (float)e;
+        rest = lg2_approx(sum * __uint_as_float((uint32_t)(127 - e) << 23));
       }
     }
     if (lane == 0) {
-      kind[j] = what;
-      base[j] = (double)c - l;
-      base_f[j] = (float)base[j];
-      top[j] = m;
+      sm.kind[j] = what;
+      sm.sum[j] = make_float2(log2, rest);
+      sm.score[j] = c;
+      sm.base_f[j] = c - (log2 + rest) * 0.69314718f;
+      sm.top[j] = m;
     }
   }
   // f(beam, key) of this thread's candidates; a finished beam's key is that of its
@@ -459,80 +485,83 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
     unsigned long long k = early[0];
 #pragma unroll 1
     for (int i = tid;;) {
-      if (k != 0 && kind[beam] == 1) f(beam, k);
+      if (k != 0 && sm.kind[beam] == 1) f(beam, k);
       i += kThr;
       if (i >= n_keys) break;
       if (i < 2 * kThr) {
         k = early[1];
         beam = early_beam[1];
       } else {
-        k = *key_at(i, &beam);
+        k = __ldcg(key_at(i, &beam));
       }
     }
-    if (tid < p.n && kind[tid] == 2) f(tid, 1ull);
+    if (tid < p.n && sm.kind[tid] == 2) f(tid, 1ull);
   };
-  auto rough = [&](int beam, unsigned long long k) { return kind[beam] == 2 ? base_f[beam] : base_f[beam] + (value_of(k) - top[beam]); };
+  auto rough = [&](int beam, unsigned long long k) { return sm.kind[beam] == 2 ? sm.base_f[beam] : sm.base_f[beam] + (value_of(k) - sm.top[beam]); };
   auto exactly = [&](int beam, unsigned long long k) {
     Pick x;
-    const bool end = kind[beam] == 2;
-    x.s = ordered(end ? base[beam] : base[beam] + ((double)value_of(k) - (double)top[beam]));
+    const bool end = sm.kind[beam] == 2;
+    x.s = ordered(end ? sm.base[beam] : sm.base[beam] + ((double)value_of(k) - (double)sm.top[beam]));
     x.at = (uint32_t)beam << 20 | (uint32_t)(end ? p.end : token_of(k));
     return x;
   };
   for (int pass = 0; pass < 2; ++pass) {
-    if (tid == 0) count = open = 0;
+    if (tid == 0) sm.count = sm.open = 0;
     __syncthreads();
     // a lower bound of the n_out-th best, from the maxima of 32 groups of threads, those of a lane
     float g = -INFINITY;
     candidates([&](int beam, unsigned long long k) { g = fmaxf(g, rough(beam, k)); });
-    wmax[warp][lane] = g;
+    sm.wmax[warp][lane] = g;
     __syncthreads();
     if (warp == 0) {
-      for (int w = 1; w < kWarps; ++w) g = fmaxf(g, wmax[w][lane]);
-      gmax[lane] = g;
+      for (int w = 1; w < kWarps; ++w) g = fmaxf(g, sm.wmax[w][lane]);
+      sm.gmax[lane] = g;
+    } else if (warp == 1 && pass == 0 && lane < p.n) {
+      sm.base[lane] = (double)sm.score[lane] - ((double)sm.sum[lane].x + (double)sm.sum[lane].y) * 0.6931471805599453;
     }
     __syncthreads();
-    find_nth(gmax, p.n_out, &nth);
+    find_nth(sm.gmax, p.n_out, &sm.nth);
     float widest = 0.f;
     for (int j = 0; j < p.n; ++j)
-      if (kind[j]) widest = fmaxf(widest, fabsf(base_f[j]));
+      if (sm.kind[j]) widest = fmaxf(widest, fabsf(sm.base_f[j]));
     __syncthreads();
-    // rough scores are off by 2^-24 of the base, of the difference and of the sum: 2^-22 (|base| + |s|) in all, twice
-    const float least = nth == -INFINITY ? nth : nth - (2.f * (float)kSlack + (widest + fabsf(nth)) * (1.f / (1 << 20)));
+    // rough scores are off by 2^-24 of the base, of the difference and of the sum, 2^-22 (|base| + |s|)
+    // in all, and by L's product and sum in fp32, less than kSlack / 2; twice
+    const float least = sm.nth == -INFINITY ? sm.nth : sm.nth - (4.f * (float)kSlack + (widest + fabsf(sm.nth)) * (1.f / (1 << 20)));
     candidates([&](int beam, unsigned long long k) {
       if (rough(beam, k) >= least) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kRoom) room[at] = exactly(beam, k);
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kRoom) sm.room[at] = exactly(beam, k);
       }
     });
     __syncthreads();
-    const int c = count;
+    const int c = sm.count;
     if (c <= kRoom) {
-      rank_all(c, [&](int i, int j) { return before(room[j], room[i]); }, [&](int i, int rank) {
-        sorted[rank] = (uint16_t)i;
-        if (rank < p.n_out) best[rank] = room[i];
+      rank_all(c, [&](int i, int j) { return before(sm.room[j], sm.room[i]); }, [&](int i, int rank) {
+        sm.sorted[rank] = (uint16_t)i;
+        if (rank < p.n_out) sm.best[rank] = sm.room[i];
       });
       __syncthreads();
       if (pass == 1) break;
       // Neighbours of two beams whose order is open, down to where no candidate that counts is in question
       for (int i = tid; i + 1 < c; i += kThr) {
-        const Pick x = room[sorted[i]], y = room[sorted[i + 1]];
-        if (x.beam() == y.beam() || (kind[x.beam()] == 2 && kind[y.beam()] == 2)) continue;
+        const Pick x = sm.room[sm.sorted[i]], y = sm.room[sm.sorted[i + 1]];
+        if (x.beam() == y.beam() || (sm.kind[x.beam()] == 2 && sm.kind[y.beam()] == 2)) continue;
         const double s = of_ordered(x.s);
-        if (s - of_ordered(y.s) <= 2 * kSlack && (i < p.n_out || of_ordered(best[p.n_out - 1].s) - s <= 2 * kSlack))
-          atomicOr(&open, 1 << x.beam() | 1 << y.beam());
+        if (s - of_ordered(y.s) <= 2 * kSlack && (i < p.n_out || of_ordered(sm.best[p.n_out - 1].s) - s <= 2 * kSlack))
+          atomicOr(&sm.open, 1 << x.beam() | 1 << y.beam());
       }
       __syncthreads();
-      if (open == 0) break;
+      if (sm.open == 0) break;
     } else if (pass == 0) {
-      if (tid == 0) open = (1 << p.n) - 1;
+      if (tid == 0) sm.open = (1 << p.n) - 1;
       __syncthreads();
     } else {  // too many of one score: one at a time
       for (int r = 0; r < p.n_out; ++r) {
         Pick x = {0, ~0u};
         candidates([&](int beam, unsigned long long k) {
           const Pick y = exactly(beam, k);
-          if (before(y, x) && (r == 0 || before(best[r - 1], y))) x = y;
+          if (before(y, x) && (r == 0 || before(sm.best[r - 1], y))) x = y;
         });
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
@@ -541,12 +570,12 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
           y.at = __shfl_xor_sync(0xffffffffu, x.at, d);
           if (before(y, x)) x = y;
         }
-        if (lane == 0) wbest[warp] = x;
+        if (lane == 0) sm.wbest[warp] = x;
         __syncthreads();
         if (tid == 0) {
           for (int w = 1; w < kWarps; ++w)
-            if (before(wbest[w], x)) x = wbest[w];
-          best[r] = x;
+            if (before(sm.wbest[w], x)) x = sm.wbest[w];
+          sm.best[r] = x;
         }
         __syncthreads();
       }
@@ -556,33 +585,33 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
     if (tid < 64) {
       const double v = exp2((double)tid / 64);
       const float hi = (float)v;
-      precise.power[tid] = make_float2(hi, (float)(v - (double)hi));
+      sm.precise.power[tid] = make_float2(hi, (float)(v - (double)hi));
     }
-    const int redo = open;
+    const int redo = sm.open;
     __syncthreads();
     for (int j = 0; j < p.n; ++j) {
-      if (!(redo >> j & 1) || kind[j] != 1) continue;
-      const double sum = precise_sum<T>(p, first + j, top[j], precise, wsum);
+      if (!(redo >> j & 1) || sm.kind[j] != 1) continue;
+      const double sum = precise_sum<T>(p, first + j, sm.top[j], sm.precise, sm.wsum);
       if (tid == 0) {
-        base[j] = (double)p.scores[first + j] - log(sum);
-        base_f[j] = (float)base[j];
+        sm.base[j] = (double)p.scores[first + j] - log(sum);
+        sm.base_f[j] = (float)sm.base[j];
       }
     }
     __syncthreads();
   }
-  const int found = min(count, p.n_out);
+  const int found = min(sm.count, p.n_out);
   if (status && lane == 0) set_status(p.status, status);
   if (warp > 0) return;
   // results: lane i has the i-th best
   float score = -INFINITY;
   int beam = -1, token = -1;
   if (lane < found) {
-    const Pick x = best[lane];
+    const Pick x = sm.best[lane];
     score = (float)of_ordered(x.s);
     beam = x.beam();
     token = x.token();
   }
-  const int over = lane >= found || token == p.end || kind[max(beam, 0)] == 2;
+  const int over = lane >= found || token == p.end || sm.kind[max(beam, 0)] == 2;
   int at = lane;
   if (p.placed) {  // the best child of a surviving parent goes to the parent's slot, the others fill up in order
     bool eldest = lane < found;
@@ -599,7 +628,7 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
         if (!(taken >> at & 1) && k-- == 0) break;
   }
   if (lane < p.n_out) {
-    const int64_t o = (int64_t)blockIdx.x * p.n_out + at;
+    const int64_t o = (int64_t)group * p.n_out + at;
     p.scores_out[o] = score;
     p.parent[o] = beam;
     p.token[o] = token;
@@ -607,20 +636,41 @@ __global__ void __launch_bounds__(kThr) pick_kernel(const __grid_constant__ Sele
   }
 }
 
+template <typename T, int U>
+__global__ void __launch_bounds__(kThr, 4) select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ union Shared {
+    ScanShared scan;
+    PickShared pick;
+    __device__ Shared() {}
+  } sm;
+  __shared__ bool last;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int b = blockIdx.y, group = b / p.n;
+  if (goes_on(p, b)) scan_piece<T, U>(p, sm.scan, blockIdx.x, b);
+  // Whoever is the last of a group's CTAs chooses.  What a CTA wrote ahead of the
+  // barrier that thread 0 has come through is seen by whoever finds it counted.
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.counts + group) : "memory");
+    last = before + 1 == (uint32_t)p.n * gridDim.x;
+    if (last) p.counts[group] = 0;  // for the next call
+  }
+  __syncthreads();
+  if (last) pick<T>(p, sm.pick, group);
+}
+
 template <typename T>
-cudaError_t launch(const SelectParams &p, int sms, cudaStream_t s) {
+cudaError_t launch(const SelectParams &p, cudaStream_t s) {
   const dim3 grid(p.segs, p.S);
-  cudaError_t e = p.steps == 1 ? launch_dependent(scan_kernel<T, 1>, grid, kThr, 0, s, p) : launch_dependent(scan_kernel<T, 4>, grid, kThr, 0, s, p);
-  if (e != cudaSuccess) return e;
-  static DeviceFlags done;
-  if ((e = prepare_chunk(pick_kernel<T>, done, kApart, 0)) != cudaSuccess) return e;
-  return launch_dependent(pick_kernel<T>, p.S / p.n, kThr, p.S / p.n <= sms ? kApart : 0, s, p);
+  return p.steps == 1 ? launch_dependent(select_kernel<T, 1>, grid, kThr, 0, s, p) : launch_dependent(select_kernel<T, 4>, grid, kThr, 0, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_select(const SelectParams &p, int dtype, int sms, cudaStream_t s) {
-  return dtype == MAC_F32 ? launch<float>(p, sms, s) : launch<uint16_t>(p, sms, s);
+cudaError_t launch_select(const SelectParams &p, int dtype, cudaStream_t s) {
+  return dtype == MAC_F32 ? launch<float>(p, s) : launch<uint16_t>(p, s);
 }
 
 }  // namespace mac

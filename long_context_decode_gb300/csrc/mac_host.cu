@@ -308,19 +308,20 @@ int select_pieces(int rows, int vocab, int es, int sms) {
   return pieces < steps ? pieces : steps;
 }
 
-// Selection workspace: the status word, then every piece's maximum and sum,
+// Selection workspace: the status word, the groups' counts of CTAs done, then every piece's maximum and sum,
 // and its best logits.  Laid out for the most pieces.
 struct SelectLayout {
-  size_t ctl, ml, keys, total;
+  size_t ctl, counts, ml, keys, total;
 };
 SelectLayout select_layout(const mac_config *c, int32_t vocab, int32_t n_out) {
   const int steps = select_steps(vocab, 4);
   const size_t pieces = (size_t)c->batch * (steps < kMaxPieces ? steps : kMaxPieces);
   SelectLayout L;
   size_t off = 0;
-  L.ctl = off;   off = align_up(off + 64 * 4, 256);
-  L.ml = off;    off = align_up(off + pieces * sizeof(float2), 256);
-  L.keys = off;  off = align_up(off + pieces * n_out * 8, 256);
+  L.ctl = off;     off = align_up(off + 64 * 4, 256);
+  L.counts = off;  off = align_up(off + (size_t)c->batch * 4, 256);
+  L.ml = off;      off = align_up(off + pieces * sizeof(float2), 256);
+  L.keys = off;    off = align_up(off + pieces * n_out * 8, 256);
   L.total = off;
   return L;
 }
@@ -883,10 +884,11 @@ int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const
   const SelectLayout L = select_layout(cfg, vocab, n_out);
   uint8_t *ws = (uint8_t *)beam_ws;
   p.status = (uint32_t *)(ws + L.ctl);
+  p.counts = (uint32_t *)(ws + L.counts);
   p.ml = (float2 *)(ws + L.ml);
   p.keys = (unsigned long long *)(ws + L.keys);
   note_launch((cudaStream_t)stream, nullptr, nullptr);
-  return launch_select(p, logits_dtype, sms, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+  return launch_select(p, logits_dtype, (cudaStream_t)stream) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
 }
 
 int mac_reorder_tables(const mac_config *cfg, void *chunk_ws, const mac_pages *pages, int32_t n_beams,
