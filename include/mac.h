@@ -248,7 +248,8 @@ int mac_chunk_workspace_size(const mac_config *cfg, int32_t n_tokens, size_t *ch
  *     first gives its ceil(len_in/16) pages back and starts at length 0: in
  *     order of request and page they go on top of the stack.  The flags
  *     are not cleared (mac_reset_requests on the same flags, after this
- *     call, empties the request's rings and clears them).
+ *     call, empties the request's rings and clears them).  Slots that share
+ *     pages are given back by mac_reorder_tables, not so.
  *   Pages: the k-th new page, in order of request and page, is the stack's
  *     k-th entry from the top.  Entries above the count stay as they are.
  *   A request is admitted whole or not at all: while the pages and the rows
@@ -349,7 +350,8 @@ int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, co
 #define MAC_MAX_CANDIDATES 32
 
 /* Bytes of beam_ws for mac_beam_select: zero-filled before its first use, for
- * one stream at a time; its device status word is read by
+ * one stream at a time; calls of other n_beams, vocab and n_out may use it if
+ * it is large enough for each.  Its device status word is read by
  * mac_last_status(cfg, beam_ws, ..). */
 int mac_beam_workspace_size(const mac_config *cfg, int32_t n_beams, int32_t vocab, int32_t n_out,
                             size_t *beam_bytes);

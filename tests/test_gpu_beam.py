@@ -292,6 +292,25 @@ def test_select_in_place_on_a_stream_and_in_a_graph():
             assert torch.equal(x, y)
 
 
+def test_select_calls_of_different_sizes_share_a_workspace():
+    # groups, vocabularies and candidates differ from call to call; what a call counts is left as it was found
+    S = 24
+    calls = [Selection(S, n, V, n_out, dt, seed=V + n, placed=n == n_out) for n, V, n_out, dt in [
+        (4, 32000, 4, BF16), (1, 300, 32, F32), (12, 50001, 16, F32), (2, 7, 2, BF16), (3, 128000, 1, BF16), (8, 2048, 8, F32)]]
+    ws = max((c.ws for c in calls), key=len)
+    for c in calls:
+        c.ws = ws
+    calls[2].scores[:12] = -math.inf  # a group without a beam to look at
+    for _ in range(3):
+        for c in calls:
+            c.out.fill_(7)
+            c.parent.fill_(7)
+            c.run()
+    assert calls[0].status() == 0
+    for c in calls:
+        c.check()
+
+
 # ---------------------------------------------------------------------------
 # tables
 # ---------------------------------------------------------------------------

@@ -344,6 +344,34 @@ def test_cross_spans_without_a_tile(dt, paged):
 
 @pytest.mark.parametrize("paged", [True, False])
 @pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("new", [3, 150])
+def test_cross_caches_beyond_32_bit_offsets(new, dt, paged):
+    # the last source's keys and values lie past element 2^32
+    Hkv, mem = 2, [70, 333]
+    c = Sources(mem, [new, new], 1, 8, Hkv, dt, paged, seed=12)
+    if paged:
+        far = (1 << 32) // (Hkv * PAGE * D) + 7
+        big = [torch.empty(far + 40, Hkv, PAGE, D, device=DEV, dtype=dt) for _ in range(2)]
+        for x, small in zip(big, (c.k, c.v)):
+            x[far:far + small.shape[0]] = small
+        c.table[c.table >= 0] += far
+    else:
+        cap = (1 << 32) // (3 * D) + 64
+        big = [torch.empty(2, Hkv, cap, D, device=DEV, dtype=dt) for _ in range(2)]
+        for x, small in zip(big, (c.k, c.v)):
+            x[:, :, :small.shape[2]] = small
+            x[:, :, small.shape[2]:small.shape[2] + 256] = float("nan")
+        assert big[0][1, 1].storage_offset() > 1 << 32
+        c.cfg = mac.config(2, 8, Hkv, dtype=c.cfg.dtype, max_context=cap)
+        c.ws = torch.zeros(mac.mac_chunk_workspace_size(c.cfg, c.T), dtype=torch.uint8, device=DEV)
+    c.kv = mac.kv_view(*big, c.table)
+    c.run()
+    assert c.status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("dt", [BF16, F32])
 def test_cross_wait_runs_out(dt, paged):
     # many rows: the kernels that wait for copies and products.  A key stage that is never filled is reported and left
     c = Sources([3000, 1500], [90, 90], 1, 8, 2, dt, paged, seed=9)
