@@ -363,8 +363,9 @@ int mac_beam_workspace_size(const mac_config *cfg, int32_t n_beams, int32_t voca
  * candidates (all but one slot of a group before its first token), and its
  * logits may be anything.  A candidate is (beam j, token v) with score s =
  * scores[j] + x_jv - ln sum_v exp x_jv; logits of -inf are no candidates.
- * The order is that of the exact scores (by s, rounded no coarser than 2^-36),
- * ties to the lowest (j, v), whatever the card's sums in fp32 make of it.
+ * The order is that of the exact scores (by s, rounded no coarser than 2^-36
+ * or, where that is more, 2^-51 |s|), ties to the lowest (j, v), whatever the
+ * card's sums in fp32 make of it.
  * done (int32 [batch] or NULL): a beam whose flag is set is finished and is
  * one candidate, end_token with the beam's score; its logits may be anything.
  * end_token: a token, or any other number if there is none (then done must be
