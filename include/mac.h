@@ -330,10 +330,10 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
  * 0) gives its rows out 0 and lse -inf.  Bad lengths, pages and rows are
  * reported and left out as there.  Cache rows beyond mem_len may hold
  * anything.  The numerics are mac_chunk_attention's; where there are at most
- * 16 rows of a KV head per source (n_tokens Hq / Hkv <= 16 B), in bf16 the
- * probabilities are not rounded to bf16, and in fp32 each product is good to
- * 2^-20 of its size (2^-24 on average) and elements beyond 3.39e38 count as
- * infinite. */
+ * 16 rows of a KV head per source (n_tokens Hq / Hkv <= 16 B), or few more
+ * and the memory is short, in bf16 the probabilities are not rounded to bf16,
+ * and in fp32 each product is good to 2^-20 of its size (2^-24 on average)
+ * and elements beyond 3.39e38 count as infinite. */
 int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, const int32_t *q_start,
                         int32_t group, const int32_t *mem_len, int32_t n_tokens, const mac_kv *kv,
                         void *out, float *lse, void *stream);

@@ -100,6 +100,16 @@ struct CrossF32 : ChunkF32 {
 // 308.  With two row tiles of 16 it was no faster than they are: 20 rows of 4 sources
 // of 8192 to 32768 keys 56.8 and 53.4, 32 in fp32 over 4 x 32768 357 and 308.
 constexpr int kFewRows = 16;          // most rows of a source, on average
+// More rows take blocks of 16 of them, each of which reads the keys again; the tcgen05
+// kernels start later and take 128 at once.  So this is for memories (caches, as far as
+// the host knows) of that many keys in all blocks, if there is an SM for each block.
+// us here and there, 32 / 8 heads: 5 rows of one source of 128 keys (16 blocks) 6.0 and
+// 8.1, of 8192 (2^17 keys) 15.8 and 17.6, 9 rows of it (2^17.6) 17.8 and 17.9, 16 rows
+// (2^18) 20.5 and 17.6; 8 rows of 4 sources of 2048 (2^17) 15.8 and 16.8, 9 rows 19.1 and
+// 17.0; in fp32 8.5 and 15.3, 33.7 and 33.5, 45.2 and 34.5, 56.8 and 35.9, 33.0 and 36.0,
+// 44.7 and 36.3.  More blocks than SMs: 5 rows of 16 sources of 128 keys (256) 9.6 and
+// 9.4, of 512 18.5 and 12.4.
+constexpr int64_t kFewKeys = 1 << 17;
 // Pieces of a unit, on average, that the last of them joins by itself (more: the merge kernel).
 constexpr int kFewPieces = 24;
 template <int KEYS, int START>

@@ -5,7 +5,7 @@
 //   x_j = q . k_j log2(e)/sqrt(d);  m a running reference of the row's maximum;
 //   l = sum 2^(x_j - m);  o = sum 2^(x_j - m) v_j;  out = o / l;  lse = m ln 2 + ln l.
 // A unit is up to 16 packed rows (token-major, the G heads of a token together)
-// of one KV head.  Bound by HBM: every key and value is read once for a unit, and
+// of one KV head (more rows of a source are more units).  Bound by HBM: every key and value is read once for a unit, and
 // 16 rows are few enough for the warps' own matrix instructions (m16n8, 32 to 96
 // of them per 8 KB), which start on 4 KB of keys where a tcgen05 tile wants 128
 // rows and 32 KB.

@@ -50,14 +50,14 @@ def near(got, want, tol):
 class Sources:
     """mem[b] states of each source and new[s] rows of each of its `group` slots."""
 
-    def __init__(self, mem, new, group, Hq, Hkv, dt=BF16, paged=True, seed=0, pad=0, fill=float("nan"), scale=1.0):
+    def __init__(self, mem, new, group, Hq, Hkv, dt=BF16, paged=True, seed=0, pad=0, fill=float("nan"), scale=1.0, room=0):
         assert len(new) == len(mem) * group
         g = torch.Generator(device=DEV)
         g.manual_seed(seed)
         self.mem, self.new, self.group, self.Hq, self.Hkv, self.dt = mem, new, group, Hq, Hkv, dt
         B, self.T = len(mem), sum(new) + pad
         self.start = np.concatenate([[0], np.cumsum(new)]).tolist()
-        width = pages_of(max(mem + [1])) + 1
+        width = pages_of(max(mem + [1])) + 1 + pages_of(room)
         cap = width * PAGE
         self.q = (torch.randn(max(self.T, 1), Hq, D, generator=g, device=DEV) * scale).to(dt)
         if pad:
@@ -150,6 +150,33 @@ def test_cross(shape, Hq, Hkv, dt, paged):
     # rows of the cache beyond the lengths, and queries of rows that belong to nobody, are NaN
     mem, group, new = SHAPES[shape]
     c = Sources(mem, new, group, Hq, Hkv, dt, paged, seed=shape, pad=shape % 3)
+    c.run()
+    assert c.status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (8, 1), (4, 4)])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_cross_in_a_large_cache(shape, Hq, Hkv, dt, paged):
+    # what fits in the cache, not the lengths, says which kernels run
+    mem, group, new = SHAPES[shape]
+    c = Sources(mem, new, group, Hq, Hkv, dt, paged, seed=shape, pad=shape % 3, room=(1 << 18) // len(mem))
+    c.run()
+    assert c.status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("Hq,Hkv,mem,group,new", [
+    (32, 8, [128] * 4, 1, [16] * 4), (32, 8, [100], 1, [75]), (32, 8, [128], 1, [77]), (8, 1, [2000], 1, [9]), (8, 2, [8100], 4, [1, 2, 9, 4]),
+    (8, 2, [500, 0, 37], 2, [3, 40, 0, 1, 7, 0]), (4, 4, [1], 1, [600]), (4, 4, [1, 1], 1, [300, 308]), (1, 1, [3, 800, 90], 1, [0, 2400, 1]),
+    (2, 2, [1700, 30], 8, [5] * 16), (8, 4, [129, 640, 17], 5, [1] * 15),
+])
+def test_cross_of_more_rows_than_a_block(Hq, Hkv, mem, group, new, dt, paged):
+    c = Sources(mem, new, group, Hq, Hkv, dt, paged, seed=len(new), pad=3)
     c.run()
     assert c.status() == 0
     c.check()
