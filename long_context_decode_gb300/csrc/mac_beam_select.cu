@@ -169,7 +169,12 @@ __device__ __forceinline__ void scan_piece(const SelectParams &p, ScanShared &sm
   constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Row<T> row(p, b);
-  const int i0 = seg * p.steps * kThr + tid;
+  // A thread's place among the vectors of a step.  Where they are too few for twice
+  // n_out groups of eight neighbours, neighbours are in groups of their own (32 beams of
+  // 218 logits, 16 of each 16: 13.3 -> 10.6; of full steps, which they read apart, + 0.5).
+  const bool spread = U == 1 && row.full - seg * kThr < min(16 * p.n_out, kThr);
+  const int turn = spread ? (tid & 7) << 5 | tid >> 3 : tid;
+  const int i0 = seg * p.steps * kThr + turn;
   if (tid == 0) sm.count = sm.n_passed = 0;
 
   Running r;
@@ -183,7 +188,7 @@ __device__ __forceinline__ void scan_piece(const SelectParams &p, ScanShared &sm
     }
   };
   load(cur, 0);
-  const int extra = seg == p.segs - 1 ? row.loose(tid) : -1;  // the last piece takes the row's ends
+  const int extra = seg == p.segs - 1 ? row.loose(turn) : -1;  // the last piece takes the row's ends
   const float loose = extra >= 0 ? elem_f32<T>(row.at, extra) : -INFINITY;
   for (int k = 0; k < p.steps; k += U) {
     if (k + U < p.steps) load(next, k + U);
@@ -232,7 +237,7 @@ __device__ __forceinline__ void scan_piece(const SelectParams &p, ScanShared &sm
   __syncthreads();
   const float least = sm.nth;
   // the threads whose logits may pass, looked through by all of them
-  if (mx >= least && mx > -INFINITY) sm.passed[atomicAdd(&sm.n_passed, 1)] = (uint8_t)tid;
+  if (mx >= least && mx > -INFINITY) sm.passed[atomicAdd(&sm.n_passed, 1)] = (uint8_t)turn;
   __syncthreads();
   auto take = [&](float x, int v) {
     if (x >= least && x > -INFINITY) {
@@ -424,12 +429,15 @@ template <typename T>
 __device__ __forceinline__ void pick(const SelectParams &p, PickShared &sm, int group) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = group * p.n;
   uint32_t status = 0;
-  // The group's keys, the pieces' best ones first, one to a thread in turn; the
+  // The group's keys, the pieces' best ones first, one to a thread in turn (a piece's
+  // own one lane further with every rank: all that count may be of one piece); the
   // first of each are on their way before anything else is waited for.
   const int lists = p.n * p.segs, n_keys = lists * p.n_out;
   const unsigned long long *keys = p.keys + (int64_t)first * p.n_out * p.segs;
   auto key_at = [&](int i, int *beam) {
-    const int rank = (int)((unsigned long long)i * p.lists_inv >> 40), list = i - rank * lists;
+    const int rank = (int)((unsigned long long)i * p.lists_inv >> 40), turns = (int)((unsigned long long)rank * p.lists_inv >> 40);
+    int list = i - rank * lists - (rank - turns * lists);
+    if (list < 0) list += lists;
     *beam = (int)((unsigned long long)list * p.segs_inv >> 40);
     return keys + (int64_t)(*beam * p.n_out + rank) * p.segs + list - *beam * p.segs;
   };

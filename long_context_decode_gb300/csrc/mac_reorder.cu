@@ -365,6 +365,8 @@ cudaError_t launch(const ReorderParams &p, cudaStream_t s) {
 // its launch and three trips to memory.  Beams opened on two prompts (8 slots of
 // 8 / 2 fp32 heads, 119 MB read and written): 15.6 us from L2, 19.9 from HBM.  With
 // four CTAs per SM, and so 64 registers, they took 5.9 and 22.6, with three 4.4 and 15.6.
+// Groups of two slots have less on its way per thread, and room for four CTAs: 16 of
+// 418 positions at most, 128 in the ring, copied whole (110 MB) 30.5 where two CTAs take 48.7.
 constexpr int kStateThr = 256;
 
 struct StateShared {
@@ -559,6 +561,7 @@ cudaError_t launch_reorder(const ReorderParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_state(const StateParams &p, int sms, cudaStream_t s) {
+  if (p.n <= 2) return launch_dependent(state_kernel<2, 4>, sms * 4, kStateThr, 0, s, p);
   if (p.n <= 4) return launch_dependent(state_kernel<4, 2>, sms * 2, kStateThr, 0, s, p);
   return p.n <= 8 ? launch_dependent(state_kernel<8, 2>, sms * 2, kStateThr, 0, s, p) : launch_dependent(state_kernel<16, 1>, sms, kStateThr, 0, s, p);
 }

@@ -589,7 +589,7 @@ class Layer:
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
-@pytest.mark.parametrize("groups,n,Hq,Hkv,K", [(2, 4, 8, 2, 32), (1, 2, 1, 1, 7), (3, 5, 4, 4, 50), (1, 16, 8, 1, 64), (2, 8, 2, 1, 16)])
+@pytest.mark.parametrize("groups,n,Hq,Hkv,K", [(2, 4, 8, 2, 32), (1, 2, 1, 1, 7), (3, 5, 4, 4, 50), (1, 16, 8, 1, 64), (2, 8, 2, 1, 16), (20, 2, 8, 4, 24)])
 def test_reorder_state(groups, n, Hq, Hkv, K, dt):
     """After every step a slot holds what a copy of its parent's whole state would hold."""
     cap = 96
