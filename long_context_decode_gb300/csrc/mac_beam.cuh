@@ -16,7 +16,7 @@ constexpr int kScanThreads = 256, kMaxPieces = 64;
 struct SelectParams {
   int S, n, V, n_out, placed, end;
   int steps, segs;                // of a piece; pieces of a row
-  unsigned long long lists_inv, segs_inv;  // 2^40 / (n segs) and / segs, rounded up: i times it, shifted, is the quotient
+  unsigned long long beam_inv;     // 2^40 / (n_out segs), rounded up: i times it, shifted, is the quotient
   int64_t stride;                 // elements between rows
   const void *logits;
   const float *scores;            // [S]

@@ -396,16 +396,13 @@ static_assert(kMaxVocab == 1 << 20 && kMaxBeams <= 1 << 11, "a place in 32 bits"
 __device__ __forceinline__ bool before(const Pick &x, const Pick &y) { return x.s > y.s || (x.s == y.s && x.at < y.at); }
 
 // A load that is issued where it stands (the compiler moves others to their use).
-__device__ __forceinline__ unsigned long long load_now(const unsigned long long *at) {
-  unsigned long long v;
-  asm volatile("ld.global.cg.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
-  return v;
-}
 __device__ __forceinline__ float2 load_now(const float2 *at) {
   float2 v;
   asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(at) : "memory");
   return v;
 }
+
+constexpr int kHeld = 2048;  // keys of a group that are held
 
 struct PickShared {
   double base[kMaxBeams];                   // c - L + its largest logit; of a finished beam c
@@ -417,6 +414,7 @@ struct PickShared {
   __align__(16) float gmax[32];
   double wsum[kWarps];
   Pick room[kRoom];
+  __align__(16) unsigned long long keys[kHeld + 2];  // the group's, from the 16-byte boundary before them
   Pick best[kMaxPicks], wbest[kWarps];
   uint16_t sorted[kRoom];                   // places in `room`, best first
   Precise precise;
@@ -429,23 +427,13 @@ template <typename T>
 __device__ __forceinline__ void pick(const SelectParams &p, PickShared &sm, int group) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = group * p.n;
   uint32_t status = 0;
-  // The group's keys, the pieces' best ones first, one to a thread in turn (a piece's
-  // own one lane further with every rank: all that count may be of one piece); the
-  // first of each are on their way before anything else is waited for.
-  const int lists = p.n * p.segs, n_keys = lists * p.n_out;
-  const unsigned long long *keys = p.keys + (int64_t)first * p.n_out * p.segs;
-  auto key_at = [&](int i, int *beam) {
-    const int rank = (int)((unsigned long long)i * p.lists_inv >> 40), turns = (int)((unsigned long long)rank * p.lists_inv >> 40);
-    int list = i - rank * lists - (rank - turns * lists);
-    if (list < 0) list += lists;
-    *beam = (int)((unsigned long long)list * p.segs_inv >> 40);
-    return keys + (int64_t)(*beam * p.n_out + rank) * p.segs + list - *beam * p.segs;
-  };
-  unsigned long long early[2] = {0, 0};
-  int early_beam[2] = {0, 0};
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    if (tid + q * kThr < n_keys) early[q] = load_now(key_at(tid + q * kThr, &early_beam[q]));
+  // The group's keys lie end to end.  They are on their way before anything else is
+  // waited for, past L1, which may hold what they were when a neighbour was read.
+  const int per_beam = p.n_out * p.segs, n_keys = p.n * per_beam;
+  const unsigned long long *keys = p.keys + (int64_t)first * per_beam;
+  const int odd = (int)((uintptr_t)keys >> 3 & 1);
+  for (int i = 2 * tid - odd; i < min(n_keys, kHeld); i += 2 * kThr)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(sm.keys + odd + i)), "l"(keys + i) : "memory");
   for (int j = warp; j < p.n; j += kWarps) {
     const float2 *ml = p.ml + (int64_t)(first + j) * p.segs;
     // whatever it is worth: no wait for the score
@@ -485,23 +473,19 @@ __device__ __forceinline__ void pick(const SelectParams &p, PickShared &sm, int 
       sm.top[j] = m;
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   // f(beam, key) of this thread's candidates; a finished beam's key is that of its
-  // end.  (A loop that is not unrolled: what a choice waits for is code that has
-  // not been fetched yet.)
+  // end.  Lanes are turned by 5 with every 32 keys, so that neither the best of all
+  // pieces nor all of one piece meet in few of them.  (A loop that is not unrolled:
+  // what a choice waits for is code that has not been fetched yet.)
   auto candidates = [&](auto f) {
-    int beam = early_beam[0];
-    unsigned long long k = early[0];
 #pragma unroll 1
-    for (int i = tid;;) {
+    for (int i = tid; (i & ~31) < n_keys; i += kThr) {
+      const int at = (i & ~31) | ((i + 5 * (i >> 5)) & 31);
+      if (at >= n_keys) continue;
+      const unsigned long long k = at < kHeld ? sm.keys[odd + at] : __ldcg(keys + at);
+      const int beam = (int)((unsigned long long)at * p.beam_inv >> 40);
       if (k != 0 && sm.kind[beam] == 1) f(beam, k);
-      i += kThr;
-      if (i >= n_keys) break;
-      if (i < 2 * kThr) {
-        k = early[1];
-        beam = early_beam[1];
-      } else {
-        k = __ldcg(key_at(i, &beam));
-      }
     }
     if (tid < p.n && sm.kind[tid] == 2) f(tid, 1ull);
   };

@@ -880,8 +880,7 @@ int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const
   const int steps = select_steps(vocab, es);
   p.steps = (steps + select_pieces(p.S, vocab, es, sms) - 1) / select_pieces(p.S, vocab, es, sms);
   p.segs = (steps + p.steps - 1) / p.steps;
-  p.lists_inv = ((1ull << 40) - 1) / ((unsigned long long)p.segs * n_beams) + 1;
-  p.segs_inv = ((1ull << 40) - 1) / p.segs + 1;
+  p.beam_inv = ((1ull << 40) - 1) / ((unsigned long long)p.segs * n_out) + 1;
   const SelectLayout L = select_layout(cfg, vocab, n_out);
   uint8_t *ws = (uint8_t *)beam_ws;
   p.status = (uint32_t *)(ws + L.ctl);
