@@ -20,15 +20,16 @@
 // beams in question are summed again to 2^-38 and the candidates ranked anew.
 // So the choice is that of the exact scores, however the card adds.
 //
-// In a graph (us; floor: bytes at 6.7 TB/s): 4 beams of 32000 bf16 logits 8.0 (0.04);
-// 64 of 128000 11.6 from L2, 12.9 from HBM (2.4); 256 of 50001 fp32 logits, 16 of
-// each 8 beams, 16.6 and 22.0 (7.6).  Bound by barriers and by code that is fetched
-// for the first time (about 3 us of a scan, 4 of a choice), then by the scan's CTAs,
-// which end together: their thresholds and rankings overlap nothing.  Four CTAs per
-// SM aimed at: with three 11.7 and 20.1, with five 13.5 and 16.6 of 11.6 and 16.6.
-// With the choice a kernel of its own, whose CTAs start ahead, a graph takes 7.9,
-// 10.3 and 17.0, but calls from Python one after another 14.2, 15.8 and 22.0 where
-// this takes 11.0, 11.9 and 21.5.  A beam summed again takes its group's CTA 12 us
+// In a graph (us; floor: bytes at 6.7 TB/s): 4 beams of 32000 bf16 logits 6.7 (0.04);
+// 64 of 128000 9.4 from L2, 10.9 from HBM (2.4); 256 of 50001 fp32 logits, 16 of
+// each 8 beams, 13.4 and 16.5 (7.6).  Bound by barriers, trips to L2 and code that is
+// fetched for the first time (about 3 us of a scan, 3.5 of a choice), then by the
+// scan's CTAs, which end together: their thresholds and rankings overlap nothing.
+// All CTAs run at once, four to an SM at most: with a fifth as many again 12.2 and
+// 14.8 of 9.4 and 13.4, with three per SM 9.4 and 13.2, with two 11.3 and 13.3.  With
+// the choice a kernel of its own, whose CTAs start ahead, 7.0, 9.6 and 15.8 where this
+// took 6.8, 9.4 and 14.9, and 13.8, 15.8 and 20.8 where this took 11.1, 13.0 and 19.4 of
+// calls one after another from Python.  A beam summed again takes its group's CTA 12 us
 // of 32000 logits, 65 of 128000 (instructions: some 100 for each logit).
 #include <cuda_bf16.h>
 #include <math.h>

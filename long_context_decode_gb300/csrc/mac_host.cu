@@ -296,14 +296,16 @@ int check_select(const mac_config *c, int32_t n_beams, int32_t vocab, int32_t n_
 }
 
 // Steps of 16 bytes per thread that a row of the selection takes, and its
-// pieces where a card of `sms` SMs is to have four CTAs on each.
+// pieces where a card of `sms` SMs has at most four CTAs on each, so that all
+// run at once.
 int select_steps(int vocab, int es) {
   const int per = kScanThreads * (16 / es);
   return (vocab + per - 1) / per;
 }
 int select_pieces(int rows, int vocab, int es, int sms) {
   const int steps = select_steps(vocab, es);
-  int pieces = (4 * sms + rows - 1) / rows;
+  int pieces = 4 * sms / rows;
+  if (pieces < 1) pieces = 1;
   if (pieces > kMaxPieces) pieces = kMaxPieces;
   return pieces < steps ? pieces : steps;
 }
