@@ -62,6 +62,11 @@ struct Piece {
   __device__ bool cut() const { return t1 - t0 < tiles; }
 };
 
+// A cut unit: its pieces' CTAs, its rows.
+struct Cut {
+  int c0, n, tok0, g, n_rows;
+};
+
 template <typename T>
 struct Shared {
   static constexpr bool kF32 = sizeof(T) == 4;
@@ -69,6 +74,8 @@ struct Shared {
   float q[kF32 ? 2 : 1][kF32 ? kRows * kQStride : 4];  // fp32: the queries' parts (bf16's stay in registers)
   float2 ml[kWarps][kRows];
   Piece pieces[kWarps][4];
+  int2 ctas[kWarps];     // that hold the first and last tile of a cut unit
+  Cut cut[2];            // the units of this CTA's first and last piece
   uint32_t arrived[2];   // pieces of a cut unit that were done before this CTA's
 };
 
@@ -134,7 +141,7 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 // A source, as the plan sees it.
 struct Source {
   int row0, n, keys;   // first row, rows (0: nothing to attend), states
-  int units, tiles;    // of all its KV heads; key tiles
+  int blocks, tiles;   // units of a KV head; key tiles
   bool odd;            // rows that are not attended: bad lengths, or no states
 };
 
@@ -142,7 +149,7 @@ struct Source {
 template <typename C>
 struct Walk {
   static constexpr int START = C::kStart, TILE = C::kTile;
-  int lt;              // log2 of the tokens of a unit
+  int lg, lt;          // log2 of the heads of a KV head, and of the tokens of a unit
   int b, k;            // source, unit (KV head by head, in each its rows' blocks)
   Source src;
   bool whole, odd;     // a unit per CTA; some source is odd
@@ -156,7 +163,7 @@ struct Walk {
     s.keys = m;
     s.odd = !in || (r1 > r0 && (m < 1 || m > p.max_len));
     s.n = s.odd ? 0 : r1 - r0;
-    s.units = ((s.n + (1 << lt) - 1) >> lt) * p.Hkv;
+    s.blocks = (s.n + (1 << lt) - 1) >> lt;
     s.tiles = (int)(((long long)m + C::kKeys - 1) / C::kKeys);
     return s;
   }
@@ -165,7 +172,8 @@ struct Walk {
   // false: nothing to do
   __device__ bool start(const ChunkParams &p) {
     const int lane = threadIdx.x & 31;
-    lt = log2i(C::kRows) - (31 - __clz(p.G));
+    lg = 31 - __clz(p.G);
+    lt = log2i(C::kRows) - lg;
     long long total = 0;
     int units = 0, top = 0;  // 2^24 and 2^28 at most
     odd = false;
@@ -174,9 +182,9 @@ struct Walk {
       mine = {};
       if (b0 + lane < p.B) mine = source(p, b0 + lane);
       odd |= mine.odd;
-      if (mine.units) {
-        total += (long long)mine.units * cost(mine);
-        units += mine.units;
+      if (mine.blocks) {
+        total += (long long)mine.blocks * p.Hkv * cost(mine);
+        units += mine.blocks * p.Hkv;
         top = max(top, cost(mine));
       }
     }
@@ -197,7 +205,7 @@ struct Walk {
         mine = {};
         if (b0 + lane < p.B) mine = source(p, b0 + lane);
       }
-      const long long v = whole ? mine.units : mine.units ? (long long)mine.units * cost(mine) : 0;
+      const long long v = whole ? mine.blocks * p.Hkv : mine.blocks ? (long long)mine.blocks * p.Hkv * cost(mine) : 0;
       long long sum = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -214,7 +222,7 @@ struct Walk {
       src.row0 = __shfl_sync(0xffffffffu, mine.row0, hit);
       src.n = __shfl_sync(0xffffffffu, mine.n, hit);
       src.keys = __shfl_sync(0xffffffffu, mine.keys, hit);
-      src.units = __shfl_sync(0xffffffffu, mine.units, hit);
+      src.blocks = __shfl_sync(0xffffffffu, mine.blocks, hit);
       src.tiles = __shfl_sync(0xffffffffu, mine.tiles, hit);
       before += __shfl_sync(0xffffffffu, sum - v, hit);
       found = true;
@@ -241,9 +249,9 @@ struct Walk {
         if (end <= last) t1 = end > first ? (int)((end - first + TILE - 1) / TILE) : 0;
         at = x = last + TILE;
       }
-      const int blocks = src.units / p.Hkv, g = k / blocks, i = k - g * blocks;
+      const int g = src.blocks == 1 ? k : k / src.blocks, i = k - g * src.blocks;
       const Piece q = {b, g, src.row0 + (i << lt), min(1 << lt, src.n - (i << lt)), src.keys, t0, t1, src.tiles, first};
-      if (++k == src.units && x < end) {
+      if (++k == src.blocks * p.Hkv && x < end) {
         k = 0;
         do {
           if (++b == p.B) {  // (nor this)
@@ -251,7 +259,7 @@ struct Walk {
             break;
           }
           src = source(p, b);
-        } while (src.units == 0);
+        } while (src.blocks == 0);
       }
       if (t0 < t1) return q;
     }
@@ -275,10 +283,10 @@ __device__ __forceinline__ void add_state(float4 &x, float4 &y, float &sum, floa
   y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
 }
 
-// Row `at` of a unit: 4 columns from 4 col and 64 + 4 col on.
+// Row `at` of a unit that starts at tok0, of KV head g: 4 columns from 4 col and 64 + 4 col on.
 template <typename T>
-__device__ __forceinline__ void write_row(const ChunkParams &p, const Piece &q, int at, int col, float4 x, float4 y, float m, float l) {
-  const int64_t to = (int64_t)(q.tok0 + at / p.G) * p.Hq + q.g * p.G + at % p.G;
+__device__ __forceinline__ void write_row(const ChunkParams &p, int tok0, int g, int lg, int at, int col, float4 x, float4 y, float m, float l) {
+  const int64_t to = (int64_t)(tok0 + (at >> lg)) * p.Hq + (g << lg) + (at & ((1 << lg) - 1));
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T *dst = (T *)p.out + to * kHeadDim + col * 4;
   store_out(dst, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
@@ -319,8 +327,8 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
   uint32_t qa[F32 ? 1 : 8][4];
   float4 fresh[F32 ? kRows * kHeadDim / 4 / kThr : 1];
   auto load_q = [&](const Piece &q) {
-    const int n_rows = q.n_tok * p.G;
-    auto q_row = [&](int r) { return (const T *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim; };
+    const int n_rows = q.n_tok << walk.lg, G1 = (1 << walk.lg) - 1;
+    auto q_row = [&](int r) { return (const T *)p.q + ((int64_t)(q.tok0 + (r >> walk.lg)) * p.Hq + (q.g << walk.lg) + (r & G1)) * kHeadDim; };
     if constexpr (F32) {
 #pragma unroll
       for (int i = 0; i < kRows * kHeadDim / 4 / kThr; ++i) {
@@ -433,12 +441,12 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
   const uint32_t of_v = place<uint16_t>(lane & 15, lane >> 4, true);
   int4 note = make_int4(0, 0, 0, 0);
   int stage = 0;
-  Piece cut[2];        // the cut units of this CTA's first and last piece
   int n_cut = 0;
 #pragma unroll 1
   for (int number = 0;; ++number) {
     const Piece q = sm.pieces[warp][number & 3];
     if (q.t1 <= q.t0) break;
+    if (q.cut() && lane == 0) sm.ctas[warp] = make_int2(walk.first_cta(q), walk.last_cta(q));  // while keys are on their way
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -599,9 +607,10 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     const Piece after = sm.pieces[warp][number + 1 & 3];
     if (after.t1 > after.t0) load_q(after);  // on its way meanwhile
     const int last = stage == 0 ? kStages - 1 : stage - 1;  // the stage that has been read
-    const int n_rows = q.n_tok * p.G, c = blockIdx.x;
+    const int n_rows = q.n_tok << walk.lg, c = blockIdx.x;
     const bool whole = !q.cut();
-    const int c0 = whole ? 0 : walk.first_cta(q);
+    const int2 ctas = sm.ctas[warp];
+    const int c0 = ctas.x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -647,7 +656,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
         add_state(x, y, sum, ex2(ml[w].x - ref), u, v, ml[w].y);
       }
       if (whole) {
-        write_row<T>(p, q, row, col, x, y, big, sum);
+        write_row<T>(p, q.tok0, q.g, walk.lg, row, col, x, y, big, sum);
       } else {
         float *dst = p.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.part_rows + row) * kChunkStride;
         *reinterpret_cast<float4 *>(dst + col * 4) = x;
@@ -658,10 +667,12 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     __syncthreads();  // the stages are free again, the partials written
     put_q();
     if (whole) continue;
-    if (c == c0) note = make_int4(q.tok0, q.g, n_rows, walk.last_cta(q));
+    if (c == c0) note = make_int4(q.tok0, q.g, n_rows, ctas.y);
     if (p.counts) {
-      cut[n_cut] = q;
-      if (tid == 0) sm.arrived[n_cut] = arrive(p.counts + c0);
+      if (tid == 0) {
+        sm.cut[n_cut] = Cut{c0, ctas.y - c0 + 1, q.tok0, q.g, n_rows};
+        sm.arrived[n_cut] = arrive(p.counts + c0);
+      }
       ++n_cut;
     }
   }
@@ -675,12 +686,12 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < n_cut; ++i) {
-    const Piece q = i ? cut[1] : cut[0];
-    const int c0 = walk.first_cta(q), n = walk.last_cta(q) - c0 + 1, n_rows = q.n_tok * p.G;
+    const Cut q = sm.cut[i];
+    const int c0 = q.c0, n = q.n;
     if (sm.arrived[i] + 1 != (uint32_t)n) continue;
     if (tid == 0) p.counts[c0] = 0;  // for the next call
     const int row = tid >> 4, col = tid & 15;
-    if (row >= n_rows) continue;
+    if (row >= q.n_rows) continue;
     float big = -INFINITY, sum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 1
@@ -709,7 +720,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) add_state(x, y, sum, ex2(ml[j].x - ref), u[j], v[j], ml[j].y);
     }
-    write_row<T>(p, q, row, col, x, y, big, sum);
+    write_row<T>(p, q.tok0, q.g, walk.lg, row, col, x, y, big, sum);
   }
 }
 
