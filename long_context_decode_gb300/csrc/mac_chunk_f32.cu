@@ -191,7 +191,8 @@ __device__ __forceinline__ float4 load_if(const float *src, bool ok) {
 
 template <bool PAGED, bool CROSS>
 __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, uint8_t *vbuf, Control *ct) {
-  const int lane = threadIdx.x & 31, me_q = (threadIdx.x >> 5) - 4, me = me_q & (kConv - 1);
+  const int lane = threadIdx.x & 31, me_q = (threadIdx.x >> 5) - 4, me = me_q & (kConv - 1), lg = 31 - __clz(p.G);
+  static_assert(kRows == 2 * kConv * kPage, "a warp's rows of Q are as many as of a tile");
   const bool is_k = me_q < kConv;  // one copy of the code for both: see above
   const float *src = (const float *)(is_k ? p.kv.k : p.kv.v) + lane * 4;
   unsigned long long *full = is_k ? &ct->k_full : &ct->v_full, *free = is_k ? &ct->k_free : &ct->v_free;
@@ -221,18 +222,25 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
 #pragma unroll
       for (int i = 0; i < kPage; ++i) f[i] = load_if(row + i * kHeadDim, i < n);
     };
-    load(q.t0, at(q.t0));
+    // Q first, all of a warp's rows on their way at once (two at a time took 5 us of
+    // a piece of 128 rows), then the first keys (values)
+#pragma unroll
+    for (int i = 0; i < kPage; ++i) {
+      const int r = me_q + i * 2 * kConv;
+      f[i] = load_if((const float *)p.q + ((int64_t)(q.tok0 + (r >> lg)) * p.Hq + (q.g << lg) + (r & (p.G - 1))) * kHeadDim + lane * 4, r < n_rows);
+    }
     if (wait(&ct->q_free, (nq + 1) & 1)) {
       ++nq;
-#pragma unroll 2
-      for (int r = me_q; r < kRows; r += 2 * kConv) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n_rows)
-          x = *reinterpret_cast<const float4 *>((const float *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim + lane * 4);
-        put_parts<kRows>(qbuf, r, lane, x);
+#pragma unroll 1
+      for (int c = 0; c < kPage; c += kPage / 2) {
+#pragma unroll
+        for (int i = 0; i < kPage / 2; ++i) put_parts<kRows>(qbuf, me_q + (c + i) * 2 * kConv, lane, f[i]);
+#pragma unroll
+        for (int i = 0; i < kPage / 2; ++i) f[i] = f[i + kPage / 2];
       }
       hand_over(&ct->q_full);
     }
+    load(q.t0, at(q.t0));
     int64_t next = at(q.t0 + 1);  // a tile ahead of its use
     for (int t = q.t0; t < q.t1; ++t, ++nt) {
       if (wait(free, (nt + 1) & 1)) {
