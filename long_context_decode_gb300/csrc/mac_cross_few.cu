@@ -71,7 +71,8 @@ template <typename T>
 struct Shared {
   static constexpr bool kF32 = sizeof(T) == 4;
   uint8_t stage[kWarps][kStages][kStep];
-  float q[kF32 ? 2 : 1][kF32 ? kRows * kQStride : 4];  // fp32: the queries' parts (bf16's stay in registers)
+  float q[kF32 ? 2 : 1][kF32 ? kRows * kQStride : 4];  // fp32: the queries' parts
+  __align__(256) uint8_t qb[kF32 ? 1 : 4][kF32 ? 16 : kRows * kHeadDim * 2];  // bf16: the queries of four pieces, on their way to registers (their swizzle is an exclusive or of the address)
   float2 ml[kWarps][kRows];
   Piece pieces[kWarps][4];
   int2 ctas[kWarps];     // that hold the first and last tile of a cut unit
@@ -321,30 +322,39 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     __syncwarp();
   };
 
-  // ---- queries: bf16 as the products' operands; fp32 by way of registers into
-  // shared memory, which a piece's end must leave first
+  // ---- queries: bf16 by way of shared memory, with the copies of their piece's
+  // first step, into registers as the products' operands (read straight into
+  // registers by every warp they took up to 1 us of a piece); fp32 by way of
+  // registers into shared memory, which a piece's end must leave first
   constexpr int UNITS = kHeadDim * (int)sizeof(T) / 16;  // 16-byte parts of a row
   uint32_t qa[F32 ? 1 : 8][4];
   float4 fresh[F32 ? kRows * kHeadDim / 4 / kThr : 1];
+  auto q_row = [&](const Piece &q, int r) {
+    return (const T *)p.q + ((int64_t)(q.tok0 + (r >> walk.lg)) * p.Hq + (q.g << walk.lg) + (r & ((1 << walk.lg) - 1))) * kHeadDim;
+  };
   auto load_q = [&](const Piece &q) {
-    const int n_rows = q.n_tok << walk.lg, G1 = (1 << walk.lg) - 1;
-    auto q_row = [&](int r) { return (const T *)p.q + ((int64_t)(q.tok0 + (r >> walk.lg)) * p.Hq + (q.g << walk.lg) + (r & G1)) * kHeadDim; };
     if constexpr (F32) {
+      const int n_rows = q.n_tok << walk.lg;
 #pragma unroll
       for (int i = 0; i < kRows * kHeadDim / 4 / kThr; ++i) {
         const int e = i * kThr + tid, r = e / UNITS;
-        fresh[i] = r < n_rows ? *reinterpret_cast<const float4 *>(q_row(r) + e % UNITS * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        fresh[i] = r < n_rows ? *reinterpret_cast<const float4 *>(q_row(q, r) + e % UNITS * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-    } else {
+    }
+  };
+  // bf16: a thread copies 16 bytes; rows that are not there are the last one
+  auto copy_q = [&](const Piece &q, int number) {
+    if constexpr (!F32) {
+      static_assert(kRows * UNITS == kThr, "a part for each thread");
+      const int r = tid >> 4, c = tid & 15;
+      copy16(smem_addr(sm.qb[number & 3]) + place<T>(r, c, false), q_row(q, min(r, (q.n_tok << walk.lg) - 1)) + c * 8);
+    }
+  };
+  auto take_q = [&](int number) {
+    if constexpr (!F32) {
+      const uint32_t at = smem_addr(sm.qb[number & 3]) + place<T>(lane & 15, lane >> 4, false);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(q_row(min(h * 8 + g, n_rows - 1))) + t;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          qa[c][h] = src[c * 8];
-          qa[c][h + 2] = src[c * 8 + 4];
-        }
-      }
+      for (int c = 0; c < 8; ++c) ldm4(qa[c], (at ^ (c & 3) << 5) + (c >> 2) * 128);
     }
   };
   auto put_q = [&] {
@@ -383,6 +393,7 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
     walk_on();
     in = sm.pieces[warp][known - 1 & 3];
     in_tile = in.t0;
+    if (in.t1 > in.t0) copy_q(in, known - 1);  // (four places: the copies are at most three pieces ahead)
   };
   enter();
   if (in.t1 <= in.t0) {  // a span behind the last tile, or before the next unit's first
@@ -434,6 +445,11 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
 #pragma unroll 1
   for (int i = 0; i < AHEAD; ++i) issue();
   put_q();
+  if constexpr (!F32) {
+    copies_wait<AHEAD - 1>();
+    __syncthreads();
+    take_q(0);
+  }
 
   const float scale = p.q_scale, lazy = 8.f / scale;
   // a lane's rows of the bf16 operands; two 16-byte parts further on are an exclusive or away
@@ -664,8 +680,10 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
         if (col == 0) *reinterpret_cast<float2 *>(dst + kHeadDim) = make_float2(big, sum);
       }
     }
+    if constexpr (!F32) copies_wait<AHEAD - 1>();  // the next piece's queries
     __syncthreads();  // the stages are free again, the partials written
     put_q();
+    if (after.t1 > after.t0) take_q(number + 1);
     if (whole) continue;
     if (c == c0) note = make_int4(q.tok0, q.g, n_rows, ctas.y);
     if (p.counts) {
