@@ -95,8 +95,8 @@ struct CrossF32 : ChunkF32 {
 };
 // The same for few rows per source (mac_cross_few.cu), in quarters of a tile's
 // 64 KB of keys and values, 1.4 us at an SM's share of HBM.
-// Against the kernels above (us): one row over 57 keys 4.6 and 7.8; 16 rows of 16
-// sources of 400 to 1500 keys 15.9 and 18.3; in fp32 16 rows over 4 x 32768 196 and
+// Against the kernels above (us): one row over 57 keys 4.4 and 7.8; 16 rows of 16
+// sources of 400 to 1500 keys 14.4 and 18.3; in fp32 16 rows over 4 x 32768 196 and
 // 308.  With two row tiles of 16 it was no faster than they are: 20 rows of 4 sources
 // of 8192 to 32768 keys 56.8 and 53.4, 32 in fp32 over 4 x 32768 357 and 308.
 constexpr int kFewRows = 16;          // most rows of a source, on average

@@ -28,7 +28,7 @@
 // S of the next tile is made while the softmax runs; K is stored while the
 // products of the last weights run, V while the scores do.
 //
-// 4096 tokens, 8 heads of 2 KV heads: 193 to 217 us, 158 to 178 TFLOP/s of fp32
+// 4096 tokens, 8 heads of 2 KV heads: 178 to 183 us, 188 to 193 TFLOP/s of fp32
 // products (multiply-adds on the CUDA cores: 945 us).  A tile takes 7200 cycles
 // whatever its rows, so single tokens are bound by splitting and products, not
 // by HBM: four of 32 / 8 heads at 8192 take 95 us (2.8 TB/s).  Of a tile, its 72

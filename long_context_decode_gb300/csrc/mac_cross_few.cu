@@ -5,10 +5,10 @@
 //   x_j = q . k_j log2(e)/sqrt(d);  m a running reference of the row's maximum;
 //   l = sum 2^(x_j - m);  o = sum 2^(x_j - m) v_j;  out = o / l;  lse = m ln 2 + ln l.
 // A unit is up to 16 packed rows (token-major, the G heads of a token together)
-// of one KV head (more rows of a source are more units).  Bound by HBM: every key and value is read once for a unit, and
-// 16 rows are few enough for the warps' own matrix instructions (m16n8, 32 to 96
-// of them per 8 KB), which start on 4 KB of keys where a tcgen05 tile wants 128
-// rows and 32 KB.
+// of one KV head (more rows of a source are more units).  Bound by HBM: every key
+// and value is read once for a unit, and 16 rows are few enough for the warps' own
+// matrix instructions (m16n8, 32 to 96 of them per 8 KB), which start on 4 KB of
+// keys where a tcgen05 tile wants 128 rows and 32 KB.
 //
 // One CTA per SM, eight warps.  Within a key tile a warp has keys of its own,
 // copies them into stages of its own and keeps maximum, sum and output of its
@@ -30,11 +30,11 @@
 // 2^-20 of its size (2^-24 on average).
 //
 // In a graph (us; floor: bytes at 6.7 TB/s): 16 rows of each of 4 sources of 32768
-// keys, 32 / 8 heads, 86.3 (80.1; 6.2 TB/s), in fp32 196 (160); 64 rows over 16
-// sources of 1024 keys 10.2 from L2, 15.2 from HBM (10.2); of 400 to 1500 keys, cut,
-// 16.6 and 19.7 (9.6); one row over 57 keys 4.6.  What is left over the floor
-// is the start (4.5 us until the first keys are there) and, of cut units, join,
-// count and output behind the last key (3 us).
+// keys, 32 / 8 heads, 84.5 (80.1; 6.4 TB/s), in fp32 196 (160); 64 rows over 16
+// sources of 1024 keys 10.8 from L2, 15.2 from HBM (10.2); of 400 to 1500 keys, cut,
+// 14.6 and 18.3 (9.6); one row over 57 keys 4.4.  What is left over the floor is the
+// start (3.5 us until the first keys are there), some 2.5 us of every further piece of
+// a CTA and, of cut units, join, count and output behind the last key (3 us).
 #include <math.h>
 
 #include "mac_tc.cuh"
@@ -72,7 +72,8 @@ struct Shared {
   static constexpr bool kF32 = sizeof(T) == 4;
   uint8_t stage[kWarps][kStages][kStep];
   float q[kF32 ? 2 : 1][kF32 ? kRows * kQStride : 4];  // fp32: the queries' parts
-  __align__(256) uint8_t qb[kF32 ? 1 : 4][kF32 ? 16 : kRows * kHeadDim * 2];  // bf16: the queries of four pieces, on their way to registers (their swizzle is an exclusive or of the address)
+  // bf16: the queries of four pieces, on their way to registers (their swizzle is an exclusive or of the address)
+  __align__(256) uint8_t qb[kF32 ? 1 : 4][kF32 ? 16 : kRows * kHeadDim * 2];
   float2 ml[kWarps][kRows];
   Piece pieces[kWarps][4];
   int2 ctas[kWarps];     // that hold the first and last tile of a cut unit
