@@ -361,12 +361,13 @@ cudaError_t launch(const ReorderParams &p, cudaStream_t s) {
 // slots may change places.  A warp takes an entry of a head (its query and
 // summary) or a row of a KV head (key and value).  Only positions that a slot
 // does not share with its parent are moved.
-// A step (32 slots, 12 positions apart at most, 32 / 8 bf16 heads, paged): 3.8 us,
+// A step (32 slots, 12 positions apart at most, 32 / 8 bf16 heads, paged): 3.5 us,
 // its launch and three trips to memory.  Beams opened on two prompts (8 slots of
-// 8 / 2 fp32 heads, 119 MB read and written): 15.6 us from L2, 19.9 from HBM.  With
-// four CTAs per SM, and so 64 registers, they took 5.9 and 22.6, with three 4.4 and 15.6.
-// Groups of two slots have less on its way per thread, and room for four CTAs: 16 of
-// 418 positions at most, 128 in the ring, copied whole (110 MB) 30.5 where two CTAs take 48.7.
+// 8 / 2 fp32 heads, 119 MB read and written): 14.8 us from L2, 19.8 from HBM.  With
+// four CTAs per SM, and so 64 registers, they took 5.9 and 22.6 of 3.8 and 15.6, with
+// three 4.4 and 15.6.  Groups of two slots have less on its way per thread, and room
+// for four CTAs: 16 of 418 positions at most, 128 in the ring, copied whole (110 MB)
+// 29.2, 48.7 with two.
 constexpr int kStateThr = 256;
 
 struct StateShared {
@@ -421,9 +422,9 @@ __global__ void __launch_bounds__(kStateThr, CTAS) state_kernel(const __grid_con
     if (by_slot) sm.rows[s + 1] = rows;
   }
   if (status && blockIdx.x == 0) set_status(p.status, status);
+  if (t == 0) sm.rings[0] = sm.rows[0] = 0;
   __syncthreads();
   // positions and rows of every group (paged: rows of every slot)
-  long long sum[2] = {0, 0};
   for (int g0 = 0; g0 < (by_slot ? p.S : groups); g0 += kStateThr) {
     const int g = g0 + t;
     long long v[2] = {0, 0};
@@ -458,20 +459,15 @@ __global__ void __launch_bounds__(kStateThr, CTAS) state_kernel(const __grid_con
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      long long add = sum[i];
-#pragma unroll
-      for (int w = 0; w < kStateThr / 32; ++w) {
-        if (w < warp) add += sm.tot[i][w];
-        sum[i] += sm.tot[i][w];
-      }
       long long *to = i ? sm.rows : sm.rings;
-      if (g < (i && by_slot ? p.S : groups)) to[g + 1] = v[i] + add;
+      if (g >= (i && by_slot ? p.S : groups)) continue;
+      long long before = to[g0];
+      for (int w = 0; w < warp; ++w) before += sm.tot[i][w];
+      to[g + 1] = before + v[i];
     }
     __syncthreads();
   }
-  if (t == 0) sm.rings[0] = sm.rows[0] = 0;
-  __syncthreads();
-  const long long n_rings = sum[0] * p.Hq, n_rows = sum[1] * p.Hkv;
+  const long long n_rings = sm.rings[groups] * p.Hq, n_rows = sm.rows[by_slot ? p.S : groups] * p.Hkv;
   auto find = [](const long long *start, int count, long long x) {
     int lo = 0, hi = count;
     while (hi - lo > 1) {
@@ -489,7 +485,8 @@ __global__ void __launch_bounds__(kStateThr, CTAS) state_kernel(const __grid_con
       const int pos = sm.ring_first[g] + (int)(line - sm.rings[g]), c = pos % p.K;
       // slots that take this entry, and from whom
       const int4 m = lane < n ? sm.move[base + lane] : make_int4(-1, 0, 0, 0);
-      const uint32_t take = __ballot_sync(0xffffffffu, m.x >= 0 && m.z - (m.z % p.K - c + p.K) % p.K >= m.y);
+      const int ahead = m.z % p.K - c, back = ahead < 0 ? ahead + p.K : ahead;  // of the slot's last position, to this entry's
+      const uint32_t take = __ballot_sync(0xffffffffu, m.x >= 0 && m.z - back >= m.y);
       if (!take) continue;
       const int64_t entry = (int64_t)h * p.K + c, slots = (int64_t)p.Hq * p.K;
       uint4 o[NB], q[NB];
