@@ -483,7 +483,7 @@ int attend_rows(const mac_config *cfg, void *chunk_ws, const void *q, const int3
   const bool f32 = cfg->dtype == MAC_F32;
   const int grid = sms < kChunkGrid ? sms : kChunkGrid;
   const int64_t in_block = (int64_t)kFewRows / p.G * p.B, blocks = (n_tokens + in_block - 1) / in_block * p.B * p.Hkv;  // rows shared evenly
-  const bool few = cross && (n_tokens <= in_block || (blocks <= grid && blocks * p.max_len <= kFewKeys));
+  const bool few = cross && (n_tokens <= in_block || (blocks <= grid && blocks * p.max_len <= (f32 ? FewF32::kMostKeys : FewBf16::kMostKeys)));
   // (the kernel's last piece joins a unit's pieces, if there are units enough for each to have few)
   if (few && (int64_t)p.B * p.Hkv * kFewPieces >= grid) p.counts = (uint32_t *)(ws + L.counts);
   if ((few     ? launch_cross_few(p, f32, grid, s)
