@@ -332,7 +332,8 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
  * anything.  The numerics are mac_chunk_attention's; where there are at most
  * 16 rows of a KV head per source (n_tokens Hq / Hkv <= 16 B), or few more
  * and the memory is short, in bf16 the probabilities are not rounded to bf16,
- * and in fp32 each product is good to 2^-20 of its size (2^-24 on average)
+ * and in fp32 each product is good to 2^-20 of its size (2^-24 on average),
+ * sums over the memory round to nearest, tile by tile, however long it is,
  * and elements beyond 3.39e38 count as infinite. */
 int mac_cross_attention(const mac_config *cfg, void *chunk_ws, const void *q, const int32_t *q_start,
                         int32_t group, const int32_t *mem_len, int32_t n_tokens, const mac_kv *kv,

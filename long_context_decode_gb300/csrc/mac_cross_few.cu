@@ -27,10 +27,15 @@
 // fp32: a = a0 + a1 of 11 bits each (rounded, so a1 is good to 2^-22 of a), and
 //   a b = a0 b0 + a0 b1 + a1 b0 + (a1 b1, up to 2^-22 of a b, left out):
 // three products in tf32, each exact in the sums, so a product is off by at most
-// 2^-20 of its size (2^-24 on average).
+// 2^-20 of its size (2^-24 on average).  The tensor cores cut their sums off, by up
+// to 2^-23 each time and always towards zero: a tile's products are summed there
+// (2^-22 in all) and added to o with rounding to nearest.  With o among the tensor
+// cores' sums, outputs over values of one sign came out 2^-14.5 too small after 32768
+// keys of a CTA, 2^-12.5 after 131072; now 2^-24, which costs 4 to 9% (4 x 32768 keys
+// 195 and 211 us; with single adds, not pairs, 216).
 //
 // In a graph (us; floor: bytes at 6.7 TB/s): 16 rows of each of 4 sources of 32768
-// keys, 32 / 8 heads, 84.5 (80.1; 6.4 TB/s), in fp32 196 (160); 64 rows over 16
+// keys, 32 / 8 heads, 84.5 (80.1; 6.4 TB/s), in fp32 211 (160); 64 rows over 16
 // sources of 1024 keys 10.8 from L2, 15.2 from HBM (10.2); of 400 to 1500 keys, cut,
 // 14.6 and 18.3 (9.6); one row over 57 keys 4.4.  What is left over the floor is the
 // start (3.5 us until the first keys are there), some 2.5 us of every further piece of
@@ -110,6 +115,12 @@ __device__ __forceinline__ void mma_tf32(float *c, const float *a, float b0, flo
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
                  "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+__device__ __forceinline__ void mma_tf32_first(float *c, const float *a, float b0, float b1) {  // c = a b
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
+                 "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(0.f));
 }
 __device__ __forceinline__ float tf32(float x) {
   uint32_t u;
@@ -589,12 +600,20 @@ __global__ void __launch_bounds__(kThr, 1) few_kernel(const __grid_constant__ Ch
             split(a[e], ah[e], al[e]);
             split(b[e], bh[e], bl[e]);
           }
+          float y[4][4];  // of this tile alone: see above
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma_tf32(o[c * 4 + e], pl, ah[e], bh[e]);
+          for (int e = 0; e < 4; ++e) mma_tf32_first(y[e], pl, ah[e], bh[e]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma_tf32(o[c * 4 + e], ph, al[e], bl[e]);
+          for (int e = 0; e < 4; ++e) mma_tf32(y[e], ph, al[e], bl[e]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma_tf32(o[c * 4 + e], ph, ah[e], bh[e]);
+          for (int e = 0; e < 4; ++e) mma_tf32(y[e], ph, ah[e], bh[e]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float *to = &o[c * 4 + (e >> 2)][e & 3];
+            const float2 sum = add2(make_float2(to[0], to[1]), make_float2(y[e >> 2][e & 3], y[e >> 2][(e & 3) + 1]));
+            to[0] = sum.x;
+            to[1] = sum.y;
+          }
         }
       } else {
         // the weights in two bf16 parts: the tensor cores have the time, and the output
