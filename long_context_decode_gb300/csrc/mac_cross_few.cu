@@ -156,6 +156,7 @@ struct Source {
   int row0, n, keys;   // first row, rows (0: nothing to attend), states
   int blocks, tiles;   // units of a KV head; key tiles
   bool odd;            // rows that are not attended: bad lengths, or no states
+  bool back;           // q_start goes back here
 };
 
 // The pieces of a CTA, worked out by every warp for itself (all lanes call it).
@@ -165,8 +166,8 @@ struct Walk {
   int lg, lt;          // log2 of the heads of a KV head, and of the tokens of a unit
   int b, k;            // source, unit (KV head by head, in each its rows' blocks)
   Source src;
-  bool whole, odd;     // a unit per CTA; some source is odd
-  long long x, end, share, at;  // this CTA's span; the unit's place
+  bool whole, odd;     // no unit is cut; some source is odd
+  long long x, end, share, at;  // this CTA's span (whole: units); the unit's place
 
   __device__ __forceinline__ Source source(const ChunkParams &p, int i) const {
     Source s;
@@ -175,6 +176,7 @@ struct Walk {
     s.row0 = r0;
     s.keys = m;
     s.odd = !in || (r1 > r0 && (m < 1 || m > p.max_len));
+    s.back = r1 < r0;
     s.n = s.odd ? 0 : r1 - r0;
     s.blocks = (s.n + (1 << lt) - 1) >> lt;
     s.tiles = (int)(((long long)m + C::kKeys - 1) / C::kKeys);
@@ -190,11 +192,13 @@ struct Walk {
     long long total = 0;
     int units = 0, top = 0;  // 2^24 and 2^28 at most
     odd = false;
+    bool back = false;
     Source mine;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       mine = {};
       if (b0 + lane < p.B) mine = source(p, b0 + lane);
       odd |= mine.odd;
+      back |= mine.back;
       if (mine.blocks) {
         total += (long long)mine.blocks * p.Hkv * cost(mine);
         units += mine.blocks * p.Hkv;
@@ -208,6 +212,12 @@ struct Walk {
     const long long ctas = max(1, (int)min(total / C::kMinShare, (long long)gridDim.x));
     whole = units <= (int)gridDim.x && (top - C::kCut - 1) * ctas < total;
     share = whole ? 1 : div_down(total + ctas - 1, ctas);
+    // Rows that several sources claim, as a q_start that goes back has them, may be more
+    // units than the host counted when it left the merge kernel out: then none is cut.
+    if (odd && __any_sync(0xffffffffu, back)) {
+      whole = true;
+      share = div_down(units + gridDim.x - 1, gridDim.x);
+    }
     x = blockIdx.x * share;
     end = min(whole ? units : total, x + share);
     if (x >= end) return false;
