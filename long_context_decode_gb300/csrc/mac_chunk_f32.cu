@@ -31,7 +31,7 @@
 // 4096 tokens, 8 heads of 2 KV heads: 178 to 183 us, 188 to 193 TFLOP/s of fp32
 // products (multiply-adds on the CUDA cores: 945 us).  A tile takes 7200 cycles
 // whatever its rows, so single tokens are bound by splitting and products, not
-// by HBM: four of 32 / 8 heads at 8192 take 95 us (2.8 TB/s).  Of a tile, its 72
+// by HBM: four of 32 / 8 heads at 8192 take 89 us (3.0 TB/s).  Of a tile, its 72
 // products 4100 (S 48 of 55, reading Q from shared memory, P V 24 of 60), the
 // rest waits for K and V to be split, which is 45 instructions per row and
 // warp.  Error against 64 bits 3.2e-7 where fp32 matrix products have 5.6e-7.
@@ -189,9 +189,19 @@ __device__ __forceinline__ float4 load_if(const float *src, bool ok) {
   return f;
 }
 
-template <bool PAGED, bool CROSS>
+// FEW: for batches of few rows per request.  A piece's first keys (values) are then asked
+// for ahead of its queries, and those two rows at a time; else all of a warp's queries
+// first, whose rows would take 5 us of a piece of 128 at two at a time, then the first keys.
+// FEW and not, us, 32 / 8 heads: 4 requests of a token at 8192 89.2 and 91.6, 16 at 2000
+// 94.8 and 97.3, 64 at 500 103.7 and 105.9, of 2 tokens at 100 45.0 and 47.9, of 4 46.2 and 47.7,
+// of 8 49.2 and 48.6; 16 of 4 at 2000 95.3 and 96.6, of 16 101.2 and 98.4; 63 of one and one of 150
+// 70.7 and 56.4, so the bound lies where a batch can hardly be that uneven.  Each is a kernel of
+// its own: with a branch for it in one, every tile takes 1 to 2% more, whichever way it goes.
+constexpr int kFewQ = 8;  // rows of a request and KV head, on average
+
+template <bool PAGED, bool CROSS, bool FEW>
 __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, uint8_t *vbuf, Control *ct) {
-  const int lane = threadIdx.x & 31, me_q = (threadIdx.x >> 5) - 4, me = me_q & (kConv - 1), lg = 31 - __clz(p.G);
+  const int lane = threadIdx.x & 31, me_q = (threadIdx.x >> 5) - 4, me = me_q & (kConv - 1);
   static_assert(kRows == 2 * kConv * kPage, "a warp's rows of Q are as many as of a tile");
   const bool is_k = me_q < kConv;  // one copy of the code for both: see above
   const float *src = (const float *)(is_k ? p.kv.k : p.kv.v) + lane * 4;
@@ -222,25 +232,39 @@ __device__ void split_role(const ChunkParams &p, uint8_t *qbuf, uint8_t *kbuf, u
 #pragma unroll
       for (int i = 0; i < kPage; ++i) f[i] = load_if(row + i * kHeadDim, i < n);
     };
-    // Q first, all of a warp's rows on their way at once (two at a time took 5 us of
-    // a piece of 128 rows), then the first keys (values)
-#pragma unroll
-    for (int i = 0; i < kPage; ++i) {
-      const int r = me_q + i * 2 * kConv;
-      f[i] = load_if((const float *)p.q + ((int64_t)(q.tok0 + (r >> lg)) * p.Hq + (q.g << lg) + (r & (p.G - 1))) * kHeadDim + lane * 4, r < n_rows);
-    }
-    if (wait(&ct->q_free, (nq + 1) & 1)) {
-      ++nq;
-#pragma unroll 1
-      for (int c = 0; c < kPage; c += kPage / 2) {
-#pragma unroll
-        for (int i = 0; i < kPage / 2; ++i) put_parts<kRows>(qbuf, me_q + (c + i) * 2 * kConv, lane, f[i]);
-#pragma unroll
-        for (int i = 0; i < kPage / 2; ++i) f[i] = f[i + kPage / 2];
+    if constexpr (FEW) {
+      load(q.t0, at(q.t0));
+      if (wait(&ct->q_free, (nq + 1) & 1)) {
+        ++nq;
+#pragma unroll 2
+        for (int r = me_q; r < kRows; r += 2 * kConv) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < n_rows)
+            x = *reinterpret_cast<const float4 *>((const float *)p.q + ((int64_t)(q.tok0 + r / p.G) * p.Hq + q.g * p.G + r % p.G) * kHeadDim + lane * 4);
+          put_parts<kRows>(qbuf, r, lane, x);
+        }
+        hand_over(&ct->q_full);
       }
-      hand_over(&ct->q_full);
+    } else {
+      const int lg = 31 - __clz(p.G);
+#pragma unroll
+      for (int i = 0; i < kPage; ++i) {
+        const int r = me_q + i * 2 * kConv;
+        f[i] = load_if((const float *)p.q + ((int64_t)(q.tok0 + (r >> lg)) * p.Hq + (q.g << lg) + (r & (p.G - 1))) * kHeadDim + lane * 4, r < n_rows);
+      }
+      if (wait(&ct->q_free, (nq + 1) & 1)) {
+        ++nq;
+#pragma unroll 1
+        for (int c = 0; c < kPage; c += kPage / 2) {
+#pragma unroll
+          for (int i = 0; i < kPage / 2; ++i) put_parts<kRows>(qbuf, me_q + (c + i) * 2 * kConv, lane, f[i]);
+#pragma unroll
+          for (int i = 0; i < kPage / 2; ++i) f[i] = f[i + kPage / 2];
+        }
+        hand_over(&ct->q_full);
+      }
+      load(q.t0, at(q.t0));
     }
-    load(q.t0, at(q.t0));
     int64_t next = at(q.t0 + 1);  // a tile ahead of its use
     for (int t = q.t0; t < q.t1; ++t, ++nt) {
       if (wait(free, (nt + 1) & 1)) {
@@ -432,7 +456,7 @@ __device__ void row_role(const ChunkParams &p, Control *ct, uint32_t tmem) {
   if (status) set_status(p.status, status);
 }
 
-template <bool PAGED, typename C>
+template <bool PAGED, typename C, bool FEW>
 __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
   using Plan = ChunkPlan<C>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -490,7 +514,7 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
     row_role<PAGED, C::kCross>(p, ct, tmem);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSplit));
-    split_role<PAGED, C::kCross>(p, qbuf, kbuf, vbuf, ct);
+    split_role<PAGED, C::kCross, FEW>(p, qbuf, kbuf, vbuf, ct);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == 12) mma_role(p, smem_addr(qbuf), smem_addr(kbuf), smem_addr(vbuf), ct, tmem);
@@ -501,22 +525,24 @@ __global__ void __launch_bounds__(kThr, 1) chunk_kernel(const __grid_constant__ 
   if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <bool PAGED, typename C>
+template <bool PAGED, typename C, bool FEW>
 cudaError_t launch(const ChunkParams &p, int grid, cudaStream_t s) {
   // with fewer registers at launch the split between the roles would wait forever
   static DeviceFlags done;
-  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED, C>, done, kSmemBytes, kRegsLaunch);
+  const cudaError_t e = prepare_chunk(chunk_kernel<PAGED, C, FEW>, done, kSmemBytes, kRegsLaunch);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_kernel<PAGED, C>, grid, kThr, kSmemBytes, s, p);
+  return launch_dependent(chunk_kernel<PAGED, C, FEW>, grid, kThr, kSmemBytes, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_f32(const ChunkParams &p, int grid, cudaStream_t s) {
-  return p.kv.paged ? launch<true, ChunkF32>(p, grid, s) : launch<false, ChunkF32>(p, grid, s);
+  if ((int64_t)p.T * p.G <= (int64_t)kFewQ * p.B)
+    return p.kv.paged ? launch<true, ChunkF32, true>(p, grid, s) : launch<false, ChunkF32, true>(p, grid, s);
+  return p.kv.paged ? launch<true, ChunkF32, false>(p, grid, s) : launch<false, ChunkF32, false>(p, grid, s);
 }
-cudaError_t launch_cross_f32(const ChunkParams &p, int grid, cudaStream_t s) {
-  return p.kv.paged ? launch<true, CrossF32>(p, grid, s) : launch<false, CrossF32>(p, grid, s);
+cudaError_t launch_cross_f32(const ChunkParams &p, int grid, cudaStream_t s) {  // (few rows have a kernel of their own)
+  return p.kv.paged ? launch<true, CrossF32, false>(p, grid, s) : launch<false, CrossF32, false>(p, grid, s);
 }
 
 }  // namespace mac
