@@ -249,7 +249,9 @@ int mac_chunk_workspace_size(const mac_config *cfg, int32_t n_tokens, size_t *ch
  *     order of request and page they go on top of the stack.  The flags
  *     are not cleared (mac_reset_requests on the same flags, after this
  *     call, empties the request's rings and clears them).  Slots that share
- *     pages are given back by mac_reorder_tables, not so.
+ *     pages are given back by mac_reorder_tables, not so; beams that share
+ *     none may be, but this call does not reach what mac_reorder_tables
+ *     holds of their common positions (shared_in there).
  *   Pages: the k-th new page, in order of request and page, is the stack's
  *     k-th entry from the top.  Entries above the count stay as they are.
  *   A request is admitted whole or not at all: while the pages and the rows
@@ -393,7 +395,14 @@ int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const
  * slot; a child has its parent's.  shared_in, shared_out: int32
  * [batch][n_beams], for each slot of a group how many leading positions a
  * slot has in common with it; the caller keeps the array, zero-filled at
- * first, and only these calls write it.
+ * first.  These calls write it, and take its counts at their word: positions
+ * that two slots have in common are not moved.  So a slot begins anew with
+ * parent -1, which clears its counts (then its rings by mac_reset_requests,
+ * its new tokens by mac_build_tables).  Where it begins anew in another way,
+ * or goes back to a shorter history (reset_flags of slots without a common
+ * page, lengths written by the caller), the caller clears its row, and its
+ * column in the rows of its group, before the next call: what it had in
+ * common would be taken for the beginning of its new history.
  *   Pages (pages == NULL for a contiguous cache): children share their
  *     parent's pages.  A history whose last page is not full is parted: its
  *     slot keeps that page if it goes on as its own child, else the child of
@@ -404,7 +413,10 @@ int mac_beam_select(const mac_config *cfg, void *beam_ws, int32_t n_beams, const
  *     slot's pages stay as they are.  Pages are shared within a group only,
  *     and slots that share pages are given back here, with parent -1, not
  *     with mac_build_tables' reset_flags.
- *   A child whose free page is missing (MAC_DEV_NO_ROOM) is empty afterwards.
+ *   A child whose free page is missing (MAC_DEV_NO_ROOM) is empty afterwards
+ *     (len_out 0, parent >= 0) and has nothing in common with any slot: its
+ *     rings are to be reset as after parent -1, and the caller sets its score
+ *     to -inf, or the next selection counts it as a beam.
  *     A parent outside [-1, n_beams) (MAC_DEV_BAD_PARENT) is taken for the
  *     slot itself.  A group with a length outside [0, limit]
  *     (MAC_DEV_BAD_SEQ_LEN) is passed over.  A held page id outside

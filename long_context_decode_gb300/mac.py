@@ -339,7 +339,10 @@ def mac_beam_select(cfg, beam_ws, n_beams, logits, scores, done, end_token, n_ou
 def mac_reorder_tables(cfg, chunk_ws, pages: mac_pages | None, n_beams, parent, len_in, len_out, shared_in, shared_out, moves,
                        stream=None):
     """Slots take over their parents' pages, lengths and common positions; moves
-    ([slots, 8] int32) says what mac_reorder_state has to move."""
+    ([slots, 8] int32) says what mac_reorder_state has to move.  A slot begins
+    anew with parent -1; one that does so in another way (reset flags, where it
+    shares no page) gets its row and its column of the common positions cleared
+    by the caller first."""
     S = cfg.batch
     pairs = S * n_beams
     _check(load().mac_reorder_tables(ctypes.byref(cfg), _ptr(chunk_ws), ctypes.byref(pages) if pages is not None else None, n_beams,
