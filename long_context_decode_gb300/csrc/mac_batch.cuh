@@ -96,8 +96,8 @@ struct CrossF32 : ChunkF32 {
 // The same for few rows per source (mac_cross_few.cu), in quarters of a tile's
 // 64 KB of keys and values, 1.4 us at an SM's share of HBM.
 // Against the kernels above (us): one row over 57 keys 4.4 and 7.8; 16 rows of 16
-// sources of 400 to 1500 keys 14.4 and 18.3; in fp32 16 rows over 4 x 32768 196 and
-// 308.  With two row tiles of 16 it was no faster than they are: 20 rows of 4 sources
+// sources of 400 to 1500 keys 14.4 and 18.3; in fp32 16 rows over 4 x 32768 210 and
+// 306.  With two row tiles of 16 it was no faster than they are: 20 rows of 4 sources
 // of 8192 to 32768 keys 56.8 and 53.4, 32 in fp32 over 4 x 32768 357 and 308.
 constexpr int kFewRows = 16;          // most rows of a source, on average
 // Pieces of a unit, on average, that the last of them joins by itself (more: the merge kernel).
@@ -111,21 +111,22 @@ struct CrossFew {
 };
 // A start and end in bf16 as 7 quarters of a tile: 16 rows of 2 sources of 3000 keys
 // 10.3 us, as 5 11.1; in fp32, whose tiles take longer, as 5: 10 sources of 100 to 5000
-// 48.4, as 6 49.3, as 4 48.2.
+// 48.5, as 6 50.0, as 4 48.4.
 // kMostKeys: more rows take blocks of 16 of them, each of which reads the keys again; the
 // tcgen05 kernels start later and take 128 at once.  So this is for memories (caches, as
 // far as the host knows) of that many keys in all blocks, if there is an SM for each block.
 // us here and there, 32 / 8 heads: 5 rows of one source of 128 keys (16 blocks) 5.4 and
 // 8.1, of 8192 14.4 and 17.5, 9 rows of it (3 2^16 keys) 16.4 and 17.8, 16 rows (2^18)
 // 18.9 and 17.6; 12 rows of 4 sources of 2048 (3 2^16) 16.6 and 17.3; 5 of 4096 (2^18)
-// 19.1 and 18.7.  In fp32 8.1 and 15.0, 32.3 and 33.4 (2^17), 44.0 and 34.1, 55.5 and 34.5;
-// 12 rows of 4 sources of 1024 (3 2^15) 26.5 and 25.1, 16 rows (2^17) 32.4 and 25.7.  More
+// 19.1 and 18.7.  In fp32 5 rows of one source of 128 keys 8.1 and 14.4, of 4096 (2^16)
+// 21.1 and 24.7, of 8192 34.2 and 32.7; 16 rows of one of 2048 (2^16) 20.7 and 24.6, of 3000
+// 27.7 and 25.1; 12 rows of 4 sources of 700 (2^16) 22.1 and 24.3, of 1024 (3 2^15) 27.7 and 24.5.  More
 // blocks than SMs: 5 rows of 16 sources of 128 keys (256) 8.4 and 9.5, of 512 16.0 and 12.3.
 struct FewBf16 : CrossFew<128, 7> {
   static constexpr int64_t kMostKeys = 3 << 16;
 };
 struct FewF32 : CrossFew<64, 5> {
-  static constexpr int64_t kMostKeys = 3 << 15;
+  static constexpr int64_t kMostKeys = 5 << 14;
 };
 constexpr int kChunkStride = kHeadDim + 8;  // floats per row of a partial: o[d], m, l, and to a multiple of 32 bytes
 

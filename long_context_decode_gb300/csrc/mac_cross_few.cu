@@ -32,10 +32,10 @@
 // (2^-22 in all) and added to o with rounding to nearest.  With o among the tensor
 // cores' sums, outputs over values of one sign came out 2^-14.5 too small after 32768
 // keys of a CTA, 2^-12.5 after 131072; now 2^-24, which costs 4 to 9% (4 x 32768 keys
-// 195 and 211 us; with single adds, not pairs, 216).
+// 195 and 210 us; with single adds, not pairs, 216).
 //
 // In a graph (us; floor: bytes at 6.7 TB/s): 16 rows of each of 4 sources of 32768
-// keys, 32 / 8 heads, 84.5 (80.1; 6.4 TB/s), in fp32 211 (160); 64 rows over 16
+// keys, 32 / 8 heads, 84.5 (80.1; 6.4 TB/s), in fp32 210 (160); 64 rows over 16
 // sources of 1024 keys 10.8 from L2, 15.2 from HBM (10.2); of 400 to 1500 keys, cut,
 // 14.6 and 18.3 (9.6); one row over 57 keys 4.4.  What is left over the floor is the
 // start (3.5 us until the first keys are there), some 2.5 us of every further piece of
