@@ -331,7 +331,12 @@ int mac_chunk_attention(const mac_config *cfg, void *chunk_ws, const void *q,
  * this cfg; the query is taken as it is.  A source without states (mem_len
  * 0) gives its rows out 0 and lse -inf.  Bad lengths, pages and rows are
  * reported and left out as there.  Cache rows beyond mem_len may hold
- * anything.  The numerics are mac_chunk_attention's; where there are at most
+ * anything; an infinity that is attended makes its outputs infinite or NaN.
+ * cfg->max_context bounds mem_len, as the cache's room does, and with the
+ * number of rows it says which kernels run: a caller that knows its memories
+ * to be shorter than the cache gives that bound (one row of 8 / 2 heads over
+ * 57 keys 4.4 us, 5.9 where 32768 would fit; five rows of 32 / 8 heads over
+ * 128 5.0 and 9.4).  The numerics are mac_chunk_attention's; where there are at most
  * 16 rows of a KV head per source (n_tokens Hq / Hkv <= 16 B), or few more
  * and the memory is short, in bf16 the probabilities are not rounded to bf16,
  * and in fp32 each product is good to 2^-20 of its size (2^-24 on average),

@@ -363,7 +363,8 @@ cudaError_t launch(const ReorderParams &p, cudaStream_t s) {
 // does not share with its parent are moved.
 // A step (32 slots, 12 positions apart at most, 32 / 8 bf16 heads, paged): 3.5 us,
 // its launch and three trips to memory.  Beams opened on two prompts (8 slots of
-// 8 / 2 fp32 heads, 119 MB read and written): 14.8 us from L2, 19.8 from HBM.  With
+// 8 / 2 fp32 heads, 59 MB written, 20 MB of parents' state read, by three children
+// each): 14.8 us from L2, 19.6 from HBM, 1.7 times the bytes' time there.  With
 // four CTAs per SM, and so 64 registers, they took 5.9 and 22.6 of 3.8 and 15.6, with
 // three 4.4 and 15.6.  Groups of two slots have less on its way per thread, and room
 // for four CTAs: 16 of 418 positions at most, 128 in the ring, copied whole (110 MB)
