@@ -369,9 +369,10 @@ int mac_beam_workspace_size(const mac_config *cfg, int32_t n_beams, int32_t voca
  * slot, row_stride >= vocab elements apart, on any element boundary.  scores:
  * f32 [batch], the beams' sums of log probabilities; -inf: the beam has no
  * candidates (all but one slot of a group before its first token), and its
- * logits may be anything (a very low number in its place makes it a live beam
- * whose score fp32 tells apart too coarsely: 5 beams of 128000 logits then take
- * 130 us of 13, as their sums are made again).  A candidate is (beam j, token v) with score s =
+ * logits may be anything (a very low number in its place makes it a live beam,
+ * and the choice, whose first threshold in fp32 allows for the largest score,
+ * ranks many more candidates: of 5 beams of 128000 logits, -1e9 for four of
+ * them, the 10 best take 130 us, not 13).  A candidate is (beam j, token v) with score s =
  * scores[j] + x_jv - ln sum_v exp x_jv; logits of -inf are no candidates.
  * The order is that of the exact scores (by s, rounded no coarser than 2^-36
  * or, where that is more, 2^-51 |s|), ties to the lowest (j, v), whatever the
